@@ -12,6 +12,14 @@ C ABI declared in include/fp8gemm.h.  torch supplies device memory and the curre
     A, sa = quantize_1x128_masked(X, masked_m)             # the same, masked layout
     H, sh = swiglu_quantize_1x128(Y)                       # silu(gate) * up -> codes + scales
     out = moe_expert_masked(A, sa, W1, s1, W2, s2, masked_m, expected_m)  # one MoE expert layer
+    ids, w = route_topk(logits, k, bias, score="sigmoid", ...)   # the router's experts and weights
+    dlogits = route_topk_backward(logits, ids, dw, ...)          # and their gradient
+    A, sa, masked_m, rows = moe_dispatch_masked(X, ids, G, M_max)      # tokens -> masked rows, quantised
+    A, sa, m_indices, rows = moe_dispatch_contiguous(X, ids, G)        # the same, contiguous layout
+    out = moe_combine(Y, w, rows)                                # expert rows -> tokens, weighted
+    dY, dw = moe_combine_backward(dout, Y, w, rows)              # and its gradients
+    Y = w4_gemv(X, W4, scales, zeros)                            # few rows times 4-bit weights
+    Y = w4_gemv_experts(X, W4, scales, ids, zeros, swiglu=True)  # the same, by the router's ids
 
 A and B are E4M3 codes (torch.float8_e4m3fn or uint8), sa one fp32 scale per 1x128 block of a
 row of A stored K-block-major (sa[kb, m], shape [K/128, M]), sb one per 128x128 block of B (page "DeepSeek開源第三彈：V3/R1訓練推理關鍵秘籍，核心代碼僅
@@ -26,7 +34,8 @@ import os
 __all__ = ["gemm_nt", "gemm_nt_noalloc", "gemm_nt_specialized", "specialize_nt", "specialized_code_object", "specialized_count",
            "grouped_contiguous", "grouped_masked", "quantize_1x128",
            "quantize_1x128_masked", "fp8fp4_grouped_masked", "swiglu_quantize_1x128", "swiglu_quantize_1x128_masked",
-           "moe_expert_masked", "init", "prepare_stream", "set_num_cus",
+           "moe_expert_masked", "route_topk", "route_topk_backward", "moe_dispatch_masked",
+           "moe_dispatch_contiguous", "moe_combine", "moe_combine_backward", "w4_gemv", "w4_gemv_experts", "init", "prepare_stream", "set_num_cus",
            "last_config", "read_device_error", "status_string", "lib", "library_path",
            "Fp8GemmError", "STATUS", "DEVERR_BAD_INDEX", "DEVERR_BAD_COUNT"]
 
@@ -41,7 +50,7 @@ DEVERR_BAD_INDEX = 1
 DEVERR_BAD_COUNT = 2
 
 #: exported C symbols and their ctypes signatures (restype, argtypes)
-_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_P, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 SIGNATURES = {
     "fp8gemm_nt": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "fp8gemm_nt_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
@@ -60,6 +69,14 @@ SIGNATURES = {
     "fp8gemm_swiglu_quantize_1x128_masked": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I64, _I64, _P]),
     "fp8gemm_moe_expert_masked": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                  _I32, _I64, _I64, _I64, _I64, _P]),
+    "fp8gemm_route_topk": (ctypes.c_int, [_P, _P, _P, _P, _I64] + [_I32] * 8 + [_F32, _P]),
+    "fp8gemm_route_topk_backward": (ctypes.c_int, [_P, _P, _P, _P, _I64] + [_I32] * 5 + [_F32, _P]),
+    "fp8gemm_moe_dispatch_masked": (ctypes.c_int, [_P] * 6 + [_I64, _I64, _I32, _I32, _I64, _I32, _P]),
+    "fp8gemm_moe_dispatch_contiguous": (ctypes.c_int, [_P] * 6 + [_I64, _I64, _I32, _I32, _I64, _I32, _P]),
+    "fp8gemm_moe_combine": (ctypes.c_int, [_P] * 4 + [_I64, _I64, _I32, _I64, _P]),
+    "fp8gemm_moe_combine_backward": (ctypes.c_int, [_P] * 6 + [_I64, _I64, _I32, _I64, _P]),
+    "fp8gemm_w4_gemv": (ctypes.c_int, [_P] * 5 + [_I64, _I64, _I64, _I32, _I32, _P]),
+    "fp8gemm_w4_gemv_experts": (ctypes.c_int, [_P] * 6 + [_I64, _I32, _I32, _I64, _I64] + [_I32] * 5 + [_P]),
     "fp8gemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8gemm_init": (ctypes.c_int, []),
     "fp8gemm_prepare_stream": (ctypes.c_int, [_P]),
@@ -465,3 +482,283 @@ def moe_expert_masked(A, sa, W1, s1, W2, s2, masked_m, expected_m: int, out=None
                                              G, M_max, H, I, int(expected_m), _stream(stream, A.device))
     _check(st, "fp8gemm_moe_expert_masked")
     return D
+
+
+# ---- expert routing, token permutation, 4-bit matrix-vector products ---------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _call(fn, device, stream, *args):
+    """One C call on torch's current stream of `device` (or `stream`)."""
+    torch = _torch()
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    f = getattr(_lib or lib(), fn)
+    if device == torch._C._cuda_getDevice():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st != 0:
+        raise Fp8GemmError(st, fn)
+
+
+def _take(t, dtype, shape, device, name):
+    """Address of a contiguous device tensor of this type and shape."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != device:
+        raise ValueError("%s must be a tensor of device %d" % (name, device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _device_of(t, dims, name):
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions" % (name, dims))
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("%s must be a device tensor" % name)
+    return d
+
+
+def _logits(logits, device):
+    torch = _torch()
+    if logits.dtype is torch.float32:
+        return _take(logits, torch.float32, logits.shape, device, "logits"), 0
+    return _take(logits, torch.bfloat16, logits.shape, device, "logits"), 1
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError('score must be "softmax" or "sigmoid"')
+    return _SCORES[score]
+
+
+def route_topk(logits, k: int, bias=None, score="softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+               renorm: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The k experts of each token and their weights: logits fp32 or bf16 [T,E] -> (ids int32 [T,k],
+    weights fp32 [T,k]).  ``bias`` fp32 [E] enters the choice, not the weights; with ``n_group`` > 1
+    only the experts of the ``topk_group`` best groups (by the sum of their ``group_top`` largest
+    choice values) can be chosen; ``renorm`` divides a token's weights by their sum.  Ties go to the
+    lower index; where fewer than k experts can be chosen the rest are id -1, weight 0."""
+    torch = _torch()
+    dev = _device_of(logits, 2, "logits")
+    p, dtype = _logits(logits, dev)
+    T, E = logits.shape
+    pb = None if bias is None else _take(bias, torch.float32, (E,), dev, "bias")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _call("fp8gemm_route_topk", dev, stream, p, pb, _take(ids, torch.int32, (T, k), dev, "ids"),
+          _take(weights, torch.float32, (T, k), dev, "weights"), T, E, k, dtype, _score(score), n_group, topk_group,
+          group_top, int(renorm), scale)
+    return ids, weights
+
+
+def route_topk_backward(logits, ids, dweights, score="softmax", renorm: bool = True, scale: float = 1.0, dlogits=None,
+                        stream=None):
+    """Gradient of route_topk's weights: dweights fp32 [T,k] -> dlogits [T,E] of the logits' type."""
+    torch = _torch()
+    dev = _device_of(logits, 2, "logits")
+    p, dtype = _logits(logits, dev)
+    T, E = logits.shape
+    _device_of(ids, 2, "ids")
+    k = ids.shape[1]
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _call("fp8gemm_route_topk_backward", dev, stream, p, _take(ids, torch.int32, (T, k), dev, "ids"),
+          _take(dweights, torch.float32, (T, k), dev, "dweights"), _take(dlogits, logits.dtype, (T, E), dev, "dlogits"),
+          T, E, k, dtype, _score(score), int(renorm), scale)
+    return dlogits
+
+
+def _code_ptr(t, shape, device, name):
+    torch = _torch()
+    return _take(t, torch.uint8 if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape, device, name)
+
+
+def moe_dispatch_masked(X, ids, G: int, M_max: int, first_expert: int = 0, codes=None, scales=None, masked_m=None,
+                        row_map=None, stream=None):
+    """Token rows into the masked layout, quantised: X bf16 [T,H], ids int32 [T,k] -> (codes
+    [G,M_max,H], scales fp32 [G,H/128,M_max], masked_m int32 [G], row_map int32 [T,k]).  A pair goes
+    to expert ids - first_expert if that is one of the G; its row is g * M_max + rank, or -1 (another
+    rank's expert, or past M_max).  Rows that no pair goes to are left untouched (zeros when the
+    outputs are allocated here)."""
+    torch = _torch()
+    dev = _device_of(X, 2, "X")
+    T, H = X.shape
+    _device_of(ids, 2, "ids")
+    k = ids.shape[1]
+    if codes is None:
+        codes = torch.zeros((G, M_max, H), dtype=torch.uint8, device=X.device).view(torch.float8_e4m3fn)
+    if scales is None:
+        scales = torch.zeros((G, H // 128, M_max), dtype=torch.float32, device=X.device)
+    if masked_m is None:
+        masked_m = torch.empty((G,), dtype=torch.int32, device=X.device)
+    if row_map is None:
+        row_map = torch.empty((T, k), dtype=torch.int32, device=X.device)
+    _call("fp8gemm_moe_dispatch_masked", dev, stream, _take(X, torch.bfloat16, (T, H), dev, "X"),
+          _take(ids, torch.int32, (T, k), dev, "ids"), _code_ptr(codes, (G, M_max, H), dev, "codes"),
+          _take(scales, torch.float32, (G, H // 128, M_max), dev, "scales"),
+          _take(masked_m, torch.int32, (G,), dev, "masked_m"), _take(row_map, torch.int32, (T, k), dev, "row_map"),
+          T, H, k, G, M_max, first_expert)
+    return codes, scales, masked_m, row_map
+
+
+def moe_dispatch_contiguous(X, ids, G: int, M_total: int = None, first_expert: int = 0, codes=None, scales=None,
+                            m_indices=None, row_map=None, stream=None):
+    """Token rows into the contiguous layout, quantised: X bf16 [T,H], ids int32 [T,k] -> (codes
+    [M_total,H], scales fp32 [H/128,M_total], m_indices int32 [M_total], row_map int32 [T,k]).  Each
+    expert's rows are padded to a multiple of 128.  M_total None: the rows of ``codes`` or
+    ``m_indices`` if given, else room for every pair."""
+    torch = _torch()
+    dev = _device_of(X, 2, "X")
+    T, H = X.shape
+    _device_of(ids, 2, "ids")
+    k = ids.shape[1]
+    if M_total is None:
+        if codes is not None:
+            M_total = codes.shape[0]
+        elif m_indices is not None:
+            M_total = m_indices.shape[0]
+        else:
+            M_total = -(-(T * k + 127 * min(G, T * k)) // 128) * 128
+    if codes is None:
+        codes = torch.zeros((M_total, H), dtype=torch.uint8, device=X.device).view(torch.float8_e4m3fn)
+    if scales is None:
+        scales = torch.zeros((H // 128, M_total), dtype=torch.float32, device=X.device)
+    if m_indices is None:
+        m_indices = torch.empty((M_total,), dtype=torch.int32, device=X.device)
+    if row_map is None:
+        row_map = torch.empty((T, k), dtype=torch.int32, device=X.device)
+    _call("fp8gemm_moe_dispatch_contiguous", dev, stream, _take(X, torch.bfloat16, (T, H), dev, "X"),
+          _take(ids, torch.int32, (T, k), dev, "ids"), _code_ptr(codes, (M_total, H), dev, "codes"),
+          _take(scales, torch.float32, (H // 128, M_total), dev, "scales"),
+          _take(m_indices, torch.int32, (M_total,), dev, "m_indices"),
+          _take(row_map, torch.int32, (T, k), dev, "row_map"), T, H, k, G, M_total, first_expert)
+    return codes, scales, m_indices, row_map
+
+
+def _combine_shapes(Y, weights, row_map, T):
+    """(k, rows of Y) of a combine; Y [R,H] or [G,M_max,H]."""
+    pairs = weights if weights is not None else row_map
+    if pairs is None:
+        raise ValueError("weights or row_map must be given")
+    if pairs.dim() != 2:
+        raise ValueError("weights and row_map must be [T,k]")
+    if T is not None and pairs.shape[0] != T:
+        raise ValueError("weights and row_map must have a row per token")
+    R = None
+    if Y is not None:
+        if Y.dim() not in (2, 3):
+            raise ValueError("Y must be [R,H] or [G,M_max,H]")
+        R = Y.shape[0] if Y.dim() == 2 else Y.shape[0] * Y.shape[1]
+    return pairs.shape[0], pairs.shape[1], R
+
+
+def moe_combine(Y, weights=None, row_map=None, out=None, stream=None):
+    """out[t] = sum_j weights[t,j] * Y[row_map[t,j]]: Y bf16 [R,H] (or [G,M_max,H]), weights fp32
+    [T,k] (None: ones), row_map int32 [T,k] with -1 left out (None: row t * k + j) -> bf16 [T,H]."""
+    torch = _torch()
+    T, k, R = _combine_shapes(Y, weights, row_map, None)
+    dev, H = Y.get_device(), Y.shape[-1]
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=Y.device)
+    _call("fp8gemm_moe_combine", dev, stream, _take(Y, torch.bfloat16, Y.shape, dev, "Y"),
+          None if weights is None else _take(weights, torch.float32, (T, k), dev, "weights"),
+          None if row_map is None else _take(row_map, torch.int32, (T, k), dev, "row_map"),
+          _take(out, torch.bfloat16, (T, H), dev, "out"), T, H, k, R)
+    return out
+
+
+def moe_combine_backward(dout, Y, weights=None, row_map=None, dY=None, dweights=None, stream=None):
+    """Gradients of moe_combine: dout bf16 [T,H], Y bf16 [R,H] (or [G,M_max,H]) -> (dY of Y's shape,
+    dweights fp32 [T,k]).  Rows of dY that no pair names are left untouched (zeros when allocated
+    here)."""
+    torch = _torch()
+    dev = _device_of(dout, 2, "dout")
+    T, H = dout.shape
+    T, k, R = _combine_shapes(Y, weights, row_map, T)
+    if Y.shape[-1] != H:
+        raise ValueError("Y must have dout's columns")
+    if dY is None:
+        dY = torch.zeros_like(Y)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    _call("fp8gemm_moe_combine_backward", dev, stream, _take(dout, torch.bfloat16, (T, H), dev, "dout"),
+          _take(Y, torch.bfloat16, Y.shape, dev, "Y"),
+          None if weights is None else _take(weights, torch.float32, (T, k), dev, "weights"),
+          None if row_map is None else _take(row_map, torch.int32, (T, k), dev, "row_map"),
+          _take(dY, torch.bfloat16, Y.shape, dev, "dY"), _take(dweights, torch.float32, (T, k), dev, "dweights"),
+          T, H, k, R)
+    return dY, dweights
+
+
+def _w4_format(W, scales, zeros, lead, N, K, device):
+    """(addresses of W, scales, zeros, format, group): E8M0 scales (uint8) are MXFP4, bf16 ones INT4."""
+    torch = _torch()
+    if scales.dim() != len(lead) + 2 or scales.shape[-1] == 0 or K % scales.shape[-1] != 0:
+        raise ValueError("scales must have one value per group of K")
+    groups = scales.shape[-1]
+    shape = (*lead, N, groups)
+    pw = _take(W, torch.uint8, W.shape, device, "W")
+    if scales.dtype is torch.uint8:
+        if zeros is not None:
+            raise ValueError("MXFP4 weights have no zeros")
+        return pw, _take(scales, torch.uint8, shape, device, "scales"), None, 0, K // groups
+    ps = _take(scales, torch.bfloat16, shape, device, "scales")
+    return pw, ps, None if zeros is None else _take(zeros, torch.uint8, shape, device, "zeros"), 1, K // groups
+
+
+def w4_gemv(X, W, scales, zeros=None, out=None, stream=None):
+    """Y = X . V^T for few rows: X bf16 [M,K], W uint8 [N,K/2] (two codes a byte, the even element in
+    the low nibble) -> bf16 [M,N].  ``scales`` uint8 [N,K/32]: MXFP4 (E2M1 codes, E8M0 scales);
+    bf16 [N,K/group], group 32, 64 or 128: INT4, V = (code - zero) * scale with ``zeros`` uint8
+    [N,K/group] (None: 8)."""
+    torch = _torch()
+    dev = _device_of(X, 2, "X")
+    M, K = X.shape
+    if W.dim() != 2 or 2 * W.shape[1] != K:
+        raise ValueError("W must be [N,K/2]")
+    N = W.shape[0]
+    pw, ps, pz, fmt, group = _w4_format(W, scales, zeros, (), N, K, dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+    _call("fp8gemm_w4_gemv", dev, stream, _take(X, torch.bfloat16, (M, K), dev, "X"), pw, ps, pz,
+          _take(out, torch.bfloat16, (M, N), dev, "out"), M, N, K, fmt, group)
+    return out
+
+
+def w4_gemv_experts(X, W, scales, ids, zeros=None, first_expert: int = 0, swiglu: bool = False, out=None, stream=None):
+    """w4_gemv with the matrix of each pair's expert: W uint8 [E,N,K/2], scales (and zeros)
+    [E,N,K/group], ids int32 [T,k] -> bf16 [T*k,N].  X bf16 [T,K], or [T*k,K] with a row per pair.
+    ``swiglu``: silu(rows [0,N/2)) * rows [N/2,N) -> [T*k,N/2].  Pairs without an expert among the E
+    (id - first_expert) get zeros."""
+    torch = _torch()
+    dev = _device_of(X, 2, "X")
+    _device_of(ids, 2, "ids")
+    T, k = ids.shape
+    rows, K = X.shape
+    if rows != T and rows != T * k:
+        raise ValueError("X must have a row per token or per pair")
+    if W.dim() != 3 or 2 * W.shape[2] != K:
+        raise ValueError("W must be [E,N,K/2]")
+    E, N = W.shape[0], W.shape[1]
+    if swiglu and N % 2:
+        raise ValueError("swiglu needs gate and up rows")
+    pw, ps, pz, fmt, group = _w4_format(W, scales, zeros, (E,), N, K, dev)
+    nout = N // 2 if swiglu else N
+    if out is None:
+        out = torch.empty((T * k, nout), dtype=torch.bfloat16, device=X.device)
+    _call("fp8gemm_w4_gemv_experts", dev, stream, _take(X, torch.bfloat16, (rows, K), dev, "X"), pw, ps, pz,
+          _take(ids, torch.int32, (T, k), dev, "ids"), _take(out, torch.bfloat16, (T * k, nout), dev, "out"),
+          T, k, E, N, K, fmt, group, first_expert, int(rows != T), int(swiglu))
+    return out

@@ -25,7 +25,9 @@ PROBE_LIB = os.path.join(HERE, "libreadprobe.so")
 PROBE_SOURCE = os.path.join(HERE, "csrc", "read_probe.hip")
 SOURCES = [os.path.join(CSRC, "fp8gemm_kernels.hip"), os.path.join(CSRC, "stream_kernels.hip"),
            os.path.join(CSRC, "quantize_kernels.hip"), os.path.join(CSRC, "scratch.hip"),
-           os.path.join(CSRC, "fp8gemm_api.cpp"),
+           os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "permute_kernels.hip"),
+           os.path.join(CSRC, "w4_kernels.hip"),
+           os.path.join(CSRC, "fp8gemm_api.cpp"), os.path.join(CSRC, "moe_api.cpp"),
            os.path.join(CSRC, "fp8gemm_jit.cpp")]
 # headers of the tiled kernel, compiled into the library as text for the run-time build
 JIT_HEADERS = ["fp8gemm_args.h", "fp8gemm_device.h", "fp8gemm_tiled.h"]

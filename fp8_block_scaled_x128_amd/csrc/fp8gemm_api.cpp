@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -20,6 +21,7 @@
 
 #include "fp8gemm.h"
 #include "fp8gemm_internal.h"
+#include "moe_internal.h"
 
 using namespace fp8gemm;
 
@@ -533,6 +535,38 @@ int dense(const void* A, const float* sa, const void* B, const float* sb, void* 
 }
 
 }  // namespace
+
+namespace fp8gemm {
+
+int host_device(HostDevice* out) {
+    DeviceState* d = nullptr;
+    const int st = device_state(&d);
+    if (st != FP8GEMM_OK) return st;
+    out->cus = d->cus;
+    out->err = d->err;
+    return FP8GEMM_OK;
+}
+
+int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch) {
+    DeviceState* d = nullptr;
+    int st = device_state(&d);
+    if (st != FP8GEMM_OK) return st;
+    Workspace* w = nullptr;
+    st = workspace(d, stream, bytes, 0, &w);
+    if (st != FP8GEMM_OK) return st;
+    *scratch = w->partials;
+    return FP8GEMM_OK;
+}
+
+void host_set_config(const char* fmt, ...) {
+    va_list args;
+    va_start(args, fmt);
+    std::vsnprintf(g_last_config, sizeof g_last_config, fmt, args);
+    va_end(args);
+    if (std::getenv("FP8GEMM_LOG")) std::fprintf(stderr, "[fp8gemm] %s\n", g_last_config);
+}
+
+}  // namespace fp8gemm
 
 extern "C" {
 

@@ -1,0 +1,339 @@
+// moe_api.cpp -- C ABI of the operators around the grouped products: expert routing, token
+// permutation (dispatch and combine) and 4-bit matrix-vector products.  Argument validation,
+// launch-shape choice and launch (host code); meaning and layouts: include/fp8gemm.h.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fp8gemm.h"
+#include "fp8gemm_internal.h"
+#include "moe_internal.h"
+
+using namespace fp8gemm;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxBytes = int64_t(1) << 40;
+constexpr int64_t kMaxPairs = int64_t(1) << 30;
+constexpr int64_t kMaxK4 = int64_t(1) << 22;      // 64 rows of a matrix stay below 2^31 bytes
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_ERR_LAUNCH; }
+
+// Shared checks of the two routing calls.
+int check_route(int64_t T, int32_t E, int32_t k, int32_t dtype, int32_t score, float scale) {
+    if (T < 0 || E <= 0 || k <= 0 || k > E) return FP8GEMM_ERR_BAD_SHAPE;
+    if ((dtype != FP8GEMM_F32 && dtype != FP8GEMM_BF16) ||
+        (score != FP8GEMM_SCORE_SOFTMAX && score != FP8GEMM_SCORE_SIGMOID) || !std::isfinite(scale))
+        return FP8GEMM_ERR_BAD_SHAPE;
+    if (E > kRouteMaxExperts || k > kRouteMaxTopk || T > kMaxRows) return FP8GEMM_ERR_UNSUPPORTED;
+    return FP8GEMM_OK;
+}
+
+int check_dispatch(int64_t T, int64_t H, int32_t k, int32_t G, int64_t cap) {
+    if (T < 0 || k <= 0 || G <= 0 || cap < 0 || H <= 0 || H % 128 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (k > kDispatchMaxTopk || G > kDispatchMaxGroups || T >= kMaxPairs / k ||
+        H > (int64_t(1) << 24) || 2 * T * H >= kMaxBytes || T * ((H + 2047) / 2048) > kMaxRows)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    return FP8GEMM_OK;
+}
+
+// Batches of at most this many pairs are ranked inside the copying launch.  Measured (H = 7168,
+// k = 8, 64 experts): see the comment at the choice below.
+constexpr int64_t kSmallPairs = 2048;
+
+int dispatch(DispatchArgs a, hipStream_t stream) {
+    HostDevice d;
+    int st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    a.err = d.err;
+    a.nkb = a.H / 128;
+    a.pairs = (int32_t)(a.T * a.k);
+    a.div_k = make_fastdiv((uint32_t)a.k);
+    const bool large = a.pairs > kSmallPairs;
+    if (large) {
+        a.chunks = (a.pairs + kDispatchChunk - 1) / kDispatchChunk;
+        const size_t words = (size_t)a.G * a.chunks + 2 * (size_t)a.G + (size_t)a.pairs;
+        void* p = nullptr;
+        st = host_stream_scratch(stream, words * sizeof(int32_t), &p);
+        if (st != FP8GEMM_OK) return st;
+        a.scratch = static_cast<int32_t*>(p);
+    }
+    host_set_config("moe_dispatch_%s pairs=%d experts=%d %s", a.contiguous ? "contiguous" : "masked", a.pairs, a.G,
+                    large ? "count+scan+copy" : "one launch");
+    launch_dispatch(a, large, stream);
+    return launched();
+}
+
+int check_combine(int64_t T, int64_t H, int32_t k, int64_t R, const int32_t* row_map) {
+    if (T < 0 || k <= 0 || R < 0 || H <= 0 || H % 8 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (k > kCombineMaxTopk || T > kMaxRows / k || R > kMaxRows || H > (int64_t(1) << 24) || 2 * T * H >= kMaxBytes ||
+        2 * R * H >= kMaxBytes || T * ((H + 2047) / 2048) > kMaxRows)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    if (!row_map && R < T * k) return FP8GEMM_ERR_BAD_SHAPE;
+    return FP8GEMM_OK;
+}
+
+// Shared checks of the two 4-bit products; G matrices [N][K].
+int check_w4(int64_t rows, int64_t G, int64_t N, int64_t K, int32_t format, int32_t group, const uint8_t* zeros) {
+    if (rows < 0 || N < 0 || K <= 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (format == FP8GEMM_W4_MXFP4) {
+        if (group != 32 || zeros) return FP8GEMM_ERR_BAD_SHAPE;
+    } else if (format != FP8GEMM_W4_INT4 || (group != 32 && group != 64 && group != 128)) {
+        return FP8GEMM_ERR_BAD_SHAPE;
+    }
+    if (K % group != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (K > kMaxK4 || N > (int64_t(1) << 24) || rows > kMaxRows || G * N * (K / 2) >= kMaxBytes || rows * K * 2 >= kMaxBytes ||
+        rows * N * 2 >= kMaxBytes)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    return FP8GEMM_OK;
+}
+
+int check_w4_ptrs(const void* X, const void* W, const void* scales, const uint8_t* zeros, const void* Y) {
+    if (!X || !W || !scales || !Y) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(scales, 4) || !aligned(zeros, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    return FP8GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights, int64_t T, int32_t E,
+                       int32_t k, int32_t dtype, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                       int32_t renorm, float scale, void* stream) {
+    int st = check_route(T, E, k, dtype, score, scale);
+    if (st != FP8GEMM_OK) return st;
+    if (n_group <= 0 || E % n_group != 0 || topk_group <= 0 || topk_group > n_group) return FP8GEMM_ERR_BAD_SHAPE;
+    const int32_t size = E / n_group;
+    if (k > topk_group * size || (n_group > 1 && (group_top < 1 || group_top > 2 || group_top > size)))
+        return FP8GEMM_ERR_BAD_SHAPE;
+    if (n_group > kRouteMaxGroups) return FP8GEMM_ERR_UNSUPPORTED;
+    if (T == 0) return FP8GEMM_OK;
+    if (!logits || !ids || !weights) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(logits, dtype == FP8GEMM_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    RouteArgs a{};
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.n_group = topk_group == n_group ? 1 : n_group;   // every group stays: no choice between them
+    a.topk_group = topk_group;
+    a.group_top = group_top;
+    a.group_size = size;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    host_set_config("route_topk T=%lld E=%d k=%d groups=%d/%d", (long long)T, E, k, topk_group, n_group);
+    launch_route_topk(a, dtype == FP8GEMM_BF16, score == FP8GEMM_SCORE_SIGMOID, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int64_t T,
+                                int32_t E, int32_t k, int32_t dtype, int32_t score, int32_t renorm, float scale,
+                                void* stream) {
+    const int st = check_route(T, E, k, dtype, score, scale);
+    if (st != FP8GEMM_OK) return st;
+    if (T == 0) return FP8GEMM_OK;
+    if (!logits || !ids || !dweights || !dlogits) return FP8GEMM_ERR_NULL_PTR;
+    const uintptr_t al = dtype == FP8GEMM_F32 ? 4 : 2;
+    if (!aligned(logits, al) || !aligned(dlogits, al) || !aligned(ids, 4) || !aligned(dweights, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    RouteBackwardArgs a{};
+    a.logits = logits;
+    a.ids = ids;
+    a.dweights = dweights;
+    a.dlogits = dlogits;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    host_set_config("route_topk_backward T=%lld E=%d k=%d", (long long)T, E, k);
+    launch_route_backward(a, dtype == FP8GEMM_BF16, score == FP8GEMM_SCORE_SIGMOID, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+int fp8gemm_moe_dispatch_masked(const void* X, const int32_t* ids, void* A, float* sa, int32_t* masked_m,
+                                int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_max,
+                                int32_t first_expert, void* stream) {
+    int st = check_dispatch(T, H, k, G, M_max);
+    if (st != FP8GEMM_OK) return st;
+    if (first_expert < 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (M_max > kMaxRows / G || (int64_t)G * M_max * H >= kMaxBytes) return FP8GEMM_ERR_UNSUPPORTED;
+    if (!masked_m || (T > 0 && (!X || !ids || !row_map || (M_max > 0 && (!A || !sa))))) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(X, 16) || !aligned(A, 16) || !aligned(sa, 4) || !aligned(ids, 4) || !aligned(masked_m, 4) ||
+        !aligned(row_map, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    DispatchArgs a{};
+    a.X = static_cast<const uint16_t*>(X);
+    a.ids = ids;
+    a.A = static_cast<uint8_t*>(A);
+    a.sa = sa;
+    a.where = masked_m;
+    a.row_map = row_map;
+    a.T = T;
+    a.H = (int32_t)H;
+    a.k = k;
+    a.G = G;
+    a.first = first_expert;
+    a.cap = (int32_t)M_max;
+    return dispatch(a, static_cast<hipStream_t>(stream));
+}
+
+int fp8gemm_moe_dispatch_contiguous(const void* X, const int32_t* ids, void* A, float* sa, int32_t* m_indices,
+                                    int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_total,
+                                    int32_t first_expert, void* stream) {
+    int st = check_dispatch(T, H, k, G, M_total);
+    if (st != FP8GEMM_OK) return st;
+    if (first_expert < 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (M_total > kMaxRows || M_total * H >= kMaxBytes) return FP8GEMM_ERR_UNSUPPORTED;
+    if ((M_total > 0 && !m_indices) || (T > 0 && (!X || !ids || !row_map || (M_total > 0 && (!A || !sa)))))
+        return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(X, 16) || !aligned(A, 16) || !aligned(sa, 4) || !aligned(ids, 4) || !aligned(m_indices, 4) ||
+        !aligned(row_map, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    DispatchArgs a{};
+    a.X = static_cast<const uint16_t*>(X);
+    a.ids = ids;
+    a.A = static_cast<uint8_t*>(A);
+    a.sa = sa;
+    a.where = m_indices;
+    a.row_map = row_map;
+    a.T = T;
+    a.H = (int32_t)H;
+    a.k = k;
+    a.G = G;
+    a.first = first_expert;
+    a.cap = (int32_t)M_total;
+    a.contiguous = 1;
+    return dispatch(a, static_cast<hipStream_t>(stream));
+}
+
+int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_map, void* out, int64_t T, int64_t H,
+                        int32_t k, int64_t R, void* stream) {
+    int st = check_combine(T, H, k, R, row_map);
+    if (st != FP8GEMM_OK) return st;
+    if (T == 0) return FP8GEMM_OK;
+    if (!out || (R > 0 && !Y)) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(Y, 16) || !aligned(out, 16) || !aligned(weights, 4) || !aligned(row_map, 4)) return FP8GEMM_ERR_MISALIGNED;
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    CombineArgs a{};
+    a.Y = static_cast<const uint16_t*>(Y);
+    a.weights = weights;
+    a.row_map = row_map;
+    a.out = static_cast<uint16_t*>(out);
+    a.T = T;
+    a.R = R;
+    a.H = (int32_t)H;
+    a.k = k;
+    a.err = d.err;
+    host_set_config("moe_combine T=%lld k=%d H=%lld", (long long)T, k, (long long)H);
+    launch_combine(a, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* weights, const int32_t* row_map, void* dY,
+                                 float* dweights, int64_t T, int64_t H, int32_t k, int64_t R, void* stream) {
+    int st = check_combine(T, H, k, R, row_map);
+    if (st != FP8GEMM_OK) return st;
+    if (T == 0) return FP8GEMM_OK;
+    if (!dout || (R > 0 && (!dY || (dweights && !Y)))) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(dout, 16) || !aligned(Y, 16) || !aligned(dY, 16) || !aligned(weights, 4) || !aligned(row_map, 4) ||
+        !aligned(dweights, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    CombineArgs a{};
+    a.Y = static_cast<const uint16_t*>(Y);
+    a.weights = weights;
+    a.row_map = row_map;
+    a.dout = static_cast<const uint16_t*>(dout);
+    a.dY = static_cast<uint16_t*>(dY);
+    a.dweights = dweights;
+    a.T = T;
+    a.R = R;
+    a.H = (int32_t)H;
+    a.k = k;
+    a.err = d.err;
+    host_set_config("moe_combine_backward T=%lld k=%d H=%lld", (long long)T, k, (long long)H);
+    launch_combine_backward(a, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint8_t* zeros, void* Y, int64_t M, int64_t N,
+                    int64_t K, int32_t format, int32_t group, void* stream) {
+    int st = check_w4(M, 1, N, K, format, group, zeros);
+    if (st != FP8GEMM_OK) return st;
+    if (M > (int64_t(1) << 20)) return FP8GEMM_ERR_UNSUPPORTED;   // the grid's second dimension
+    if (M == 0 || N == 0) return FP8GEMM_OK;
+    st = check_w4_ptrs(X, W, scales, zeros, Y);
+    if (st != FP8GEMM_OK) return st;
+    W4Args a{};
+    a.X = static_cast<const uint16_t*>(X);
+    a.W = static_cast<const uint8_t*>(W);
+    a.scales = scales;
+    a.zeros = zeros;
+    a.Y = static_cast<uint16_t*>(Y);
+    a.M = M;
+    a.N = a.nout = (int32_t)N;
+    a.K = (int32_t)K;
+    a.groups = (int32_t)(K / group);
+    a.div_k = make_fastdiv(1);
+    host_set_config("w4_gemv %s group=%d M=%lld N=%lld K=%lld", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4", group,
+                    (long long)M, (long long)N, (long long)K);
+    launch_w4(a, group, format == FP8GEMM_W4_MXFP4, 0, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, const uint8_t* zeros, const int32_t* ids,
+                            void* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t format, int32_t group,
+                            int32_t first_expert, int32_t x_per_pair, int32_t swiglu, void* stream) {
+    if (T < 0 || k <= 0 || E <= 0 || first_expert < 0) return FP8GEMM_ERR_BAD_SHAPE;
+    int st = check_w4(T, E, N, K, format, group, zeros);
+    if (st != FP8GEMM_OK) return st;
+    if (swiglu && N % 2 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (T > kMaxPairs / k || E > 65534 || T * k * N * 2 >= kMaxBytes || (x_per_pair ? T * k : T) * K * 2 >= (int64_t(1) << 31))
+        return FP8GEMM_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0) return FP8GEMM_OK;
+    st = check_w4_ptrs(X, W, scales, zeros, Y);
+    if (st != FP8GEMM_OK) return st;
+    if (!ids) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(ids, 4)) return FP8GEMM_ERR_MISALIGNED;
+    W4Args a{};
+    a.X = static_cast<const uint16_t*>(X);
+    a.W = static_cast<const uint8_t*>(W);
+    a.scales = scales;
+    a.zeros = zeros;
+    a.Y = static_cast<uint16_t*>(Y);
+    a.ids = ids;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.half = swiglu ? (int32_t)(N / 2) : 0;
+    a.nout = swiglu ? a.half : a.N;
+    a.groups = (int32_t)(K / group);
+    a.pairs = (int32_t)(T * k);
+    a.E = E;
+    a.first = first_expert;
+    a.by_slot = a.pairs <= std::min(E, kW4MaxPairsBySlot);
+    a.per_pair = x_per_pair != 0;
+    a.div_k = make_fastdiv((uint32_t)k);
+    host_set_config("w4_gemv_experts %s group=%d pairs=%d N=%lld K=%lld by %s", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
+                    group, a.pairs, (long long)N, (long long)K, a.by_slot ? "pair" : "expert");
+    launch_w4_experts(a, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, 0, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+}  // extern "C"

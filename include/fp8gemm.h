@@ -212,9 +212,118 @@ int fp8gemm_moe_expert_masked(const void* A, const float* sa, const void* W1, co
                               void* Hq, float* sh, void* out, int32_t G, int64_t M_max, int64_t H,
                               int64_t I, int64_t expected_m, void* stream);
 
+/* ---- expert routing, token permutation, 4-bit matrix-vector products ------------------------
+ * The steps of an MoE layer on either side of the grouped products (page "Perpustakaan operator
+ * GPU sumber terbuka DeepSeek DeepGEMM memperbarui versi besar, menambahkan Mega MoE…": dispatch,
+ * linear layer, SwiGLU, linear layer, combine), and the products a decode step makes with few
+ * rows.  A "pair" (t, j) is pick j of token t; flat index t * k + j. */
+
+#define FP8GEMM_F32 0            /* dtype of the router's logits */
+#define FP8GEMM_BF16 1
+#define FP8GEMM_SCORE_SOFTMAX 0
+#define FP8GEMM_SCORE_SIGMOID 1
+#define FP8GEMM_W4_MXFP4 0       /* E2M1 codes, one E8M0 scale per 32 values */
+#define FP8GEMM_W4_INT4 1        /* unsigned codes, one bf16 scale (and zero point) per group */
+
+/* The k experts of each token and their weights.  logits [T][E] (fp32 or bf16), bias [E] fp32 or
+ * NULL, ids [T][k] int32 and weights [T][k] fp32 (written).  Per token, in fp32:
+ *   s = softmax(logits) over the E experts, or sigmoid(logits);
+ *   c = s + bias: the value experts are chosen by.  The bias balances the experts' load and does
+ *     not enter the weights.  Without a bias the choice goes by the logits, which order as s does
+ *     also where scores round to the same value.
+ *   With n_group > 1 the experts are n_group groups of E / n_group consecutive ones; a group's
+ *     score is the sum of its group_top (1 or 2) largest c, and only the experts of the
+ *     topk_group groups of largest score can be chosen.
+ *   ids[t] = the k largest c in descending order; weights[t][j] = s[ids[t][j]], divided by their
+ *     sum with `renorm` (0 where the sum is 0), times `scale`.
+ * Equal values go to the lower index, for groups and experts.  A NaN counts as -infinity and
+ * +infinity as the largest finite value, in logits and bias.  An expert whose logit or bias is
+ * -infinity cannot be chosen; where fewer than k can, the remaining ids are -1 and weights 0.
+ * E <= 1024, k <= 32, n_group <= 64 (else UNSUPPORTED); k at most the experts of topk_group
+ * groups, group_top at most a group's size (else BAD_SHAPE).  logits need the alignment of their
+ * type only. */
+int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights, int64_t T, int32_t E,
+                       int32_t k, int32_t dtype, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                       int32_t renorm, float scale, void* stream);
+
+/* Gradient of the router's weights with respect to the logits (the choice itself has none, nor
+ * has the bias).  dweights [T][k] fp32; dlogits [T][E] (written, the type of logits): with g =
+ * scale * dweights, p = s / sum of the picked s, over the picked experts j of a token:
+ *   sigmoid            dlogits[j] = g_j s_j (1 - s_j)
+ *   sigmoid, renorm    dlogits[j] = (g_j - sum g p) p_j (1 - s_j)
+ *   softmax            dlogits[e] = s_e ([e picked] g_e - sum g s), every expert
+ *   softmax, renorm    dlogits[j] = (g_j - sum g p) p_j
+ * and 0 elsewhere.  ids as route_topk wrote them: an id outside [0, E) contributes nothing; the
+ * ids of a token are distinct (else its row is unspecified). */
+int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int64_t T,
+                                int32_t E, int32_t k, int32_t dtype, int32_t score, int32_t renorm, float scale,
+                                void* stream);
+
+/* Dispatch: every token's row, quantised as fp8gemm_quantize_1x128 does, into the rows of its
+ * experts.  X [T][H] bf16, ids [T][k]: the pair (t, j) goes to local expert g = ids[t][j] -
+ * first_expert, or nowhere if g is outside [0, G) or the id negative.  Within an expert the rows
+ * stand in the order of t, then j.
+ *   masked: the pair of rank r of expert g goes to row r of A [G][M_max][H], with its scales in
+ *     sa [G][H/128][M_max]; masked_m [G] (written) counts an expert's rows.
+ *   contiguous: A [M_total][H], sa [H/128][M_total]; experts follow each other, each padded to a
+ *     multiple of 128 rows; m_indices [M_total] (written) holds a row's expert g, -1 on padding
+ *     and past the last expert.  M_total of T * k + 127 * min(G, T * k) always suffices.
+ *   row_map [T][k] (written): the pair's row (masked: g * M_max + r), or -1.
+ * A pair past the capacity is dropped (row -1; masked_m is at most M_max) and flags
+ * FP8GEMM_DEVERR_BAD_COUNT.  Rows of A and entries of sa that no pair goes to are left untouched.
+ * X must hold finite values.  H: a positive multiple of 128; k <= 32, G <= 1024.  X and A 16-byte
+ * aligned.  Batches of more than 2048 pairs use the stream's workspace (see fp8gemm_prepare_stream). */
+int fp8gemm_moe_dispatch_masked(const void* X, const int32_t* ids, void* A, float* sa, int32_t* masked_m,
+                                int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_max,
+                                int32_t first_expert, void* stream);
+int fp8gemm_moe_dispatch_contiguous(const void* X, const int32_t* ids, void* A, float* sa, int32_t* m_indices,
+                                    int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_total,
+                                    int32_t first_expert, void* stream);
+
+/* Combine: out[t] = bf16(sum_j weights[t][j] * Y[row_map[t][j]]), the sum in fp32 in the order of
+ * j; pairs whose row is -1 are left out (a token without any gets zeros).  Y [R][H] bf16 (any
+ * grouped output, flattened), out [T][H] bf16.  weights NULL: ones (also the gradient of a
+ * dispatch with respect to X); row_map NULL: row t * k + j.  A row of R or more is left out and
+ * flags FP8GEMM_DEVERR_BAD_INDEX.  H: a positive multiple of 8; k <= 32; Y, out 16-byte aligned. */
+int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_map, void* out, int64_t T, int64_t H,
+                        int32_t k, int64_t R, void* stream);
+
+/* Gradients of the combine: dY[row_map[t][j]] = bf16(weights[t][j] * dout[t]) and dweights[t][j] =
+ * sum_h dout[t][h] * Y[row_map[t][j]][h] (fp32; 0 for pairs without a row).  dY rows that no pair
+ * names are left untouched; rows are distinct.  dweights NULL: dY alone (Y may then be NULL). */
+int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* weights, const int32_t* row_map, void* dY,
+                                 float* dweights, int64_t T, int64_t H, int32_t k, int64_t R, void* stream);
+
+/* Y[m][n] = bf16(sum_k X[m][k] V[n][k]) for few rows of X (one to some tens: the weights are read
+ * once per 16 or 32 rows), V decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N]
+ * bf16, W [N][K/2] bytes, the even element of a row in the low nibble:
+ *   FP8GEMM_W4_MXFP4: E2M1 codes, scales uint8 [N][K/32] (E8M0), the B and sb of
+ *     fp8gemm_fp8fp4_grouped_masked; group = 32, zeros NULL.  Products are exact: a decoded value is
+ *     a bf16 value.  Scales below 2^-120 may flush; 255 gives unspecified results.
+ *   FP8GEMM_W4_INT4: codes q in 0..15, V = (q - z) * s, scales bf16 [N][K/group], zeros uint8
+ *     [N][K/group] (0..15; NULL: 8), group 32, 64 or 128.  A group's sum of x * (q - z) is formed first,
+ *     exactly up to fp32 rounding, then scaled.
+ * K: a positive multiple of the group (else BAD_SHAPE), at most 2^22; M <= 2^20, N <= 2^24.  X, W and Y 16-byte
+ * aligned, scales and zeros 4-byte aligned. */
+int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint8_t* zeros, void* Y, int64_t M, int64_t N,
+                    int64_t K, int32_t format, int32_t group, void* stream);
+
+/* The same with the matrix of each pair's expert: W [E][N][K/2], scales and zeros [E][N][K/group],
+ * ids [T][k] int32, local expert ids[t][j] - first_expert; Y [T * k][N].
+ *   X [T][K], or [T * k][K] with x_per_pair.
+ *   swiglu: rows [0, N/2) of a matrix are the gate, [N/2, N) the up projection, and Y [T * k][N/2] =
+ *     bf16(silu(gate) * up), both in fp32; N even.
+ * A pair without an expert here (id negative or outside) gets a row of zeros.  Pairs that share an
+ * expert share one reading of its matrix (up to 16 of them).  X below 2^31 bytes. */
+int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, const uint8_t* zeros, const int32_t* ids,
+                            void* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t format, int32_t group,
+                            int32_t first_expert, int32_t x_per_pair, int32_t swiglu, void* stream);
+
 /* Device-side precondition flags (bits of the device error word). */
-#define FP8GEMM_DEVERR_BAD_INDEX 1 /* contiguous: an m_indices entry outside [-1, G) or off its block's group */
-#define FP8GEMM_DEVERR_BAD_COUNT 2 /* masked GEMM or quantiser: a masked_m entry outside [0, M_max] */
+#define FP8GEMM_DEVERR_BAD_INDEX 1 /* contiguous: an m_indices entry outside [-1, G) or off its block's group;
+                                      combine: a row_map entry of R or more */
+#define FP8GEMM_DEVERR_BAD_COUNT 2 /* masked GEMM or quantiser: a masked_m entry outside [0, M_max];
+                                      dispatch: an expert's rows exceed the capacity */
 
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* fp8gemm_status_string(int status);
