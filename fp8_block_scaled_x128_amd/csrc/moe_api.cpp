@@ -101,6 +101,19 @@ int check_w4_ptrs(const void* X, const void* W, const void* scales, const uint8_
     return FP8GEMM_OK;
 }
 
+// Tiles of 16 rows that a wave takes one after the other, each with all of K, or 0: a workgroup's 8
+// waves share a tile's K.  `busy` workgroup columns (row blocks of X, pairs or experts) have work.  A
+// wave of its own needs no exchange of sums but 6 waves per CU to fill it, and all of X in LDS (64 KB, so
+// that two workgroups share a CU).  Measured, shared K and own, us, MXFP4: 1 x 24576 x 1536 9.8 and 7.8,
+// 1 x 32768 x 512 8.2 and 4.9, 16 x 24576 x 1536 12.4 and 9.3, 128 pairs of 7168 x 2048 on 64 experts 155
+// and 80; but 1 x 16384 x 2048 7.8 and 8.1, 1 x 7168 x 2048 5.1 and 7.1, 1 x 32768 x 7168 26.7 and 27.2.
+// Two tiles keep the loads going from one to the next where there are that many.
+int w4_tiles_per_wave(int64_t nout, int64_t K, int cols, int64_t busy, int cus) {
+    const int64_t tiles = (nout + 15) / 16 * busy, slots = 16 * (int64_t)cus;
+    if (tiles < 6 * (int64_t)cus || K > 4096 || cols * K * 2 > 65536) return 0;
+    return tiles >= 2 * slots ? 2 : 1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -292,9 +305,19 @@ int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint
     a.K = (int32_t)K;
     a.groups = (int32_t)(K / group);
     a.div_k = make_fastdiv(1);
-    host_set_config("w4_gemv %s group=%d M=%lld N=%lld K=%lld", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4", group,
-                    (long long)M, (long long)N, (long long)K);
-    launch_w4(a, group, format == FP8GEMM_W4_MXFP4, 0, static_cast<hipStream_t>(stream));
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    a.cols = (int32_t)std::min<int64_t>(M, 16);
+    // up to 4 rows of X leave room for whole rows of 8192 values in LDS beside narrow tiles, which fill more
+    // CUs (us, 16 and 32 rows a tile: 1 x 4096 x 7168 6.7 and 8.6, 1 x 7168 x 16384 17.6 and 17.5); wide tiles
+    // share X's LDS traffic (and a short row's exchange: 1 x 7168 x 2048 5.7 and 5.1)
+    const int rn = a.cols > 4 || K < 4096 ? 2 : 1;
+    a.tiles_per_wave = w4_tiles_per_wave(N, K, a.cols, (M + 15) / 16, d.cus);
+    host_set_config("w4_gemv %s group=%d M=%lld N=%lld K=%lld rn=%d tiles_per_wave=%d", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
+                    group, (long long)M, (long long)N, (long long)K, rn, a.tiles_per_wave);
+    launch_w4(a, rn, group, format == FP8GEMM_W4_MXFP4, s);
     return launched();
 }
 
@@ -329,10 +352,19 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
     a.first = first_expert;
     a.by_slot = a.pairs <= std::min(E, kW4MaxPairsBySlot);
     a.per_pair = x_per_pair != 0;
+    a.xrows = (int32_t)(x_per_pair ? T * k : T);
     a.div_k = make_fastdiv((uint32_t)k);
-    host_set_config("w4_gemv_experts %s group=%d pairs=%d N=%lld K=%lld by %s", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
-                    group, a.pairs, (long long)N, (long long)K, a.by_slot ? "pair" : "expert");
-    launch_w4_experts(a, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, 0, static_cast<hipStream_t>(stream));
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    // rows of X that a pass over an expert's matrix takes; a token's picks are distinct as a rule, so an
+    // expert has at most T pairs, and pairs / E on average.  A more crowded one takes more passes.
+    a.cols = (int32_t)std::min<int64_t>(std::min<int64_t>(T, 16), 4 + 2 * ((a.pairs + E - 1) / E));
+    const int64_t busy = std::min<int64_t>(a.pairs, E);
+    a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.cus);
+    host_set_config("w4_gemv_experts %s group=%d pairs=%d N=%lld K=%lld tiles_per_wave=%d by %s", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
+                    group, a.pairs, (long long)N, (long long)K, a.tiles_per_wave, a.by_slot ? "pair" : "expert");
+    launch_w4_experts(a, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, static_cast<hipStream_t>(stream));
     return launched();
 }
 

@@ -113,9 +113,15 @@ struct W4Args {
     int32_t by_slot;            // experts: grid.y counts pairs (else experts)
     int32_t per_pair;           // experts: X has a row per pair (else per token)
     FastDiv div_k;              // pair -> token
+    int32_t xrows;              // experts: rows of X
+    int32_t tiles_per_wave;     // 0: a workgroup's waves share the K of one tile
+    int32_t cols;               // rows of X a pass takes (at most 16)
+    int32_t xsteps, xstride;    // X in LDS: steps of 128 values, bytes of a row
+    FastDiv div_units;          // 16-byte units of a row
 };
 
-void launch_w4(const W4Args& a, int group, bool mxfp4, int rows_per_wave, hipStream_t s);
-void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, int rows_per_wave, hipStream_t s);
+// rn: 16-row tiles of V per workgroup where its waves share K.
+void launch_w4(const W4Args& a, int rn, int group, bool mxfp4, hipStream_t s);
+void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, hipStream_t s);
 
 }  // namespace fp8gemm

@@ -8,21 +8,27 @@
 // to decode them, 4 a weight; the products run on the matrix cores (16x16x32 bf16, X's rows as one
 // operand's 16 rows and 16 weight rows as the other's), where up to 16 rows of X cost the same.
 //
-// One workgroup of 8 waves owns 16 RN rows of V and all of K; wave w takes the steps (128 values
-// of K) w, w + 8, ..., so the workgroup reads each row in runs of 512 bytes, and a ring of PD
-// steps keeps that many loads in flight.  The waves' fp32 sums meet in LDS and are added in wave
-// order.  In a step lane (n, j) = (lane % 16, lane / 16) loads 16 bytes of row n: its chunk j of
-// 32 values.
-//   MXFP4: the lane decodes its chunk with the chunk's scale in the conversion instruction (two
+// A workgroup owns 16 RN rows of V and all of K.  Its waves take pairs of steps (a step is 128
+// values of K, 64 bytes of a row; a pair is one 128-byte line) in turn, each with all RN row
+// tiles, and keep PP pairs in registers on their way: 64 KB per workgroup of 8 waves.  X's values
+// stand in LDS, all of them or, past 128 KB, in chunks.  The waves' fp32 sums meet in LDS and are
+// added in wave order.  Splitting K over workgroups was measured and dropped: the exchange of sums
+// costs 2 us, more than the idle CUs of a small matrix do.
+//
+// In a step lane (n, j) = (lane % 16, lane / 16) loads 16 bytes of row n: its chunk j of 32 values.
+//   MXFP4: the lane decodes its 32 values with their scale in the conversion instruction (two
 //   values each, exact in bf16); matrix-core step i takes the values 8 i .. 8 i + 7 of all four
-//   chunks.
+//   lanes.
 //   INT4: the sums of different groups have to stay apart until they are scaled.  Two lane swaps
-//   transpose the four chunks' words across the four lanes of a row, so that matrix-core step i
-//   takes chunk i alone.  Codes become the bf16 values 16 + q by inserting them below the
+//   transpose the words across the four lanes of a row, so that matrix-core step i takes 32
+//   consecutive values.  Codes become the bf16 values 16 + q by inserting them below the
 //   exponent of 16 (exact); the group's sum is then (sum - (16 + z) sum_k x) * scale in fp32, with
 //   sum_k x from one more matrix-core step against ones.
 
+#include <algorithm>
+
 #include "fp8gemm_device.h"
+#include "fp8gemm_internal.h"
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -32,8 +38,9 @@ namespace {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 8, kW4Threads = kWaves * 64;
-constexpr int kStep = 128;                 // K values per wave and step: four chunks of 32
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int kStep = 128;                 // K values per wave and step: four runs of 32
+constexpr int kXSteps = 512;               // steps x rows of X that stand in LDS at a time: 128 KB
 
 enum Mode { kOne = 0, kExperts = 1, kExpertsSwiglu = 2 };
 
@@ -82,39 +89,49 @@ __device__ __forceinline__ void transpose4(v4u& w) {
     w[3] = d[1];
 }
 
-// One operand's rows as a bounded buffer: reads past `bytes` give 0.
-struct Rows {
-    __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t bytes;
-    __device__ __forceinline__ Rows(const void* p, int64_t n)
-        : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)n, kBufferFlags)), bytes((uint32_t)n) {}
-};
+// `bytes` bytes at p, a buffer: reads past them give 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kBufferFlags);
+}
 
-// GROUP: values per scale; MX: MXFP4; WIDE: a step's scales are adjacent and aligned (K a multiple
-// of 128), one load; RN: 16-row tiles of V, MT: 16-row tiles of X; MODE: see Mode (with SwiGLU
+// Workgroup barrier that orders LDS traffic only: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// GROUP: values per scale; MX: MXFP4; PAIR: a pair's scales (and zero points) are adjacent and
+// aligned, one load each, else one load per group; RN: 16-row tiles of V; PP: pairs of steps in flight per wave; MULTI: X stands in LDS by chunks; MODE: see Mode (with SwiGLU
 // tile 0 holds gate rows and tile 1 the matching up rows).
-template <int GROUP, bool MX, bool WIDE, bool ZEROS, int RN, int MT, int PD, int MODE>
-__global__ __launch_bounds__(kW4Threads) void w4_kernel(W4Args a) {
+template <int GROUP, bool MX, bool PAIR, bool ZEROS, int RN, int PP, bool ALONE, bool MULTI, int MODE>
+__global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 2 : 4) void w4_kernel(W4Args a) {
     constexpr int PER = kStep / GROUP;             // scales per step
-    constexpr int SB = MX ? 1 : 2;                 // bytes per scale
+    constexpr int SBYTES = 2 * PER * (MX ? 1 : 2); // bytes of a pair's scales
     constexpr bool SWIGLU = MODE == kExpertsSwiglu;
-    constexpr int kBatch = RN * MT < 4 ? RN * MT : 4;   // output tiles reduced at a time
-    __shared__ v4f red[kWaves][kBatch][64];
+    constexpr int SHARE = ALONE ? 1 : kWaves;      // waves that share a tile's K
+    constexpr int CS = SHARE * PP * 2;             // steps per round of the ring
+    static_assert(!(ALONE && MULTI), "waves of their own pass over X at their own pace");
+    // X's rows [cols][xstride], then the waves' sums
+    extern __shared__ v4u lds[];
+    v4f(*red)[RN][64] = reinterpret_cast<v4f(*)[RN][64]>(lds);
     __shared__ int cols[MODE == kOne ? 1 : kW4MaxPairsBySlot];
     __shared__ int count, early;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ln = lane & 15, j = lane >> 4;
-    const int tile_rows = SWIGLU ? 16 : 16 * RN;
-    const int n0 = blockIdx.x * tile_rows;
+    constexpr int kTileRows = SWIGLU ? 16 : 16 * RN;
     const int n_end = SWIGLU ? a.half : a.N;
+    // tiles of this workgroup
+    const int per_wg = ALONE ? kWaves * a.tiles_per_wave : 1;
+    const int tile0 = blockIdx.x * per_wg, tile_end = min(tile0 + per_wg, (n_end + kTileRows - 1) / kTileRows);
 
     int expert = 0;
     int window = 0;                                // experts: first pair of the scanned window
     do {
         int ncols = 0;
         if constexpr (MODE == kOne) {
-            ncols = 1;
+            ncols = (int)min(a.M - (int64_t)blockIdx.y * 16, (int64_t)16);
         } else {
             // the pairs of this workgroup's expert; their order changes no result
             const int slot = blockIdx.y;
@@ -126,277 +143,369 @@ __global__ __launch_bounds__(kW4Threads) void w4_kernel(W4Args a) {
             if (a.by_slot && none) {
                 if (tid == 0) { cols[0] = slot; count = 1; }
             } else {
-                for (int p = tid; p < last; p += kW4Threads) {
+                for (int p = tid; p < last; p += kThreads) {
                     const int o = a.ids[window + p];
                     const bool outside = o < a.first || (int64_t)o - a.first >= a.E;
                     if (none ? outside : o == id && !outside) {
                         cols[atomicAdd(&count, 1)] = window + p;
-                        if (a.by_slot && p < slot) early = 1;
+                        if (a.by_slot && p < slot) early = 1;   // an earlier pair's workgroup has them all
                     }
                 }
             }
             __syncthreads();
-            ncols = a.by_slot && early ? 0 : count;
-            expert = none ? -1 : id - a.first;
+            ncols = __builtin_amdgcn_readfirstlane(a.by_slot && early ? 0 : count);
+            expert = __builtin_amdgcn_readfirstlane(none ? -1 : id - a.first);
             if (expert < 0) {                      // pairs without an expert here: zero rows
-                for (int i = tid; i < ncols * tile_rows; i += kW4Threads) {
-                    const int n = n0 + i % tile_rows;
-                    if (n < a.nout) a.Y[(int64_t)cols[i / tile_rows] * a.nout + n] = 0;
-                }
+                const int width = min(tile_end * kTileRows, a.nout) - tile0 * kTileRows;
+                for (int i = tid; i < ncols * width; i += kThreads)
+                    a.Y[(int64_t)cols[i / width] * a.nout + tile0 * kTileRows + i % width] = 0;
                 ncols = 0;
             }
         }
-        const int64_t matrix = (int64_t)expert * a.N;
-        const int row_bytes = a.K / 2, rows = min(n_end - n0, tile_rows);
-        const int chunks = a.K / 32, steps = (chunks + 3) / 4;
-        const int group_row = a.groups * SB;
-        // buffers of this workgroup's rows; with SwiGLU one for the gate rows and one for the up rows
-        constexpr int kParts = SWIGLU ? 2 : 1;
-        const int64_t first_row[2] = {matrix + n0, matrix + a.half + n0};
-        auto part = [&](int r) { return SWIGLU ? r : 0; };
+        const int row_bytes = a.K / 2;
+        const int units32 = a.K / 32, steps = (units32 + 3) / 4;
+        const int group_row = a.groups * (MX ? 1 : 2);
+        // a row tile is a buffer of weights, one of scales and one of zero points (with SwiGLU tile 0 holds
+        // the gate rows, tile 1 the up rows); a lane's offsets in them
+        const int64_t matrix = (int64_t)max(expert, 0) * a.N;
+        const int vw = ln * row_bytes + j * 16, vs = ln * group_row, vz = ln * a.groups;
+        auto tile_row = [&](int n0, int r) { return matrix + n0 + (SWIGLU ? r * a.half : r * 16); };
+        auto tile_rows = [&](int n0, int r) { return max(0, min(16, n_end - n0 - (SWIGLU ? 0 : r * 16))); };
 
-        for (int m0 = MODE == kOne ? blockIdx.y * 16 * MT : 0; MODE == kOne ? m0 >= 0 : m0 < ncols; m0 += 16 * MT) {
-            const Rows w0(a.W + first_row[0] * row_bytes, (int64_t)rows * row_bytes);
-            const Rows w1(a.W + first_row[kParts - 1] * row_bytes, (int64_t)rows * row_bytes);
-            const uint8_t* sp = static_cast<const uint8_t*>(a.scales);
-            const Rows s0(sp + first_row[0] * group_row, (int64_t)rows * group_row);
-            const Rows s1(sp + first_row[kParts - 1] * group_row, (int64_t)rows * group_row);
-            const Rows z0(ZEROS ? a.zeros + first_row[0] * a.groups : nullptr, ZEROS ? (int64_t)rows * a.groups : 0);
-            const Rows z1(ZEROS ? a.zeros + first_row[kParts - 1] * a.groups : nullptr, ZEROS ? (int64_t)rows * a.groups : 0);
-            const int64_t xrows = MODE == kOne ? min(a.M - m0, (int64_t)16 * MT) : 0;
-            const Rows x(MODE == kOne ? a.X + (int64_t)m0 * a.K : a.X,
-                         MODE == kOne ? xrows * a.K * 2
-                                      : (int64_t)(a.per_pair ? a.pairs : a.pairs / (int)a.div_k.d) * a.K * 2);
-            uint32_t xoff[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int m = t * 16 + ln;
-                if constexpr (MODE == kOne) {
-                    xoff[t] = (uint32_t)m * a.K * 2;                     // rows past the end lie past the buffer
-                    if (m >= xrows) xoff[t] = x.bytes;
-                } else {
-                    xoff[t] = x.bytes;
-                    if (m0 + m < ncols) {
-                        const int p = cols[m0 + m];
-                        xoff[t] = (uint32_t)(a.per_pair ? p : (int)fast_div(p, a.div_k)) * a.K * 2;
-                    }
-                }
-            }
+        for (int m0 = 0; m0 < ncols; m0 += a.cols) {     // kOne: once
+            const int here = min(ncols - m0, a.cols);
 
+            constexpr int SREGS = PAIR ? (SBYTES + 3) / 4 : MX ? 2 : 2 * PER;
+            constexpr int ZREGS = !ZEROS ? 1 : PAIR ? (2 * PER + 3) / 4 : 2 * PER;
             struct Slot {
-                v4u w[RN];
-                uint32_t s[RN][WIDE || MX ? (PER * SB + 3) / 4 : 4];
-                uint32_t z[RN][WIDE ? 1 : 4];
-                v4u x[MT][4];
+                v4u w[2][RN];
+                uint32_t s[RN][SREGS], z[RN][ZREGS];
             };
-            Slot ring[PD];
-            v4f acc[MT][RN];
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int r = 0; r < RN; ++r) acc[t][r] = v4f{0.f, 0.f, 0.f, 0.f};
+            Slot ring[PP];
+            v4f acc[RN];
 
-            auto load = [&](Slot& b, int step) {
-                const int c0 = step * 4, cj = c0 + j;
+            // Loads of the pair of steps from `step` (even) of the tile from row n0.  A step past the end, or a
+            // tile past the last row, reads an empty buffer; a step's offset is uniform and stays inside a row.
+            auto load = [&](Slot& b, int step, int n0) {
 #pragma unroll
                 for (int r = 0; r < RN; ++r) {
-                    const Rows& w = part(r) ? w1 : w0;
-                    const uint32_t n = (uint32_t)((SWIGLU ? 0 : r * 16) + ln);
-                    b.w[r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
-                        w.rsrc, cj < chunks ? (int)(n * row_bytes + cj * 16) : (int)w.bytes, 0, 0));
+                    const int n = step < steps ? tile_rows(n0, r) : 0, n1 = step + 1 < steps ? tile_rows(n0, r) : 0;
+                    const uint8_t* w = a.W + tile_row(n0, r) * row_bytes;
+                    b.w[0][r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                        buffer(w, n * row_bytes), vw, n ? step * 64 : 0, 0));
+                    b.w[1][r] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                        buffer(w, n1 * row_bytes), vw, n1 ? step * 64 + 64 : 0, 0));
                 }
 #pragma unroll
                 for (int r = 0; r < RN; ++r) {
-                    const Rows& s = part(r) ? s1 : s0;
-                    const Rows& z = part(r) ? z1 : z0;
-                    const uint32_t n = (uint32_t)((SWIGLU ? 0 : r * 16) + ln);
-                    if constexpr (WIDE) {
-                        const bool in = c0 < chunks;
-                        const int o = in ? (int)(n * group_row + step * PER * SB) : (int)s.bytes;
-                        if constexpr (PER * SB == 8) {
-                            const auto v = __builtin_amdgcn_raw_buffer_load_b64(s.rsrc, o, 0, 0);
+                    const int n = step < steps ? tile_rows(n0, r) : 0;
+                    const uint8_t* sp = static_cast<const uint8_t*>(a.scales) + tile_row(n0, r) * group_row;
+                    const uint8_t* zp = ZEROS ? a.zeros + tile_row(n0, r) * a.groups : nullptr;
+                    if constexpr (PAIR) {
+                        const auto s = buffer(sp, n * group_row);
+                        const int so = n ? step / 2 * SBYTES : 0, zo = n ? step * PER : 0;
+                        if constexpr (SBYTES == 16) {
+                            const auto v = __builtin_amdgcn_raw_buffer_load_b128(s, vs, so, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) b.s[r][i] = v[i];
+                        } else if constexpr (SBYTES == 8) {
+                            const auto v = __builtin_amdgcn_raw_buffer_load_b64(s, vs, so, 0);
                             b.s[r][0] = v[0];
                             b.s[r][1] = v[1];
-                        } else if constexpr (PER * SB == 4) {
-                            b.s[r][0] = __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, o, 0, 0);
                         } else {
-                            b.s[r][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(s.rsrc, o, 0, 0);
+                            b.s[r][0] = __builtin_amdgcn_raw_buffer_load_b32(s, vs, so, 0);
                         }
                         if constexpr (ZEROS) {
-                            const int oz = in ? (int)(n * a.groups + step * PER) : (int)z.bytes;
-                            if constexpr (PER == 4) b.z[r][0] = __builtin_amdgcn_raw_buffer_load_b32(z.rsrc, oz, 0, 0);
-                            else if constexpr (PER == 2) b.z[r][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(z.rsrc, oz, 0, 0);
-                            else b.z[r][0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z.rsrc, oz, 0, 0);
+                            const auto z = buffer(zp, n * a.groups);
+                            if constexpr (PER == 4) {
+                                const auto v = __builtin_amdgcn_raw_buffer_load_b64(z, vz, zo, 0);
+                                b.z[r][0] = v[0];
+                                b.z[r][1] = v[1];
+                            } else if constexpr (PER == 2) {
+                                b.z[r][0] = __builtin_amdgcn_raw_buffer_load_b32(z, vz, zo, 0);
+                            } else {
+                                b.z[r][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(z, vz, zo, 0);
+                            }
                         }
                     } else if constexpr (MX) {
-                        b.s[r][0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                            s.rsrc, cj < chunks ? (int)(n * group_row + cj) : (int)s.bytes, 0, 0);
+                        // a lane's own scale; past the end of the row (where the next row's stand) 0
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int g = (step + i) * 4 + j;
+                            b.s[r][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                buffer(sp, n * group_row), g < units32 ? vs + g : n * group_row, 0, 0);
+                        }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool in = c0 + i < chunks;
-                            const int gi = (c0 + i) / (GROUP / 32);
+                        for (int i = 0; i < 2 * PER; ++i) {
+                            const int g = step * PER + i, in = g < a.groups ? n : 0;
                             b.s[r][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                                s.rsrc, in ? (int)(n * group_row + gi * SB) : (int)s.bytes, 0, 0);
+                                buffer(sp, in * group_row), vs, in ? g * 2 : 0, 0);
                             if constexpr (ZEROS)
                                 b.z[r][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                    z.rsrc, in ? (int)(n * a.groups + gi) : (int)z.bytes, 0, 0);
+                                    buffer(zp, in * a.groups), vz, in ? g : 0, 0);
                         }
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // values 8 i .. of chunk j (MXFP4), values 8 j .. of chunk i (INT4)
-                        const int c = MX ? cj : c0 + i;
-                        const int within = MX ? i * 16 : j * 16;
-                        const bool in = c < chunks && xoff[t] < x.bytes;
-                        b.x[t][i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
-                            x.rsrc, in ? (int)(xoff[t] + c * 64 + within) : (int)x.bytes, 0, 0));
-                    }
             };
-            auto compute = [&](Slot& b) {
+
+            // X's values of a chunk of steps in LDS, 16 bytes a thread and unit, zeros past K; INT4 keeps them
+            // in the order of the decoded codes
+            const int chunk = a.xsteps;                  // whole rounds of the ring
+            const int row_units = chunk * (kStep / 8), xrow = a.xstride / 16;
+            const auto xbuf = buffer(MODE == kOne ? a.X + (int64_t)blockIdx.y * 16 * a.K : a.X,
+                                     MODE == kOne ? ncols * a.K * 2 : a.xrows * a.K * 2);
+            constexpr int XU = MULTI ? kXSteps * 16 / kThreads : 2;   // units a thread moves at a time (MULTI: the chunk)
+            v4u xv[XU];
+            auto fetch = [&](int first_step, int u0) {
+#pragma unroll
+                for (int i = 0; i < XU; ++i) {
+                    const int u = u0 + i * kThreads, c = (int)fast_div(u, a.div_units), q = u - c * row_units;
+                    const int k = first_step * kStep + q * 8;
+                    int o = -16;                         // past the buffer (unsigned)
+                    if (c < here && k < a.K) {
+                        int row = c;
+                        if constexpr (MODE != kOne) {
+                            const int p = cols[m0 + c];
+                            row = a.per_pair ? p : (int)fast_div(p, a.div_k);
+                        }
+                        o = (row * a.K + k) * 2;
+                    }
+                    xv[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(xbuf, o, 0, 0));
+                }
+            };
+            auto stage = [&](int u0) {
+#pragma unroll
+                for (int i = 0; i < XU; ++i) {
+                    const int u = u0 + i * kThreads, c = (int)fast_div(u, a.div_units), q = u - c * row_units;
+                    if (c < here) lds[c * xrow + q] = MX ? xv[i] : order_u4(xv[i]);
+                }
+            };
+            // (opaque: nothing derived from it is worth registers across the products)
+            auto thread = [&]() {
+                int u = tid;
+                asm volatile("" : "+v"(u));
+                return u;
+            };
+
+            // a lane's values of its row of X (rows past the last repeat it: their results are not used)
+            const int xl = min(ln, here - 1) * xrow + (MX ? j * 4 : j);
+            // step `sl` of the chunk, the h-th of the slot's pair
+            auto compute = [&](Slot& b, int h, int sl) {
+                v4u x[4];
+#pragma unroll
+                // values 8 i .. of lane j's 32 (MXFP4), values 8 j .. of the i-th 32 (INT4)
+                for (int i = 0; i < 4; ++i) x[i] = lds[xl + sl * 16 + (MX ? i : i * 4)];
                 if constexpr (MX) {
 #pragma unroll
                     for (int r = 0; r < RN; ++r) {
-                        const uint32_t s = WIDE ? (b.s[r][0] >> (8 * j)) & 0xFFu : b.s[r][0];
+                        const uint32_t s = PAIR ? (b.s[r][h] >> (8 * j)) & 0xFFu : b.s[r][h];
                         const float scale = __uint_as_float(s << 23);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const v4u w = decode_e2m1(b.w[r][i], scale);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) acc[t][r] = mfma_bf16(b.x[t][i], w, acc[t][r]);
-                        }
+                        for (int i = 0; i < 4; ++i) acc[r] = mfma_bf16(x[i], decode_e2m1(b.w[h][r][i], scale), acc[r]);
                     }
                 } else {
                     const v4u ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
                     const v4f none = {0.f, 0.f, 0.f, 0.f};
-                    constexpr int CPG = GROUP / 32;    // chunks per group
-                    v4f sum[MT][PER];
+                    constexpr int CPG = GROUP / 32;    // matrix-core steps per group
+                    v4f sum[PER];
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            b.x[t][i] = order_u4(b.x[t][i]);
-                            sum[t][i / CPG] = mfma_bf16(b.x[t][i], ones, i % CPG ? sum[t][i / CPG] : none);
-                        }
+                    for (int i = 0; i < 4; ++i) sum[i / CPG] = mfma_bf16(x[i], ones, i % CPG ? sum[i / CPG] : none);
 #pragma unroll
                     for (int r = 0; r < RN; ++r) {
-                        transpose4(b.w[r]);
-                        v4f g[MT];
+                        v4u wt = b.w[h][r];
+                        transpose4(wt);
+                        v4f g;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const v4u w = decode_u4(b.w[r][i]);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) g[t] = mfma_bf16(b.x[t][i], w, i % CPG ? g[t] : none);
+                            g = mfma_bf16(x[i], decode_u4(wt[i]), i % CPG ? g : none);
                             if (i % CPG != CPG - 1) continue;
-                            const int gi = i / CPG;
+                            const int gi = h * PER + i / CPG;      // group within the pair
                             uint32_t s, z = 8;
-                            if constexpr (WIDE) {
+                            if constexpr (PAIR) {
                                 s = gi % 2 ? b.s[r][gi / 2] & 0xFFFF0000u : b.s[r][gi / 2] << 16;
-                                if constexpr (ZEROS) z = (b.z[r][0] >> (8 * gi)) & 0xFFu;
+                                if constexpr (ZEROS) z = (b.z[r][gi / 4] >> (8 * (gi % 4))) & 0xFFu;
                             } else {
-                                s = b.s[r][i] << 16;
-                                if constexpr (ZEROS) z = b.z[r][i];
+                                s = b.s[r][gi] << 16;
+                                if constexpr (ZEROS) z = b.z[r][gi];
                             }
                             const float scale = __uint_as_float(s), shift = -(16.0f + (float)z);
 #pragma unroll
-                            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    acc[t][r][q] = __builtin_fmaf(scale, __builtin_fmaf(shift, sum[t][gi][q], g[t][q]), acc[t][r][q]);
+                            for (int q = 0; q < 4; ++q)
+                                acc[r][q] = __builtin_fmaf(scale, __builtin_fmaf(shift, sum[i / CPG][q], g[q]), acc[r][q]);
                         }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);       // interleaving steps costs registers that waves need
             };
 
-            // steps past the end read zeros (a step's loads are past the buffers), so the ring
-            // needs no other end than the count
-            const int mine = (steps - wave + kWaves - 1) / kWaves;
+            // Rounds of the ring: it is refilled pair by pair for the next round, or the wave's next tile.
+            // Where X takes several chunks, the next one's values are asked for ahead of the last refills of
+            // the present one, so that waiting for them does not empty the ring.
+            const int rounds = (steps + CS - 1) / CS;
+            auto pair_step = [&](int u) { return (ALONE ? u : u * kWaves + wave) * 2; };
+            int tile = ALONE ? tile0 + wave : tile0;
+            int u0 = thread();
+            fetch(0, u0);
 #pragma unroll
-            for (int u = 0; u < PD; ++u) load(ring[u], wave + u * kWaves);
-            for (int i = 0; i < mine; i += PD) {
-#pragma unroll
-                for (int u = 0; u < PD; ++u) {
-                    compute(ring[u]);
-                    load(ring[u], wave + (i + u + PD) * kWaves);
-                    // keep the slots apart: interleaving them costs the registers that waves need
-                    __builtin_amdgcn_sched_barrier(0);
+            for (int u = 0; u < PP; ++u) load(ring[u], pair_step(u), min(tile, tile_end) * kTileRows);
+            stage(u0);
+            if constexpr (!MULTI)
+                for (u0 += XU * kThreads; u0 < here * row_units; u0 += XU * kThreads) {
+                    fetch(0, u0);
+                    stage(u0);
                 }
-            }
-
-            // the waves' sums, added in wave order
+            lds_barrier();
+            int first = 0;                               // step of the chunk in LDS
+            for (; tile < tile_end; tile += kWaves) {
+                const int n0 = tile * kTileRows;
 #pragma unroll
-            for (int b0 = 0; b0 < RN * MT; b0 += kBatch) {
+                for (int r = 0; r < RN; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int g = 0; g < rounds; ++g) {
+                    const int base = g * CS;
+                    const bool last = g + 1 == rounds;
+                    const bool more = MULTI && !last && base + CS == first + chunk;
+                    if constexpr (MULTI) {
+                        if (more) fetch(base + CS, thread());
+                    }
+                    if (!last || (ALONE && tile + kWaves < tile_end)) {
+                        const int next = last ? 0 : base + CS, next_n0 = last ? n0 + kWaves * kTileRows : n0;
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) red[wave][b][lane] = acc[(b0 + b) / RN][(b0 + b) % RN];
-                __syncthreads();
-                for (int o = tid; o < (SWIGLU ? 256 : kBatch * 256); o += kW4Threads) {
-                    const int b = o >> 8, n = o & 15, m = (o >> 4) & 15;
-                    auto total = [&](int tile) {
-                        float v = 0.0f;
-#pragma unroll
-                        for (int w = 0; w < kWaves; ++w) v += red[w][tile][(m >> 2) * 16 + n][m & 3];
-                        return v;
-                    };
-                    float v;
-                    if constexpr (SWIGLU) {
-                        const float gate = total(0), up = total(kBatch - 1);
-                        v = gate * __builtin_amdgcn_rcpf(1.0f + exp_f32(-gate)) * up;
+                        for (int u = 0; u < PP; ++u) {
+                            const int step = base + pair_step(u);
+                            if (step < steps) compute(ring[u], 0, step - first);
+                            if (step + 1 < steps) compute(ring[u], 1, step + 1 - first);
+                            load(ring[u], next + pair_step(u), next_n0);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     } else {
-                        v = total(b);
+#pragma unroll
+                        for (int u = 0; u < PP; ++u) {
+                            const int step = base + pair_step(u);
+                            if (step < steps) compute(ring[u], 0, step - first);
+                            if (step + 1 < steps) compute(ring[u], 1, step + 1 - first);
+                        }
                     }
-                    const int t = (b0 + b) / RN, r = SWIGLU ? 0 : (b0 + b) % RN;
-                    const int nn = n0 + r * 16 + n, mm = m0 + t * 16 + m;
-                    if (nn < n_end && (MODE == kOne ? mm < a.M : mm < ncols)) {
-                        const int64_t row = MODE == kOne ? mm : cols[mm];
-                        a.Y[row * a.nout + nn] = f32_to_bf16(v);
+                    if constexpr (MULTI) {
+                        if (more) {
+                            lds_barrier();               // the chunk has been read
+                            stage(thread());
+                            lds_barrier();
+                            first = base + CS;
+                        }
                     }
                 }
-                __syncthreads();
+
+                auto finish = [&](int m, int n, float v, float up) {
+                    if constexpr (SWIGLU) v = v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v)) * up;
+                    const int64_t row = MODE == kOne ? (int64_t)blockIdx.y * 16 + m : cols[m0 + m];
+                    a.Y[row * a.nout + n0 + n] = f32_to_bf16(v);
+                };
+                if constexpr (ALONE) {
+#pragma unroll
+                    for (int r = 0; r < (SWIGLU ? 1 : RN); ++r)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (j * 4 + q < here && n0 + r * 16 + ln < n_end)
+                                finish(j * 4 + q, r * 16 + ln, acc[r][q], acc[RN - 1][q]);
+                } else {
+                    // the waves' sums, added in wave order
+                    lds_barrier();
+#pragma unroll
+                    for (int r = 0; r < RN; ++r)
+                        if (j * 4 < here) red[wave][r][lane] = acc[r];
+                    lds_barrier();
+                    for (int o = thread(); o < kTileRows * 16; o += kThreads) {
+                        const int n = o % kTileRows, m = o / kTileRows;
+                        if (n0 + n >= n_end || m >= here) continue;
+                        auto total = [&](int r) {
+                            float v = 0.0f;
+#pragma unroll
+                            for (int w = 0; w < kWaves; ++w) v += red[w][r][(m >> 2) * 16 + (n & 15)][m & 3];
+                            return v;
+                        };
+                        finish(m, n, total(SWIGLU ? 0 : n >> 4), SWIGLU ? total(1) : 0.0f);
+                    }
+                    break;                               // one tile
+                }
             }
             if constexpr (MODE == kOne) break;
+            __syncthreads();                             // LDS and the list are used again
         }
-        if constexpr (MODE != kOne) __syncthreads();   // the next window resets the list
+        if constexpr (MODE != kOne) __syncthreads();
         window += kW4MaxPairsBySlot;
     } while (MODE != kOne && !a.by_slot && window < a.pairs);
 }
 
-template <int RN, int MT, int PD, int MODE, bool Z>
-void launch_int4(const W4Args& a, int group, bool wide, dim3 grid, hipStream_t s) {
-    const dim3 block(kW4Threads);
-    if (group == 32 && wide) hipLaunchKernelGGL((w4_kernel<32, false, true, Z, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else if (group == 32) hipLaunchKernelGGL((w4_kernel<32, false, false, Z, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else if (group == 64 && wide) hipLaunchKernelGGL((w4_kernel<64, false, true, Z, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else if (group == 64) hipLaunchKernelGGL((w4_kernel<64, false, false, Z, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((w4_kernel<128, false, true, Z, RN, MT, PD, MODE>), grid, block, 0, s, a);
+// Workgroups over tiles of V and rows of X (or pairs, or experts).
+template <int GROUP, bool MX, bool PAIR, bool Z, int RN, int PP, bool ALONE, int MODE>
+void launch_one(W4Args a, unsigned y, hipStream_t s) {
+    constexpr int tile_rows = MODE == kExpertsSwiglu ? 16 : 16 * RN;
+    const int steps = (a.K + kStep - 1) / kStep;
+    const int tiles = (a.nout + tile_rows - 1) / tile_rows, per_wg = ALONE ? kWaves * a.tiles_per_wave : 1;
+    const dim3 grid((unsigned)((tiles + per_wg - 1) / per_wg), y), block(kThreads);
+    const size_t red = ALONE ? 0 : (size_t)kWaves * RN * 64 * sizeof(v4f);
+    auto lds = [&](int xsteps) {
+        a.xsteps = xsteps;
+        a.xstride = xsteps * kStep * 2 + 16;         // rows 16 bytes apart in the banks
+        a.div_units = make_fastdiv((uint32_t)(xsteps * (kStep / 8)));
+        return std::max((size_t)a.cols * a.xstride, red);
+    };
+    if constexpr (!ALONE) {
+        if (a.cols * steps > kXSteps) {
+            // INT4 has fewer registers for X's values on their way: half the chunk and the ring
+            constexpr int PM = MX ? PP : (PP + 1) / 2, room = MX ? kXSteps : kXSteps / 2, round = kWaves * PM * 2;
+            static_assert(room / (RN == 1 ? 4 : 16) >= round, "X's chunk has room for a round");
+            const size_t bytes = lds(room / a.cols / round * round);
+            hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, PM, ALONE, true, MODE>), grid, block, bytes, s, a);
+            return;
+        }
+    }
+    const size_t bytes = lds(steps);
+    hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, PP, ALONE, false, MODE>), grid, block, bytes, s, a);
 }
 
-template <int RN, int MT, int PD, int MODE>
-void launch_mode(const W4Args& a, int group, bool mxfp4, dim3 grid, hipStream_t s) {
-    const dim3 block(kW4Threads);
-    const bool wide = a.K % kStep == 0;
-    if (mxfp4 && wide) hipLaunchKernelGGL((w4_kernel<32, true, true, false, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else if (mxfp4) hipLaunchKernelGGL((w4_kernel<32, true, false, false, RN, MT, PD, MODE>), grid, block, 0, s, a);
-    else if (a.zeros) launch_int4<RN, MT, PD, MODE, true>(a, group, wide, grid, s);
-    else launch_int4<RN, MT, PD, MODE, false>(a, group, wide, grid, s);
+// Scales that take more registers (groups of 32, or a load per group) leave room for half the pairs in flight.
+template <int RN, int PP, bool ALONE, int MODE, bool Z>
+void launch_int4(const W4Args& a, int group, unsigned y, hipStream_t s) {
+    constexpr int PH = (PP + 1) / 2;
+    // a pair's scales are 16, 8 or 4 bytes, its zero points 8, 4 or 2, at that many bytes' alignment (at most 4)
+    const bool pair = a.K % (group == 32 || (group == 64 && !Z) ? 128 : 256) == 0;
+    if (group == 32 && pair) launch_one<32, false, true, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else if (group == 32) launch_one<32, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else if (group == 64 && pair) launch_one<64, false, true, Z, RN, PP, ALONE, MODE>(a, y, s);
+    else if (group == 64) launch_one<64, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else if (pair) launch_one<128, false, true, Z, RN, PP, ALONE, MODE>(a, y, s);
+    else launch_one<128, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+}
+
+// PP: pairs in flight of MXFP4, PI of INT4.
+template <int RN, int PP, int PI, bool ALONE, int MODE>
+void launch_mode(const W4Args& a, int group, bool mxfp4, unsigned y, hipStream_t s) {
+    if (mxfp4 && a.K % kStep == 0) launch_one<32, true, true, false, RN, PP, ALONE, MODE>(a, y, s);
+    else if (mxfp4) launch_one<32, true, false, false, RN, PP, ALONE, MODE>(a, y, s);
+    else if (a.zeros) launch_int4<RN, PI, ALONE, MODE, true>(a, group, y, s);
+    else launch_int4<RN, PI, ALONE, MODE, false>(a, group, y, s);
 }
 
 }  // namespace
 
-void launch_w4(const W4Args& a, int group, bool mxfp4, int, hipStream_t s) {
-    auto grid = [&](int rn, int mt) {
-        return dim3((unsigned)((a.N + 16 * rn - 1) / (16 * rn)), (unsigned)((a.M + 16 * mt - 1) / (16 * mt)));
-    };
-    if (a.M <= 16) launch_mode<1, 1, 4, kOne>(a, group, mxfp4, grid(1, 1), s);
-    else launch_mode<2, 2, 2, kOne>(a, group, mxfp4, grid(2, 2), s);
+void launch_w4(const W4Args& a, int rn, int group, bool mxfp4, hipStream_t s) {
+    const unsigned y = (unsigned)((a.M + 15) / 16);
+    if (a.tiles_per_wave > 0) launch_mode<1, 4, 4, true, kOne>(a, group, mxfp4, y, s);
+    else if (rn == 1) launch_mode<1, 4, 4, false, kOne>(a, group, mxfp4, y, s);
+    else launch_mode<2, 2, 2, false, kOne>(a, group, mxfp4, y, s);
 }
 
-void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, int, hipStream_t s) {
-    const unsigned slots = a.by_slot ? a.pairs : a.E + 1;
-    if (swiglu) launch_mode<2, 1, 2, kExpertsSwiglu>(a, group, mxfp4, dim3((unsigned)((a.half + 15) / 16), slots), s);
-    else launch_mode<1, 1, 4, kExperts>(a, group, mxfp4, dim3((unsigned)((a.N + 15) / 16), slots), s);
+// (INT4 with the experts' bookkeeping has registers for one pair in flight and two workgroups per CU: us, 8
+// pairs of 4096 x 7168 with SwiGLU, groups of 64 with zero points, one pair 39, two with spills 43, two in
+// one workgroup per CU 46)
+void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, hipStream_t s) {
+    const unsigned y = a.by_slot ? a.pairs : a.E + 1;
+    if (swiglu && a.tiles_per_wave > 0) launch_mode<2, 2, 2, true, kExpertsSwiglu>(a, group, mxfp4, y, s);
+    else if (swiglu) launch_mode<2, 2, 1, false, kExpertsSwiglu>(a, group, mxfp4, y, s);
+    else if (a.tiles_per_wave > 0) launch_mode<1, 4, 4, true, kExperts>(a, group, mxfp4, y, s);
+    else launch_mode<2, 2, 1, false, kExperts>(a, group, mxfp4, y, s);
 }
 
 }  // namespace fp8gemm
