@@ -33,6 +33,7 @@ struct RouteArgs {
     int64_t T;
     int32_t E, k;
     int32_t n_group, topk_group, group_top, group_size;
+    int32_t group_lanes;        // lanes whose chunks make up a group, 0 if a group is not 1, 2, 4 or 8 chunks
     int32_t renorm;
     float scale;
 };

@@ -5,10 +5,13 @@
 // Sixteen lanes, one DPP row, own one token: reductions over a token are four cross-lane steps
 // without LDS, four tokens advance together in every instruction of a wave, and no work is
 // shared between waves.  The choice values of a token stand in LDS as 16 chunks of V consecutive
-// experts.  A pick is a two-level tournament: the best chunk maximum (one per lane), then the V
-// values of that chunk (one or a few per lane); both levels find the lowest index that equals
-// the maximum with a ballot, so ties go to the lowest index.
+// experts, chunk l read back by lane l.  A pick is a two-level tournament: the best chunk maximum
+// (one per lane), then the V values of that chunk (one or a few per lane); both levels find the
+// lowest index that equals the maximum with a ballot, so ties go to the lowest index.  Groups of
+// whole chunks take their scores from the chunks' two best values, merged across the group's
+// lanes, and strike out whole chunk maxima; other groups are scanned in LDS, a lane each.
 
+#include "fp8gemm_device.h"
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -18,8 +21,9 @@ namespace {
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kBig = 3.402823466e38f;
 
-// NaN counts as -infinity, +infinity as the largest finite value.
-__device__ __forceinline__ float clean(float x) { return x != x ? kNegInf : fminf(x, kBig); }
+// NaN counts as -infinity, +infinity as the largest finite value (the maximum of NaN and a number
+// is the number).
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, kNegInf), kBig); }
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -29,18 +33,79 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
-// Lowest set bit of the 16 bits of `ballot` that belong to DPP row `row` (16 if none).
-__device__ __forceinline__ int first_in_row(uint64_t ballot, int row) {
-    return __builtin_ctz(((uint32_t)(ballot >> (row * 16)) & 0xFFFFu) | 0x10000u);
+// Choice values (not -0) as integers that order as they do: the cross-lane steps of integer maxima
+// are single instructions.
+constexpr int kLowest = (int)0x807FFFFFu;   // of -infinity
+__device__ __forceinline__ int key_of(float x) {
+    const int b = __float_as_int(x);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ int row16_max_i(int v) {
+    v = max(v, dpp16<kDppXor1>(v));
+    v = max(v, dpp16<kDppXor2>(v));
+    v = max(v, dpp16<kDppHalfMirror>(v));
+    v = max(v, dpp16<kDppMirror>(v));
+    return v;
 }
 
-// V: values per lane and chunk length (E <= 16 V); WAVES * 4 tokens per workgroup.
-template <bool BF16, bool SIGMOID, int V, int WAVES>
+// Lowest lane of DPP row `row` whose bit of the ballot is set (16 if none).
+__device__ __forceinline__ int first_in_row(uint64_t ballot, int row) {
+    const uint32_t half = row & 2 ? (uint32_t)(ballot >> 32) : (uint32_t)ballot;
+    return __builtin_ctz((half >> (row & 1) * 16) | 0x10000u);
+}
+
+// (m1, m2), the two largest of this lane's and its partner's two largest values.
+template <int CTRL>
+__device__ __forceinline__ void merge_top2(int& m1, int& m2) {
+    const int o1 = dpp16<CTRL>(m1), o2 = dpp16<CTRL>(m2);
+    m2 = max(max(min(m1, o1), m2), o2);
+    m1 = max(m1, o1);
+}
+
+// A lane's share of a row of E values: V values in runs of P consecutive ones (P = 1 without
+// vector loads), run i at (16 i + l) P, so that a row's 16 lanes read consecutive memory.
+template <int V, int P>
+__device__ __forceinline__ int element(int i, int l) { return (i / P * 16 + l) * P + i % P; }
+
+// The lane's values of a row of logits, -infinity past E.
+template <bool BF16, int V, int P>
+__device__ __forceinline__ void load_row(const void* logits, int64_t base, int E, int l, float (&s)[V]) {
+    // (loaded and cleaned without branches: past the end a run repeats the last, and then gives way)
+#pragma unroll
+    for (int i = 0; i < V; i += P) {
+        const int in = min(element<V, P>(i, l), E - P);   // a run is in or out as a whole
+        if constexpr (BF16) {
+            uint16_t x[P];
+            __builtin_memcpy(x, __builtin_assume_aligned(static_cast<const uint16_t*>(logits) + base + in, 2 * P), 2 * P);
+#pragma unroll
+            for (int q = 0; q < P; ++q) s[i + q] = clean(bf16_to_f32(x[q]));
+        } else {
+            float x[P];
+            __builtin_memcpy(x, __builtin_assume_aligned(static_cast<const float*>(logits) + base + in, 4 * P), 4 * P);
+#pragma unroll
+            for (int q = 0; q < P; ++q) s[i + q] = clean(x[q]);
+        }
+    }
+    if (E < 16 * V) {
+#pragma unroll
+        for (int i = 0; i < V; i += P) {
+            const bool out = element<V, P>(i, l) >= E;
+#pragma unroll
+            for (int q = 0; q < P; ++q) s[i + q] = out ? kNegInf : s[i + q];
+        }
+    }
+}
+
+// V: values per lane and chunk length (E <= 16 V); P: values per load (E a multiple of it, rows
+// aligned to a run); WAVES * 4 tokens per workgroup.
+template <bool BF16, bool SIGMOID, int V, int P, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     // chunk stride in floats: 16-byte aligned, and 16 lanes reading their chunks 16 bytes at a
-    // time touch every bank group once
-    constexpr int CS = V < 4 ? V : V + 4;
-    __shared__ float lds_c[WAVES * 4][16 * CS];
+    // time touch every bank group once; tokens a quarter of the banks apart
+    constexpr int CS = V + 4, ROW = 16 * CS + 16;
+    __shared__ __align__(16) int lds_c[WAVES * 4][ROW];
     __shared__ float lds_g[WAVES * 4][kRouteMaxGroups];
     const int lane = threadIdx.x & 63, row = lane >> 4, l = lane & 15;
     const int slot = (threadIdx.x >> 6) * 4 + row;
@@ -48,130 +113,171 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     const bool live = token < a.T;
     const int64_t tok = live ? token : a.T - 1;   // rows past the end repeat the last token and store nothing
     const int64_t base = tok * a.E;
-    float* c = lds_c[slot];
+    int* c = lds_c[slot];
     auto at = [](int e) { return (e / V) * CS + (e & (V - 1)); };
 
-    // scores and choice values, lane-strided so that a row's loads are consecutive
-    float s[V];
-    float m = kNegInf;
+    float bias[V];   // (asked for first: the same for every token, from the caches)
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 16 + l;
-        s[i] = e < a.E ? load_logit<BF16>(a.logits, base + e) : kNegInf;
-        m = fmaxf(m, s[i]);
+        for (int i = 0; i < V; i += P)
+            __builtin_memcpy(bias + i, __builtin_assume_aligned(a.bias + min(element<V, P>(i, l), a.E - P), 4 * P), 4 * P);
     }
+    float s[V];
+    load_row<BF16, V, P>(a.logits, base, a.E, l, s);
+
     // scores: sigmoid(x), or exp(x - m) * inv with m and inv = 1 / sum of the token's softmax; the sum
     // is formed only where scores are used as such (a renormalised weight cancels it)
-    float inv = 1.0f;
+    float m = 0.0f, inv = 1.0f;
     if constexpr (!SIGMOID) {
+        m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = fmaxf(m, s[i]);
         m = row16_max_f(m);
         if (m == kNegInf) m = 0.0f;   // a row with no finite logit: every score is 0
         if (!a.renorm || a.bias || (a.n_group > 1 && a.group_top == 2)) {
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += s[i] == kNegInf ? 0.0f : exp_f32(s[i] - m);
+            for (int i = 0; i < V; ++i) sum += exp_f32(s[i] - m);   // e^-infinity is 0
             sum = row16_sum_f(sum);
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         }
     }
     auto score = [&](float x) { return SIGMOID ? sigmoid_f32(x) : exp_f32(x - m) * inv; };
     // choice values: score + bias; without a bias the logits, which order as the scores do and stay
-    // apart where scores round to the same value
+    // apart where scores round to the same value.  The score in them is formed by the hardware's 2^x alone:
+    // the argument's rounding, |x| 2^-24, moves a sigmoid by s (1 - s) times that and a probability by s
+    // times it, under 2e-8 for every x, less than the sum's own rounding.
+    constexpr float kLog2e = 1.44269504088896341f;
+    auto choice_score = [&](float x) {
+        if constexpr (SIGMOID) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+        else return __builtin_amdgcn_exp2f((x - m) * kLog2e) * inv;
+    };
+    int key[V];
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 16 + l;
-        float v = s[i];
-        if (a.bias && e < a.E && v != kNegInf) v = score(v) + clean(a.bias[e]);
-        c[at(e)] = v;
+        for (int i = 0; i < V; ++i)   // (0 times a logit of -infinity makes the sum NaN, and that -infinity; never -0)
+            key[i] = key_of(clean(__builtin_fmaf(s[i], 0.0f, choice_score(s[i]) + bias[i])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = key_of(s[i] + 0.0f);   // -0 as 0
     }
+    constexpr int PW = P < 4 ? P : 4;   // values per LDS store
+#pragma unroll
+    for (int i = 0; i < V; i += PW)
+        __builtin_memcpy(__builtin_assume_aligned(c + at(element<V, P>(i, l)), 4 * PW), key + i, 4 * PW);
     wave_sync();
 
-    // groups: the sum of each one's best (or best two) choice values, kept if fewer than
-    // topk_group others are better (or as good with a lower index)
-    uint64_t keep = ~0ull;
+    // this lane's chunk: its two largest values
+    int m1 = kLowest, m2 = kLowest;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int v = c[l * CS + i];
+        m2 = max(m2, min(m1, v));
+        m1 = max(m1, v);
+    }
+    int cm = m1;   // the best of the chunk that can be picked
+
     if (a.n_group > 1) {
+        // groups: the sum of each one's best (or best two) choice values, kept if fewer than topk_group
+        // others are better (or as good with a lower index)
         float* gs = lds_g[slot];
-        for (int g = l; g < a.n_group; g += 16) {
-            float m1 = kNegInf, m2 = kNegInf;
-            for (int q = 0; q < a.group_size; ++q) {
-                const float v = c[at(g * a.group_size + q)];
-                m2 = fmaxf(m2, fminf(m1, v));
-                m1 = fmaxf(m1, v);
-            }
+        auto group_score = [&](int k1, int k2) {
             // (without a bias the sum is of scores; a single largest one orders as its logit)
-            gs[g] = a.group_top == 1 ? m1 : m2 == kNegInf ? kNegInf : a.bias ? m1 + m2 : score(m1) + score(m2);
+            const float b1 = value_of(k1), b2 = value_of(k2);
+            return a.group_top == 1 ? b1 : k2 == kLowest ? kNegInf : a.bias ? b1 + b2 : score(b1) + score(b2);
+        };
+        const int lanes = a.group_lanes;          // 16-lane rows: lanes per group, 0 if groups are not whole chunks
+        if (lanes) {
+            if (lanes > 1) merge_top2<kDppXor1>(m1, m2);
+            if (lanes > 2) merge_top2<kDppXor2>(m1, m2);
+            if (lanes > 4) merge_top2<kDppHalfMirror>(m1, m2);
+            if (l % lanes == 0 && l / lanes < a.n_group) gs[l / lanes] = group_score(m1, m2);
+        } else {
+            for (int g = l; g < a.n_group; g += 16) {
+                int b1 = kLowest, b2 = kLowest;
+#pragma unroll 8
+                for (int q = 0; q < a.group_size; ++q) {
+                    const int v = c[at(g * a.group_size + q)];
+                    b2 = max(b2, min(b1, v));
+                    b1 = max(b1, v);
+                }
+                gs[g] = group_score(b1, b2);
+            }
         }
         wave_sync();
-        keep = 0;
+        uint64_t keep = 0;
         for (int g0 = 0; g0 < a.n_group; g0 += 16) {
             const int g = g0 + l;
             const float mine = g < a.n_group ? gs[g] : kNegInf;
             int better = 0;
+#pragma unroll 8
             for (int h = 0; h < a.n_group; ++h) {
                 const float o = gs[h];
-                better += (o > mine || (o == mine && h < g)) ? 1 : 0;
+                better += (int)(o > mine) | ((int)(o == mine) & (int)(h < g));
             }
             const uint64_t b = __ballot(g < a.n_group && better < a.topk_group);
             keep |= ((b >> (row * 16)) & 0xFFFFull) << g0;
         }
-    }
-
-    // chunk maxima, with the groups that were not kept struck out
-    float cm = kNegInf;
-    {
-        int g = a.n_group > 1 ? l * V / a.group_size : 0;
-        int left = a.n_group > 1 ? a.group_size - (l * V - g * a.group_size) : 1 << 30;
+        if (lanes) {
+            if (!((keep >> (l / lanes)) & 1)) cm = kLowest;
+        } else {
+            cm = kLowest;
+            int g = l * V / a.group_size, left = a.group_size - (l * V - g * a.group_size);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float v = c[l * CS + i];
-            if (a.n_group > 1) {
+            for (int i = 0; i < V; ++i) {
                 if (left == 0) { ++g; left = a.group_size; }
                 --left;
-                if (g < a.n_group && !((keep >> g) & 1)) {
-                    v = kNegInf;
-                    c[l * CS + i] = v;
-                }
+                // (past the last group the shift wraps: those values are the lowest anyway)
+                const int v = (keep >> (g & 63)) & 1 ? c[l * CS + i] : kLowest;
+                c[l * CS + i] = v;
+                cm = max(cm, v);
             }
-            cm = fmaxf(cm, v);
+            wave_sync();
         }
     }
-    wave_sync();
 
-    // k picks; lane j keeps pick j, and pick 16 + j
-    int pick0 = -1, pick1 = -1;
-    for (int j = 0; j < a.k; ++j) {
-        const float best = row16_max_f(cm);
+    // k picks; lane j keeps pick j (index and choice value), and pick 16 + j
+    int pick0 = -1, pick1 = -1, key0 = kLowest, key1 = kLowest;
+    auto pick_next = [&](int j, int& pick, int& key) {
+        const int best = row16_max_i(cm);
         const int w = first_in_row(__ballot(cm == best), row);
-        int found = V;
-        float next = kNegInf;
+        int found = 0, next = kLowest;
+        bool open = true;
 #pragma unroll
         for (int q = 0; q < (V + 15) / 16; ++q) {
-            const int i = q * 16 + l;
-            float v = (V >= 16 || i < V) ? c[w * CS + i] : kNegInf;
-            const int f = first_in_row(__ballot((V >= 16 || i < V) && v == best), row);
-            if (found == V && f < 16) {
-                found = q * 16 + f;
-                if (l == f) {
-                    c[w * CS + i] = kNegInf;
-                    v = kNegInf;
-                }
+            const int i = V >= 16 ? q * 16 + l : l & (V - 1);    // (short chunks: copies of the values, the lowest lane wins)
+            int v = c[w * CS + i];
+            const int f = first_in_row(__ballot(v == best), row);
+            if constexpr (V <= 16) {
+                found = f;
+                v = (l & (V - 1)) == f ? kLowest : v;
+            } else {
+                const bool hit = open && f < 16;
+                found = hit ? q * 16 + f : found;
+                v = hit && l == f ? kLowest : v;
+                open = open && !hit;
             }
-            next = fmaxf(next, v);
+            c[w * CS + i] = v;
+            next = max(next, v);
         }
-        next = row16_max_f(next);
-        if (l == w) cm = next;
-        if (l == (j & 15)) {
-            const int e = best > kNegInf ? w * V + found : -1;
-            if (j < 16) pick0 = e;
-            else pick1 = e;
-        }
+        next = row16_max_i(next);
+        cm = l == w ? next : cm;
+        const bool keep_it = l == j;
+        pick = keep_it ? w * V + found : pick;
+        key = keep_it ? best : key;
         wave_sync();
-    }
+    };
+    for (int j = 0; j < min(a.k, 16); ++j) pick_next(j, pick0, key0);
+    for (int j = 16; j < a.k; ++j) pick_next(j - 16, pick1, key1);
+    if (key0 == kLowest) pick0 = -1;      // nothing left to choose
+    if (key1 == kLowest) pick1 = -1;
 
     // weights: the picked experts' scores without the bias
-    float w0 = 0.0f, w1 = 0.0f;
-    if (l < a.k && pick0 >= 0) w0 = score(load_logit<BF16>(a.logits, base + pick0));
-    if (16 + l < a.k && pick1 >= 0) w1 = score(load_logit<BF16>(a.logits, base + pick1));
+    auto weight = [&](int pick, int key) {
+        if (pick < 0) return 0.0f;
+        return score(a.bias ? load_logit<BF16>(a.logits, base + pick) : value_of(key));
+    };
+    const float w0 = weight(pick0, key0), w1 = a.k > 16 ? weight(pick1, key1) : 0.0f;
     float f = a.scale;
     if (a.renorm) {
         const float sum = row16_sum_f(w0 + w1);
@@ -191,9 +297,9 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
 
 // Gradient of the weights with respect to the logits.  Renormalised weights, and sigmoid scores,
 // depend on the picked experts' logits alone; softmax scores as they are depend on every logit.
-template <bool BF16, bool SIGMOID, int V, int WAVES>
+template <bool BF16, bool SIGMOID, int V, int P, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwardArgs a) {
-    __shared__ float lds_d[WAVES * 4][16 * V];
+    __shared__ __align__(16) float lds_d[WAVES * 4][16 * V];
     const int lane = threadIdx.x & 63, row = lane >> 4, l = lane & 15;
     const int slot = (threadIdx.x >> 6) * 4 + row;
     const int64_t token = (int64_t)blockIdx.x * (WAVES * 4) + slot;
@@ -203,7 +309,7 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
     const bool dense = !SIGMOID && !a.renorm;
     float* d = lds_d[slot];
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i * 16 + l] = 0.0f;
+    for (int i = 0; i < V; ++i) d[element<V, P>(i, l)] = 0.0f;
 
     // this lane's picks (l and 16 + l): index, logit and incoming gradient
     int id[2];
@@ -219,18 +325,15 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
     float s[V];
     float m, sum = 0.0f;
     if (dense) {
+        load_row<BF16, V, P>(a.logits, base, a.E, l, s);
         m = kNegInf;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 16 + l;
-            s[i] = e < a.E ? load_logit<BF16>(a.logits, base + e) : kNegInf;
-            m = fmaxf(m, s[i]);
-        }
+        for (int i = 0; i < V; ++i) m = fmaxf(m, s[i]);
         m = row16_max_f(m);
         if (m == kNegInf) m = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[i] = s[i] == kNegInf ? 0.0f : exp_f32(s[i] - m);
+            s[i] = exp_f32(s[i] - m);   // e^-infinity is 0
             sum += s[i];
         }
         sum = row16_sum_f(sum);
@@ -270,33 +373,71 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
     }
     if (!live) return;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 16 + l;
-        if (e < a.E) {
-            float v = d[e];
-            if (dense) v = (v - mean) * (s[i] * r);
-            if constexpr (BF16) static_cast<uint16_t*>(a.dlogits)[base + e] = f32_to_bf16(v);
-            else static_cast<float*>(a.dlogits)[base + e] = v;
+    for (int i = 0; i < V; i += P) {
+        const int e = element<V, P>(i, l);
+        if (e >= a.E) continue;
+        float v[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            v[q] = d[e + q];
+            if (dense) v[q] = (v[q] - mean) * (s[i + q] * r);
+        }
+        if constexpr (BF16) {
+            uint16_t* out = static_cast<uint16_t*>(a.dlogits) + base + e;
+            if constexpr (P == 1) {
+                *out = f32_to_bf16(v[0]);
+            } else {
+                typedef uint32_t Words __attribute__((ext_vector_type(P / 2)));
+                Words w;
+#pragma unroll
+                for (int q = 0; q < P / 2; ++q) w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+                *reinterpret_cast<Words*>(out) = w;
+            }
+        } else {
+            typedef float Words __attribute__((ext_vector_type(P)));
+            Words w;
+#pragma unroll
+            for (int q = 0; q < P; ++q) w[q] = v[q];
+            *reinterpret_cast<Words*>(static_cast<float*>(a.dlogits) + base + e) = w;
         }
     }
 }
 
-template <int V, int WAVES>
-void launch_forward(const RouteArgs& a, bool bf16, bool sigmoid, hipStream_t s) {
+template <int V, int WAVES, bool BF16, int P>
+void launch_forward(const RouteArgs& a, bool sigmoid, hipStream_t s) {
     const dim3 grid((unsigned)((a.T + WAVES * 4 - 1) / (WAVES * 4))), block(WAVES * 64);
-    if (bf16 && sigmoid) hipLaunchKernelGGL((route_topk_kernel<true, true, V, WAVES>), grid, block, 0, s, a);
-    else if (bf16) hipLaunchKernelGGL((route_topk_kernel<true, false, V, WAVES>), grid, block, 0, s, a);
-    else if (sigmoid) hipLaunchKernelGGL((route_topk_kernel<false, true, V, WAVES>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((route_topk_kernel<false, false, V, WAVES>), grid, block, 0, s, a);
+    if (sigmoid) hipLaunchKernelGGL((route_topk_kernel<BF16, true, V, P, WAVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((route_topk_kernel<BF16, false, V, P, WAVES>), grid, block, 0, s, a);
+}
+
+template <int V, int WAVES, bool BF16, int P>
+void launch_back(const RouteBackwardArgs& a, bool sigmoid, hipStream_t s) {
+    const dim3 grid((unsigned)((a.T + WAVES * 4 - 1) / (WAVES * 4))), block(WAVES * 64);
+    if (sigmoid) hipLaunchKernelGGL((route_backward_kernel<BF16, true, V, P, WAVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((route_backward_kernel<BF16, false, V, P, WAVES>), grid, block, 0, s, a);
+}
+
+// Vector loads (16 bytes, 8 for 64 bf16 experts) where every row is aligned to them.
+template <int V, int WAVES>
+void launch_forward(RouteArgs a, bool bf16, bool sigmoid, hipStream_t s) {
+    constexpr int PB = V < 8 ? V : 8;
+    const int lanes = a.group_size / V;
+    a.group_lanes = a.group_size % V == 0 && (lanes == 1 || lanes == 2 || lanes == 4 || lanes == 8) ? lanes : 0;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias);
+    if (bf16 && a.E % PB == 0 && at % 16 == 0) launch_forward<V, WAVES, true, PB>(a, sigmoid, s);
+    else if (bf16) launch_forward<V, WAVES, true, 1>(a, sigmoid, s);
+    else if (a.E % 4 == 0 && at % 16 == 0) launch_forward<V, WAVES, false, 4>(a, sigmoid, s);
+    else launch_forward<V, WAVES, false, 1>(a, sigmoid, s);
 }
 
 template <int V, int WAVES>
 void launch_back(const RouteBackwardArgs& a, bool bf16, bool sigmoid, hipStream_t s) {
-    const dim3 grid((unsigned)((a.T + WAVES * 4 - 1) / (WAVES * 4))), block(WAVES * 64);
-    if (bf16 && sigmoid) hipLaunchKernelGGL((route_backward_kernel<true, true, V, WAVES>), grid, block, 0, s, a);
-    else if (bf16) hipLaunchKernelGGL((route_backward_kernel<true, false, V, WAVES>), grid, block, 0, s, a);
-    else if (sigmoid) hipLaunchKernelGGL((route_backward_kernel<false, true, V, WAVES>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((route_backward_kernel<false, false, V, WAVES>), grid, block, 0, s, a);
+    constexpr int PB = V < 8 ? V : 8;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits);
+    if (bf16 && a.E % PB == 0 && at % (2 * PB) == 0) launch_back<V, WAVES, true, PB>(a, sigmoid, s);
+    else if (bf16) launch_back<V, WAVES, true, 1>(a, sigmoid, s);
+    else if (a.E % 4 == 0 && at % 16 == 0) launch_back<V, WAVES, false, 4>(a, sigmoid, s);
+    else launch_back<V, WAVES, false, 1>(a, sigmoid, s);
 }
 
 }  // namespace
