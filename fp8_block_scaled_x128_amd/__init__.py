@@ -491,40 +491,51 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 
 def _call(fn, device, stream, *args):
     """One C call on torch's current stream of `device` (or `stream`)."""
-    torch = _torch()
+    c = _cuda()
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(device)
+        s = c._cuda_getCurrentRawStream(device)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     f = getattr(_lib or lib(), fn)
-    if device == torch._C._cuda_getDevice():
+    if device == c._cuda_getDevice():
         st = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with _torch().cuda.device(device):
             st = f(*args, s)
     if st != 0:
         raise Fp8GemmError(st, fn)
 
 
+def _cuda():
+    """torch's C module (the current stream and device without the Python layers above it)."""
+    global _torch_c
+    if _torch_c is None:
+        _torch_c = _torch()._C
+    return _torch_c
+
+
+_torch_c = None
+
+
 def _take(t, dtype, shape, device, name):
     """Address of a contiguous device tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.get_device() != device:
         raise ValueError("%s must be a tensor of device %d" % (name, device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _device_of(t, dims, name):
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions" % (name, dims))
     d = t.get_device()
     if d < 0:
         raise ValueError("%s must be a device tensor" % name)
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions" % (name, dims))
     return d
 
 

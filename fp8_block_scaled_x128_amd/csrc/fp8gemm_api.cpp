@@ -10,7 +10,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -64,6 +63,23 @@ const std::vector<KernelEntry>& kernels() {
 }
 std::atomic<int> g_cu_cap{0};
 thread_local char g_last_config[256] = "";
+
+// The last configuration of an operator whose calls are short: put into words when asked for.
+constexpr int kConfigValues = 8;
+struct PendingConfig {
+    const char* fmt = nullptr;             // %lld for each value
+    long long v[kConfigValues] = {};
+};
+thread_local PendingConfig g_pending;
+
+const char* last_config() {
+    if (g_pending.fmt) {
+        const long long* v = g_pending.v;
+        std::snprintf(g_last_config, sizeof g_last_config, g_pending.fmt, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        g_pending.fmt = nullptr;
+    }
+    return g_last_config;
+}
 
 // Query the device once: CU count, occupancy of every kernel, the device addresses of the
 // static error word and scratch.  Allocates nothing.
@@ -421,6 +437,7 @@ int launch(int layout, KernelArgs& a, int64_t expected_rows, hipStream_t stream,
     int64_t grid = streamk ? slots : std::min<int64_t>(a.units, slots);
     if (grid <= 0) return FP8GEMM_OK;
     const char* lname = layout == kDense ? "nt" : (layout == kContiguous ? "contiguous" : (fp4 ? "masked fp8xfp4" : "masked"));
+    g_pending.fmt = nullptr;
     if (e.kind == kKindStream)
         std::snprintf(g_last_config, sizeof g_last_config,
                       "%s stream tile=%dx%d waves=%d jn=%d phase=%d depth=%d split=%d kb_per_split=%d "
@@ -500,6 +517,7 @@ int quantize(const void* X, void* A, float* sa, const int32_t* masked_m, int32_t
     q.div_rows = make_fastdiv((uint32_t)rows);
     const int64_t wgs = (blocks + kQuantBlocksPerWG - 1) / kQuantBlocksPerWG;
     const int64_t grid = (wgs + 7) / 8 * 8;
+    g_pending.fmt = nullptr;
     std::snprintf(g_last_config, sizeof g_last_config, "%s blocks_per_wg=%d grid=%lld",
                   swiglu ? "swiglu_quantize_1x128" : "quantize_1x128", kQuantBlocksPerWG, (long long)grid);
     if (swiglu) launch_swiglu_quantize(q, dim3((unsigned)grid), stream);
@@ -558,12 +576,12 @@ int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch) {
     return FP8GEMM_OK;
 }
 
-void host_set_config(const char* fmt, ...) {
-    va_list args;
-    va_start(args, fmt);
-    std::vsnprintf(g_last_config, sizeof g_last_config, fmt, args);
-    va_end(args);
-    if (std::getenv("FP8GEMM_LOG")) std::fprintf(stderr, "[fp8gemm] %s\n", g_last_config);
+void host_set_config(const char* fmt, std::initializer_list<long long> values) {
+    g_pending.fmt = fmt;
+    int n = 0;
+    for (long long v : values)
+        if (n < kConfigValues) g_pending.v[n++] = v;
+    if (std::getenv("FP8GEMM_LOG")) std::fprintf(stderr, "[fp8gemm] %s\n", last_config());
 }
 
 }  // namespace fp8gemm
@@ -829,7 +847,7 @@ int fp8gemm_set_num_cus(int n) {
 
 int fp8gemm_last_config(char* buf, int len) {
     if (!buf || len <= 0) return FP8GEMM_ERR_NULL_PTR;
-    std::snprintf(buf, (size_t)len, "%s", g_last_config);
+    std::snprintf(buf, (size_t)len, "%s", last_config());
     return FP8GEMM_OK;
 }
 

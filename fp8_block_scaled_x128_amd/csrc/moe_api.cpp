@@ -64,8 +64,11 @@ int dispatch(DispatchArgs a, hipStream_t stream) {
         if (st != FP8GEMM_OK) return st;
         a.scratch = static_cast<int32_t*>(p);
     }
-    host_set_config("moe_dispatch_%s pairs=%d experts=%d %s", a.contiguous ? "contiguous" : "masked", a.pairs, a.G,
-                    large ? "count+scan+copy" : "one launch");
+    host_set_config(a.contiguous ? (large ? "moe_dispatch_contiguous pairs=%lld experts=%lld count+scan+copy"
+                                          : "moe_dispatch_contiguous pairs=%lld experts=%lld one launch")
+                                 : (large ? "moe_dispatch_masked pairs=%lld experts=%lld count+scan+copy"
+                                          : "moe_dispatch_masked pairs=%lld experts=%lld one launch"),
+                    {a.pairs, a.G});
     launch_dispatch(a, large, stream);
     return launched();
 }
@@ -146,7 +149,7 @@ int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, floa
     a.group_size = size;
     a.renorm = renorm != 0;
     a.scale = scale;
-    host_set_config("route_topk T=%lld E=%d k=%d groups=%d/%d", (long long)T, E, k, topk_group, n_group);
+    host_set_config("route_topk T=%lld E=%lld k=%lld groups=%lld/%lld", {T, E, k, topk_group, n_group});
     launch_route_topk(a, dtype == FP8GEMM_BF16, score == FP8GEMM_SCORE_SIGMOID, static_cast<hipStream_t>(stream));
     return launched();
 }
@@ -171,7 +174,7 @@ int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const fl
     a.k = k;
     a.renorm = renorm != 0;
     a.scale = scale;
-    host_set_config("route_topk_backward T=%lld E=%d k=%d", (long long)T, E, k);
+    host_set_config("route_topk_backward T=%lld E=%lld k=%lld", {T, E, k});
     launch_route_backward(a, dtype == FP8GEMM_BF16, score == FP8GEMM_SCORE_SIGMOID, static_cast<hipStream_t>(stream));
     return launched();
 }
@@ -252,7 +255,7 @@ int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_
     a.H = (int32_t)H;
     a.k = k;
     a.err = d.err;
-    host_set_config("moe_combine T=%lld k=%d H=%lld", (long long)T, k, (long long)H);
+    host_set_config("moe_combine T=%lld k=%lld H=%lld", {T, k, H});
     launch_combine(a, static_cast<hipStream_t>(stream));
     return launched();
 }
@@ -281,7 +284,7 @@ int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* w
     a.H = (int32_t)H;
     a.k = k;
     a.err = d.err;
-    host_set_config("moe_combine_backward T=%lld k=%d H=%lld", (long long)T, k, (long long)H);
+    host_set_config("moe_combine_backward T=%lld k=%lld H=%lld", {T, k, H});
     launch_combine_backward(a, static_cast<hipStream_t>(stream));
     return launched();
 }
@@ -315,8 +318,9 @@ int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint
     // share X's LDS traffic (and a short row's exchange: 1 x 7168 x 2048 5.7 and 5.1)
     const int rn = a.cols > 4 || K < 4096 ? 2 : 1;
     a.tiles_per_wave = w4_tiles_per_wave(N, K, a.cols, (M + 15) / 16, d.cus);
-    host_set_config("w4_gemv %s group=%d M=%lld N=%lld K=%lld rn=%d tiles_per_wave=%d", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
-                    group, (long long)M, (long long)N, (long long)K, rn, a.tiles_per_wave);
+    host_set_config(format == FP8GEMM_W4_MXFP4 ? "w4_gemv mxfp4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld"
+                                               : "w4_gemv int4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld",
+                    {group, M, N, K, rn, a.tiles_per_wave});
     launch_w4(a, rn, group, format == FP8GEMM_W4_MXFP4, s);
     return launched();
 }
@@ -362,8 +366,10 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
     a.cols = (int32_t)std::min<int64_t>(std::min<int64_t>(T, 16), 4 + 2 * ((a.pairs + E - 1) / E));
     const int64_t busy = std::min<int64_t>(a.pairs, E);
     a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.cus);
-    host_set_config("w4_gemv_experts %s group=%d pairs=%d N=%lld K=%lld tiles_per_wave=%d by %s", format == FP8GEMM_W4_MXFP4 ? "mxfp4" : "int4",
-                    group, a.pairs, (long long)N, (long long)K, a.tiles_per_wave, a.by_slot ? "pair" : "expert");
+    host_set_config(format == FP8GEMM_W4_MXFP4
+                        ? "w4_gemv_experts mxfp4 group=%lld pairs=%lld N=%lld K=%lld tiles_per_wave=%lld by_pair=%lld"
+                        : "w4_gemv_experts int4 group=%lld pairs=%lld N=%lld K=%lld tiles_per_wave=%lld by_pair=%lld",
+                    {group, a.pairs, N, K, a.tiles_per_wave, a.by_slot});
     launch_w4_experts(a, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, static_cast<hipStream_t>(stream));
     return launched();
 }

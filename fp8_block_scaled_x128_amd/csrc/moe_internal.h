@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "fp8gemm_args.h"
 
 namespace fp8gemm {
@@ -18,7 +20,8 @@ struct HostDevice {
 int host_device(HostDevice* out);                                       // status code
 // The stream's library-owned workspace (see fp8gemm.h): `bytes` of scratch, status code.
 int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch);
-void host_set_config(const char* fmt, ...) __attribute__((format(printf, 1, 2)));
+// The calling thread's last configuration: a static format of %lld fields and at most 8 values.
+void host_set_config(const char* fmt, std::initializer_list<long long> values);
 
 // ---- routing ----
 constexpr int kRouteMaxExperts = 1024;

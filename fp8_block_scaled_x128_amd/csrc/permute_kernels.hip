@@ -69,11 +69,16 @@ __device__ __forceinline__ int place(const DispatchArgs& a, int e, int rank, int
     return rank < a.cap && (!a.contiguous || row < a.cap) ? (int)row : -1;
 }
 
-// Quantise span `s` of token t's row and store it in the rows[0..k) that are not -1.
-__device__ __forceinline__ void copy_span(const DispatchArgs& a, int64_t t, int s, const int* rows) {
+// A thread's 8 values of span `s` of token t's row (asked for before the rows are known).
+__device__ __forceinline__ v4u load_span(const DispatchArgs& a, int64_t t, int s) {
+    const int col = s * kSpan + threadIdx.x * 8;
+    return *reinterpret_cast<const v4u*>(a.X + t * a.H + min(col, a.H - 8));
+}
+
+// Quantise them and store them in the rows[0..k) that are not -1.
+__device__ __forceinline__ void store_span(const DispatchArgs& a, int s, const v4u& c, const int* rows) {
     const int col = s * kSpan + threadIdx.x * 8;
     if (col >= a.H) return;              // the 16 lanes of a 128-value block leave together
-    const v4u c = *reinterpret_cast<const v4u*>(a.X + t * a.H + col);
     float scale;
     const uint2 q = quantize8(c, &scale);
     const int kb = col >> 7;
@@ -112,6 +117,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     __shared__ int rows[kDispatchMaxTopk], mine[kDispatchMaxTopk];
     const int64_t t = blockIdx.x / spans;
     const int s = blockIdx.x - (int)t * spans;
+    const v4u c = load_span(a, t, s);
     for (int e = threadIdx.x; e < a.G; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
     const int p0 = (int)t * a.k;
@@ -160,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         }
     }
     __syncthreads();
-    copy_span(a, t, s, rows);
+    store_span(a, s, c, rows);
 }
 
 // Scratch of the large path, in words.
@@ -290,6 +296,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_copy_kernel(DispatchArgs a,
     const Scratch sc = scratch_of(a);
     const int64_t t = blockIdx.x / spans;
     const int s = (int)(blockIdx.x - t * spans);
+    const v4u c = load_span(a, t, s);
     if (threadIdx.x < a.k) {
         const int p = (int)(t * a.k) + threadIdx.x;
         const int e = local_expert(a, p);
@@ -305,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_copy_kernel(DispatchArgs a,
     __syncthreads();
     if (s == 0 && a.contiguous)
         fill_indices(a, t, [&](int e) { return sc.first[e]; }, [&](int e) { return sc.total[e]; });
-    copy_span(a, t, s, rows);
+    store_span(a, s, c, rows);
 }
 
 // ---- combine ----
