@@ -59,8 +59,11 @@ int dispatch(DispatchArgs a, hipStream_t stream) {
     if (large) {
         a.chunks = (a.pairs + kDispatchChunk - 1) / kDispatchChunk;
         const size_t words = (size_t)a.G * a.chunks + 2 * (size_t)a.G + (size_t)a.pairs;
+        const size_t rows = (size_t)(a.contiguous ? 1 : a.G) * a.cap;
         void* p = nullptr;
-        st = host_stream_scratch(stream, words * sizeof(int32_t), &p);
+        // the turned scales where their scratch fits the workspace
+        a.by_row = host_stream_scratch(stream, (words + (size_t)a.T * a.nkb + rows) * sizeof(int32_t), &p) == FP8GEMM_OK;
+        if (!a.by_row) st = host_stream_scratch(stream, words * sizeof(int32_t), &p);
         if (st != FP8GEMM_OK) return st;
         a.scratch = static_cast<int32_t*>(p);
     }

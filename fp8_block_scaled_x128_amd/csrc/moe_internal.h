@@ -73,6 +73,7 @@ struct DispatchArgs {
     int32_t contiguous;
     int32_t pairs;              // T * k
     int32_t chunks;             // large batches: ceil(pairs / kDispatchChunk)
+    int32_t by_row;             // large batches: scales by token in scratch, turned round by a pass of their own
     FastDiv div_k;
 };
 

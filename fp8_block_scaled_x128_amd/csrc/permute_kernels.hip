@@ -6,7 +6,9 @@
 // The rank of a pair (token t, pick j) among its expert's rows is the number of earlier pairs, in
 // (t, j) order, with the same expert, so the layout does not depend on timing.  Small batches
 // recompute the ranks in every workgroup of the one copying launch; large ones count chunks of
-// pairs, scan the counts and then copy, in three launches.
+// pairs, scan the counts, copy, and put the scales in place, in four launches.
+
+#include <algorithm>
 
 #include "fp8gemm_device.h"
 #include "moe_device.h"
@@ -15,8 +17,8 @@
 namespace fp8gemm {
 namespace {
 
-// Workgroup size and elements per thread of every row pass: 16 lanes own a 128-value block, as
-// 16 bytes of bf16 per lane, so a wave's load is 1 KB of consecutive memory.
+// Workgroup size of the row passes with 16 bytes of bf16 per thread: 16 lanes own a 128-value block, and
+// a wave's load is 1 KB of consecutive memory.
 constexpr int kThreads = 256;
 constexpr int kSpan = kThreads * 8;      // elements of a row one workgroup handles per pass
 
@@ -28,30 +30,45 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, x), r, q), x);
 }
 
-// The 1x128 quantiser on 8 bf16 values of a lane (16 lanes a block): 8 codes and the scale.
-__device__ __forceinline__ uint2 quantize8(const v4u& c, float* scale) {
+// The 1x128 quantiser on 8 C bf16 values of a lane (16 / C lanes a block): codes and the scale.
+template <int C>
+struct Codes {
+    typedef uint32_t Words __attribute__((ext_vector_type(2 * C)));
+    Words w;
+    float scale;
+};
+template <int C>
+__device__ __forceinline__ Codes<C> quantize(const v4u (&x)[C]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(c[i] & 0x7FFFu, (c[i] >> 16) & 0x7FFFu));
+    for (int h = 0; h < C; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(x[h][i] & 0x7FFFu, (x[h][i] >> 16) & 0x7FFFu));
     // bit patterns of |x| order like the values
     m = max(m, (uint32_t)dpp16<kDppXor1>((int)m));
     m = max(m, (uint32_t)dpp16<kDppXor2>((int)m));
     m = max(m, (uint32_t)dpp16<kDppHalfMirror>((int)m));
-    m = max(m, (uint32_t)dpp16<kDppMirror>((int)m));
+    if constexpr (C == 1) m = max(m, (uint32_t)dpp16<kDppMirror>((int)m));
     const float s = fmaxf(__uint_as_float(m << 16), 1e-4f) / 448.0f;
     const float r = 1.0f / s;
-    float v[8];
+    Codes<C> o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __builtin_amdgcn_fmed3f(quotient(__uint_as_float(c[i] << 16), s, r), -448.0f, 448.0f);
-        v[2 * i + 1] = __builtin_amdgcn_fmed3f(quotient(__uint_as_float(c[i] & 0xFFFF0000u), s, r), -448.0f, 448.0f);
+    for (int h = 0; h < C; ++h) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __builtin_amdgcn_fmed3f(quotient(__uint_as_float(x[h][i] << 16), s, r), -448.0f, 448.0f);
+            v[2 * i + 1] = __builtin_amdgcn_fmed3f(quotient(__uint_as_float(x[h][i] & 0xFFFF0000u), s, r), -448.0f, 448.0f);
+        }
+        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+        o.w[2 * h] = (uint32_t)lo;
+        o.w[2 * h + 1] = (uint32_t)hi;
     }
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-    *scale = s;
-    return make_uint2((uint32_t)lo, (uint32_t)hi);
+    o.scale = s;
+    return o;
 }
 
 // Local expert of a pair, or -1 (no pick, or another rank's expert).
@@ -69,27 +86,28 @@ __device__ __forceinline__ int place(const DispatchArgs& a, int e, int rank, int
     return rank < a.cap && (!a.contiguous || row < a.cap) ? (int)row : -1;
 }
 
-// A thread's 8 values of span `s` of token t's row (asked for before the rows are known).
-__device__ __forceinline__ v4u load_span(const DispatchArgs& a, int64_t t, int s) {
-    const int col = s * kSpan + threadIdx.x * 8;
-    return *reinterpret_cast<const v4u*>(a.X + t * a.H + min(col, a.H - 8));
-}
-
-// Quantise them and store them in the rows[0..k) that are not -1.
-__device__ __forceinline__ void store_span(const DispatchArgs& a, int s, const v4u& c, const int* rows) {
-    const int col = s * kSpan + threadIdx.x * 8;
-    if (col >= a.H) return;              // the 16 lanes of a 128-value block leave together
-    float scale;
-    const uint2 q = quantize8(c, &scale);
-    const int kb = col >> 7;
+// Store a lane's codes at column `col` of the rows[0..k) that are not -1, past the caches (nothing reads
+// them before the next product).
+template <int C>
+__device__ __forceinline__ void store_codes(const DispatchArgs& a, int col, const Codes<C>& q, const int* rows) {
     for (int j = 0; j < a.k; ++j) {
         const int row = rows[j];
-        if (row < 0) continue;
-        *reinterpret_cast<uint2*>(a.A + (int64_t)row * a.H + col) = q;
-        if ((threadIdx.x & 15) == 0) {
-            const int e = a.contiguous ? 0 : row / a.cap;
-            a.sa[((int64_t)e * a.nkb + kb) * a.cap + (row - (int64_t)e * a.cap)] = scale;
-        }
+        if (row >= 0)
+            __builtin_nontemporal_store(q.w, reinterpret_cast<typename Codes<C>::Words*>(a.A + (int64_t)row * a.H + col));
+    }
+}
+
+// Address of the scale of row `row`, K block kb (K-block-major per group).
+__device__ __forceinline__ float* scale_at(const DispatchArgs& a, int row, int kb) {
+    const int e = a.contiguous ? 0 : row / a.cap;
+    return a.sa + ((int64_t)e * a.nkb + kb) * a.cap + (row - (int64_t)e * a.cap);
+}
+
+// Scales of K blocks kb0 .. kb0 + blocks from LDS to the rows, a lane each.
+__device__ __forceinline__ void store_scales(const DispatchArgs& a, int kb0, int blocks, const int* rows, const float* scales) {
+    for (int i = threadIdx.x; i < blocks * a.k; i += blockDim.x) {
+        const int kb = (int)fast_div(i, a.div_k), pick = i - kb * a.k;
+        if (rows[pick] >= 0) *scale_at(a, rows[pick], kb0 + kb) = scales[kb];
     }
 }
 
@@ -99,7 +117,7 @@ template <typename First, typename Count>
 __device__ __forceinline__ void fill_indices(const DispatchArgs& a, int64_t t, First first, Count count) {
     const int64_t per = (a.cap + a.T - 1) / a.T;
     const int64_t end = min((t + 1) * per, (int64_t)a.cap);
-    for (int64_t r = t * per + threadIdx.x; r < end; r += kThreads) {
+    for (int64_t r = t * per + threadIdx.x; r < end; r += blockDim.x) {
         int lo = 0, hi = a.G;            // the last expert whose first row is not past r
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -115,9 +133,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     __shared__ int all[kDispatchMaxGroups], before[kDispatchMaxGroups];
     __shared__ int first[kDispatchMaxGroups + 1];
     __shared__ int rows[kDispatchMaxTopk], mine[kDispatchMaxTopk];
+    __shared__ float scales[kSpan / 128];
     const int64_t t = blockIdx.x / spans;
     const int s = blockIdx.x - (int)t * spans;
-    const v4u c = load_span(a, t, s);
+    // a thread's 8 values are asked for before their rows are known
+    const int col = s * kSpan + threadIdx.x * 8;
+    const v4u x[1] = {*reinterpret_cast<const v4u*>(a.X + t * a.H + min(col, a.H - 8))};
     for (int e = threadIdx.x; e < a.G; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
     const int p0 = (int)t * a.k;
@@ -166,7 +187,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         }
     }
     __syncthreads();
-    store_span(a, s, c, rows);
+    const Codes<1> q = quantize(x);
+    if (col < a.H) {                     // the 16 lanes of a 128-value block are in or out together
+        store_codes(a, col, q, rows);
+        if ((threadIdx.x & 15) == 0) scales[threadIdx.x >> 4] = q.scale;
+    }
+    __syncthreads();
+    store_scales(a, s * (kSpan / 128), min(kSpan / 128, a.nkb - s * (kSpan / 128)), rows, scales);
 }
 
 // Scratch of the large path, in words.
@@ -175,6 +202,8 @@ struct Scratch {
     int32_t* first;    // [G]: first row (contiguous)
     int32_t* total;    // [G]
     int32_t* local;    // [pairs]: rank within the chunk
+    float* scales;     // by_row: [T][nkb]
+    int32_t* token;    // by_row: the token of each row of the layout that has one
 };
 __device__ __forceinline__ Scratch scratch_of(const DispatchArgs& a) {
     Scratch s;
@@ -182,6 +211,8 @@ __device__ __forceinline__ Scratch scratch_of(const DispatchArgs& a) {
     s.first = s.counts + (int64_t)a.G * a.chunks;
     s.total = s.first + a.G;
     s.local = s.total + a.G;
+    s.scales = reinterpret_cast<float*>(s.local + a.pairs);
+    s.token = s.local + a.pairs + a.T * a.nkb;
     return s;
 }
 
@@ -242,22 +273,30 @@ __global__ __launch_bounds__(1024) void dispatch_scan_kernel(DispatchArgs a) {
     __shared__ int total[kDispatchMaxGroups];
     const Scratch sc = scratch_of(a);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = wave; e < a.G; e += 16) {
-        int carry = 0;
-        int32_t* row = sc.counts + (int64_t)e * a.chunks;
+    constexpr int kBatch = 4;            // experts a wave scans side by side, their loads in flight together
+    for (int e0 = wave * kBatch; e0 < a.G; e0 += 16 * kBatch) {
+        int carry[kBatch] = {0, 0, 0, 0};
         for (int c0 = 0; c0 < a.chunks; c0 += 64) {
             const int c = c0 + lane;
-            const int n = c < a.chunks ? row[c] : 0;
-            int sum = n;
+            int n[kBatch];
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int up = __shfl_up(sum, o, 64);
-                if (lane >= o) sum += up;
+            for (int i = 0; i < kBatch; ++i)
+                n[i] = e0 + i < a.G && c < a.chunks ? sc.counts[(int64_t)(e0 + i) * a.chunks + c] : 0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                int sum = n[i];
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    const int up = __shfl_up(sum, o, 64);
+                    if (lane >= o) sum += up;
+                }
+                if (e0 + i < a.G && c < a.chunks) sc.counts[(int64_t)(e0 + i) * a.chunks + c] = carry[i] + sum - n[i];
+                carry[i] += __shfl(sum, 63, 64);
             }
-            if (c < a.chunks) row[c] = carry + sum - n;
-            carry += __shfl(sum, 63, 64);
         }
-        if (lane == 0) total[e] = carry;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (lane == 0 && e0 + i < a.G) total[e0 + i] = carry[i];
     }
     __syncthreads();
     if (wave == 0) {
@@ -291,12 +330,22 @@ __global__ __launch_bounds__(kThreads) void dispatch_empty_kernel(int32_t* where
     if (i < n) where[i] = value;
 }
 
-__global__ __launch_bounds__(kThreads) void dispatch_copy_kernel(DispatchArgs a, int spans) {
+// A workgroup per token, 16 values a thread.  A token's scattered scales (4 bytes each, a row apart) would
+// cost as much as a third of its codes, so with by_row they are kept token by token, for
+// dispatch_scales_kernel to turn round.
+__global__ __launch_bounds__(1024) void dispatch_copy_kernel(DispatchArgs a) {
     __shared__ int rows[kDispatchMaxTopk];
+    __shared__ float scales[128];
     const Scratch sc = scratch_of(a);
-    const int64_t t = blockIdx.x / spans;
-    const int s = (int)(blockIdx.x - t * spans);
-    const v4u c = load_span(a, t, s);
+    const int64_t t = blockIdx.x;
+    v4u x[2];
+    auto load = [&](int col) {
+        const v4u* p = reinterpret_cast<const v4u*>(a.X + t * a.H + min(col, a.H - 16));
+        x[0] = p[0];
+        x[1] = p[1];
+    };
+    int col = threadIdx.x * 16;
+    load(col);                           // before the rows are known
     if (threadIdx.x < a.k) {
         const int p = (int)(t * a.k) + threadIdx.x;
         const int e = local_expert(a, p);
@@ -304,15 +353,63 @@ __global__ __launch_bounds__(kThreads) void dispatch_copy_kernel(DispatchArgs a,
         if (e >= 0) {
             const int rank = sc.counts[(int64_t)e * a.chunks + p / kDispatchChunk] + sc.local[p];
             row = place(a, e, rank, sc.first[e]);
-            if (row < 0 && s == 0) atomicOr(a.err, (int32_t)kDevErrBadCount);
+            if (row < 0) atomicOr(a.err, (int32_t)kDevErrBadCount);
         }
         rows[threadIdx.x] = row;
-        if (s == 0) a.row_map[p] = row;
+        a.row_map[p] = row;
+        if (a.by_row && row >= 0) sc.token[row] = (int32_t)t;
     }
     __syncthreads();
-    if (s == 0 && a.contiguous)
-        fill_indices(a, t, [&](int e) { return sc.first[e]; }, [&](int e) { return sc.total[e]; });
-    store_span(a, s, c, rows);
+    if (a.contiguous) fill_indices(a, t, [&](int e) { return sc.first[e]; }, [&](int e) { return sc.total[e]; });
+    for (int col0 = 0; col0 < a.H; col0 += blockDim.x * 16, col += blockDim.x * 16) {
+        if (col0) load(col);
+        const Codes<2> q = quantize(x);
+        const int kb0 = col0 / 128;
+        float* keep = a.by_row ? sc.scales + t * a.nkb + kb0 : scales;
+        if (col < a.H) {                 // the 8 lanes of a 128-value block are in or out together
+            store_codes(a, col, q, rows);
+            if ((threadIdx.x & 7) == 0) keep[threadIdx.x >> 3] = q.scale;
+        }
+        if (!a.by_row) {
+            __syncthreads();
+            store_scales(a, kb0, min((int)blockDim.x / 8, a.nkb - kb0), rows, scales);
+            __syncthreads();
+        }
+    }
+}
+
+// Scales of 64 rows of the layout and 32 K blocks: read token by token, turned round in LDS, written
+// K block by K block.
+constexpr int kTurnRows = 64, kTurnBlocks = 32;
+__global__ __launch_bounds__(kThreads) void dispatch_scales_kernel(DispatchArgs a) {
+    __shared__ float tile[kTurnRows][kTurnBlocks + 1];
+    const Scratch sc = scratch_of(a);
+    const int tiles = (a.cap + kTurnRows - 1) / kTurnRows;       // per group of the masked layout
+    const int e = a.contiguous ? 0 : blockIdx.x / tiles;
+    const int r0 = (blockIdx.x - e * tiles) * kTurnRows, kb0 = blockIdx.y * kTurnBlocks;
+    const int valid = a.contiguous ? a.cap : a.where[e];
+    if (r0 >= valid) return;
+    auto there = [&](int r) { return r < valid && (!a.contiguous || a.where[r] >= 0); };
+    constexpr int kPass = kThreads / kTurnBlocks, kRows = kTurnRows / kPass;
+    const int kb = threadIdx.x % kTurnBlocks, r1 = threadIdx.x / kTurnBlocks;
+    int token[kRows];                                            // the loads of a step are in flight together
+    float v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + r1 + i * kPass;
+        token[i] = there(r) ? sc.token[(int64_t)e * a.cap + r] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        v[i] = token[i] >= 0 && kb0 + kb < a.nkb ? sc.scales[(int64_t)token[i] * a.nkb + kb0 + kb] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) tile[r1 + i * kPass][kb] = v[i];
+    __syncthreads();
+    const int r = threadIdx.x % kTurnRows;
+    if (!there(r0 + r)) return;
+#pragma unroll
+    for (int b = threadIdx.x / kTurnRows; b < kTurnBlocks; b += kThreads / kTurnRows)
+        if (kb0 + b < a.nkb) a.sa[((int64_t)e * a.nkb + kb0 + b) * a.cap + r0 + r] = tile[r][b];
 }
 
 // ---- combine ----
@@ -440,7 +537,13 @@ void launch_dispatch(const DispatchArgs& a, bool large, hipStream_t s) {
     }
     hipLaunchKernelGGL(dispatch_count_kernel, dim3((unsigned)a.chunks), dim3(kThreads), 0, s, a);
     hipLaunchKernelGGL(dispatch_scan_kernel, dim3(1), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL(dispatch_copy_kernel, grid, dim3(kThreads), 0, s, a, spans);
+    const int threads = std::min(1024, (a.H / 16 + 63) / 64 * 64);
+    hipLaunchKernelGGL(dispatch_copy_kernel, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, a);
+    if (a.by_row) {
+        const int64_t tiles = (int64_t)(a.contiguous ? 1 : a.G) * ((a.cap + kTurnRows - 1) / kTurnRows);
+        const dim3 turn((unsigned)tiles, (unsigned)((a.nkb + kTurnBlocks - 1) / kTurnBlocks));
+        if (tiles > 0) hipLaunchKernelGGL(dispatch_scales_kernel, turn, dim3(kThreads), 0, s, a);
+    }
 }
 
 void launch_combine(const CombineArgs& a, hipStream_t s) {
