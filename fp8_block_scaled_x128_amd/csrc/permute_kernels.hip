@@ -20,6 +20,7 @@ namespace {
 // Workgroup size of the row passes with 16 bytes of bf16 per thread: 16 lanes own a 128-value block, and
 // a wave's load is 1 KB of consecutive memory.
 constexpr int kThreads = 256;
+constexpr int64_t kCacheBytes = 256 << 20;   // the memory-side cache
 constexpr int kSpan = kThreads * 8;      // elements of a row one workgroup handles per pass
 
 // Correctly rounded x / s for one E4M3 conversion: with r = RN(1/s) and q = RN(x r), one
@@ -422,7 +423,10 @@ __device__ __forceinline__ int64_t pair_row(const CombineArgs& a, int64_t t, int
 }
 
 // out[t] = sum_j w[t][j] Y[row(t, j)], in fp32 in the order of j.  Memory bound: each thread owns
-// 16 bytes of the output and keeps the loads of several rows in flight.
+// 16 bytes of the output and keeps the loads of 8 rows in flight.  STREAM: Y is larger than the
+// memory-side cache and is read past the caches (us, with and without: 4096 x 8 x 7168, 470 MB, 104 and 111,
+// 5.05 and 4.75 TB/s; 128 x 8 x 7168 with Y in the cache 8.3 and 6.8).
+template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a, int spans) {
     const int64_t t = blockIdx.x / spans;
     const int s = (int)(blockIdx.x - t * spans);
@@ -431,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a, int sp
         atomicOr(a.err, (int32_t)kDevErrBadIndex);
     if (col >= a.H) return;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    constexpr int kDeep = 4;
+    constexpr int kDeep = 8;
     for (int j0 = 0; j0 < a.k; j0 += kDeep) {
         v4u y[kDeep];
         float w[kDeep];
@@ -442,7 +446,9 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a, int sp
             if (j0 + i < a.k) {
                 const int64_t r = pair_row(a, t, j0 + i);
                 if (r >= 0) {
-                    y[i] = *reinterpret_cast<const v4u*>(a.Y + r * a.H + col);
+                    const v4u* p = reinterpret_cast<const v4u*>(a.Y + r * a.H + col);
+                    if constexpr (STREAM) y[i] = __builtin_nontemporal_load(p);
+                    else y[i] = *p;
                     w[i] = a.weights ? a.weights[t * a.k + j0 + i] : 1.0f;
                 }
             }
@@ -548,7 +554,9 @@ void launch_dispatch(const DispatchArgs& a, bool large, hipStream_t s) {
 
 void launch_combine(const CombineArgs& a, hipStream_t s) {
     const int spans = spans_of(a.H);
-    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(a.T * spans)), dim3(kThreads), 0, s, a, spans);
+    const dim3 grid((unsigned)(a.T * spans));
+    if (2 * a.T * a.k * a.H > kCacheBytes) hipLaunchKernelGGL(combine_kernel<true>, grid, dim3(kThreads), 0, s, a, spans);
+    else hipLaunchKernelGGL(combine_kernel<false>, grid, dim3(kThreads), 0, s, a, spans);
 }
 
 void launch_combine_backward(const CombineArgs& a, hipStream_t s) {
