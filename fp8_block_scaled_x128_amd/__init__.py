@@ -485,65 +485,83 @@ def moe_expert_masked(A, sa, W1, s1, W2, s2, masked_m, expected_m: int, out=None
 
 
 # ---- expert routing, token permutation, 4-bit matrix-vector products ---------------------------
+#
+# These calls take a few microseconds, so their tensors go to the C ABI through the compiled module
+# `_native`, which checks them as it reads them.  A refusal there (-1) is put into words here.
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_native_module = None
 
 
-def _call(fn, device, stream, *args):
-    """One C call on torch's current stream of `device` (or `stream`)."""
-    c = _cuda()
+def _calls():
+    global _native_module
+    if _native_module is None:
+        import torch  # noqa: F401  (the module needs torch's libraries in the process)
+        if not os.path.exists(os.path.join(_HERE, "_native.so")):
+            raise RuntimeError("_native.so is not built (python -m fp8_block_scaled_x128_amd.build)")
+        from . import _native as module
+        _native_module = module
+    return _native_module
+
+
+def _handle(stream):
+    """None (the current stream) or a stream's address."""
     if stream is None:
-        s = c._cuda_getCurrentRawStream(device)
-    else:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    f = getattr(_lib or lib(), fn)
-    if device == c._cuda_getDevice():
-        st = f(*args, s)
-    else:
-        with _torch().cuda.device(device):
-            st = f(*args, s)
-    if st != 0:
-        raise Fp8GemmError(st, fn)
+        return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _cuda():
-    """torch's C module (the current stream and device without the Python layers above it)."""
-    global _torch_c
-    if _torch_c is None:
-        _torch_c = _torch()._C
-    return _torch_c
-
-
-_torch_c = None
-
-
-def _take(t, dtype, shape, device, name):
-    """Address of a contiguous device tensor of this type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.get_device() != device:
-        raise ValueError("%s must be a tensor of device %d" % (name, device))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s must be contiguous" % name)
-
-
-def _device_of(t, dims, name):
-    d = t.get_device()
-    if d < 0:
-        raise ValueError("%s must be a device tensor" % name)
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions" % (name, dims))
-    return d
-
-
-def _logits(logits, device):
+def _new(shape, dtype, like, stream, zero=False):
+    """A new tensor on `like`'s device, allocated (and filled) on the stream that is to write it."""
     torch = _torch()
-    if logits.dtype is torch.float32:
-        return _take(logits, torch.float32, logits.shape, device, "logits"), 0
-    return _take(logits, torch.bfloat16, logits.shape, device, "logits"), 1
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
+def _require(t, name, dtypes, shape, device):
+    """Raise what is wrong with an argument."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor, got %s" % (name, type(t).__name__))
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError("%s must have shape [%s], got %s" % (name, ",".join("*" if s is None else str(s) for s in shape),
+                                                              list(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _refuse(fn, status, *arguments):
+    """Raise for a call that did not succeed: the first argument (tensor, name, types, shape) that is not
+    as the call takes it, or the C call's status.  None stands for any size, and for a tensor left out."""
+    if status > 0:
+        raise Fp8GemmError(status, fn)
+    device = None
+    for t, name, dtypes, shape in arguments:
+        if t is None:
+            continue
+        if device is None:
+            device = getattr(t, "device", None)
+        _require(t, name, dtypes, shape, device)
+    raise ValueError("%s: arguments out of range" % fn)
+
+
+def _dims(t, n, name):
+    """The shape of a tensor of n dimensions."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError("%s must have %d dimensions" % (name, n))
+    return shape
 
 
 def _score(score):
@@ -559,41 +577,43 @@ def route_topk(logits, k: int, bias=None, score="softmax", n_group: int = 1, top
     only the experts of the ``topk_group`` best groups (by the sum of their ``group_top`` largest
     choice values) can be chosen; ``renorm`` divides a token's weights by their sum.  Ties go to the
     lower index; where fewer than k experts can be chosen the rest are id -1, weight 0."""
-    torch = _torch()
-    dev = _device_of(logits, 2, "logits")
-    p, dtype = _logits(logits, dev)
-    T, E = logits.shape
-    pb = None if bias is None else _take(bias, torch.float32, (E,), dev, "bias")
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _call("fp8gemm_route_topk", dev, stream, p, pb, _take(ids, torch.int32, (T, k), dev, "ids"),
-          _take(weights, torch.float32, (T, k), dev, "weights"), T, E, k, dtype, _score(score), n_group, topk_group,
-          group_top, int(renorm), scale)
+    if ids is None or weights is None:
+        torch = _torch()
+        T, _ = _dims(logits, 2, "logits")
+        if ids is None:
+            ids = _new((T, k), torch.int32, logits, stream)
+        if weights is None:
+            weights = _new((T, k), torch.float32, logits, stream)
+    st = _calls().route_topk(logits, bias, ids, weights, k, _score(score), n_group, topk_group, group_top, renorm, scale,
+                              _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, E = _dims(logits, 2, "logits")
+        _refuse("fp8gemm_route_topk", st, (logits, "logits", (torch.float32, torch.bfloat16), (T, E)),
+                (bias, "bias", (torch.float32,), (E,)), (ids, "ids", (torch.int32,), (T, k)),
+                (weights, "weights", (torch.float32,), (T, k)))
     return ids, weights
 
 
 def route_topk_backward(logits, ids, dweights, score="softmax", renorm: bool = True, scale: float = 1.0, dlogits=None,
                         stream=None):
     """Gradient of route_topk's weights: dweights fp32 [T,k] -> dlogits [T,E] of the logits' type."""
-    torch = _torch()
-    dev = _device_of(logits, 2, "logits")
-    p, dtype = _logits(logits, dev)
-    T, E = logits.shape
-    _device_of(ids, 2, "ids")
-    k = ids.shape[1]
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
-    _call("fp8gemm_route_topk_backward", dev, stream, p, _take(ids, torch.int32, (T, k), dev, "ids"),
-          _take(dweights, torch.float32, (T, k), dev, "dweights"), _take(dlogits, logits.dtype, (T, E), dev, "dlogits"),
-          T, E, k, dtype, _score(score), int(renorm), scale)
+        dlogits = _new(_dims(logits, 2, "logits"), logits.dtype, logits, stream)
+    st = _calls().route_topk_backward(logits, ids, dweights, dlogits, _score(score), renorm, scale, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, E = _dims(logits, 2, "logits")
+        k = _dims(ids, 2, "ids")[1]
+        _refuse("fp8gemm_route_topk_backward", st, (logits, "logits", (torch.float32, torch.bfloat16), (T, E)),
+                (ids, "ids", (torch.int32,), (T, k)), (dweights, "dweights", (torch.float32,), (T, k)),
+                (dlogits, "dlogits", (logits.dtype,), (T, E)))
     return dlogits
 
 
-def _code_ptr(t, shape, device, name):
+def _code_types():
     torch = _torch()
-    return _take(t, torch.uint8 if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape, device, name)
+    return (torch.float8_e4m3fn, torch.uint8)
 
 
 def moe_dispatch_masked(X, ids, G: int, M_max: int, first_expert: int = 0, codes=None, scales=None, masked_m=None,
@@ -604,23 +624,23 @@ def moe_dispatch_masked(X, ids, G: int, M_max: int, first_expert: int = 0, codes
     rank's expert, or past M_max).  Rows that no pair goes to are left untouched (zeros when the
     outputs are allocated here)."""
     torch = _torch()
-    dev = _device_of(X, 2, "X")
-    T, H = X.shape
-    _device_of(ids, 2, "ids")
-    k = ids.shape[1]
-    if codes is None:
-        codes = torch.zeros((G, M_max, H), dtype=torch.uint8, device=X.device).view(torch.float8_e4m3fn)
-    if scales is None:
-        scales = torch.zeros((G, H // 128, M_max), dtype=torch.float32, device=X.device)
-    if masked_m is None:
-        masked_m = torch.empty((G,), dtype=torch.int32, device=X.device)
-    if row_map is None:
-        row_map = torch.empty((T, k), dtype=torch.int32, device=X.device)
-    _call("fp8gemm_moe_dispatch_masked", dev, stream, _take(X, torch.bfloat16, (T, H), dev, "X"),
-          _take(ids, torch.int32, (T, k), dev, "ids"), _code_ptr(codes, (G, M_max, H), dev, "codes"),
-          _take(scales, torch.float32, (G, H // 128, M_max), dev, "scales"),
-          _take(masked_m, torch.int32, (G,), dev, "masked_m"), _take(row_map, torch.int32, (T, k), dev, "row_map"),
-          T, H, k, G, M_max, first_expert)
+    if codes is None or scales is None or masked_m is None or row_map is None:
+        H = _dims(X, 2, "X")[1]
+        if codes is None:
+            codes = _new((G, M_max, H), torch.uint8, X, stream, zero=True).view(torch.float8_e4m3fn)
+        if scales is None:
+            scales = _new((G, H // 128, M_max), torch.float32, X, stream, zero=True)
+        if masked_m is None:
+            masked_m = _new((G,), torch.int32, X, stream)
+        if row_map is None:
+            row_map = _new(_dims(ids, 2, "ids"), torch.int32, X, stream)
+    st = _calls().moe_dispatch(X, ids, codes, scales, masked_m, row_map, G, M_max, first_expert, True, _handle(stream))
+    if st != 0:
+        T, H = _dims(X, 2, "X")
+        k = _dims(ids, 2, "ids")[1]
+        _refuse("fp8gemm_moe_dispatch_masked", st, (X, "X", (torch.bfloat16,), (T, H)), (ids, "ids", (torch.int32,), (T, k)),
+                (codes, "codes", _code_types(), (G, M_max, H)), (scales, "scales", (torch.float32,), (G, H // 128, M_max)),
+                (masked_m, "masked_m", (torch.int32,), (G,)), (row_map, "row_map", (torch.int32,), (T, k)))
     return codes, scales, masked_m, row_map
 
 
@@ -631,62 +651,60 @@ def moe_dispatch_contiguous(X, ids, G: int, M_total: int = None, first_expert: i
     expert's rows are padded to a multiple of 128.  M_total None: the rows of ``codes`` or
     ``m_indices`` if given, else room for every pair."""
     torch = _torch()
-    dev = _device_of(X, 2, "X")
-    T, H = X.shape
-    _device_of(ids, 2, "ids")
-    k = ids.shape[1]
     if M_total is None:
         if codes is not None:
-            M_total = codes.shape[0]
+            M_total = _dims(codes, 2, "codes")[0]
         elif m_indices is not None:
-            M_total = m_indices.shape[0]
+            M_total = _dims(m_indices, 1, "m_indices")[0]
         else:
+            T, k = _dims(ids, 2, "ids")
             M_total = -(-(T * k + 127 * min(G, T * k)) // 128) * 128
-    if codes is None:
-        codes = torch.zeros((M_total, H), dtype=torch.uint8, device=X.device).view(torch.float8_e4m3fn)
-    if scales is None:
-        scales = torch.zeros((H // 128, M_total), dtype=torch.float32, device=X.device)
-    if m_indices is None:
-        m_indices = torch.empty((M_total,), dtype=torch.int32, device=X.device)
-    if row_map is None:
-        row_map = torch.empty((T, k), dtype=torch.int32, device=X.device)
-    _call("fp8gemm_moe_dispatch_contiguous", dev, stream, _take(X, torch.bfloat16, (T, H), dev, "X"),
-          _take(ids, torch.int32, (T, k), dev, "ids"), _code_ptr(codes, (M_total, H), dev, "codes"),
-          _take(scales, torch.float32, (H // 128, M_total), dev, "scales"),
-          _take(m_indices, torch.int32, (M_total,), dev, "m_indices"),
-          _take(row_map, torch.int32, (T, k), dev, "row_map"), T, H, k, G, M_total, first_expert)
+    if codes is None or scales is None or m_indices is None or row_map is None:
+        H = _dims(X, 2, "X")[1]
+        if codes is None:
+            codes = _new((M_total, H), torch.uint8, X, stream, zero=True).view(torch.float8_e4m3fn)
+        if scales is None:
+            scales = _new((H // 128, M_total), torch.float32, X, stream, zero=True)
+        if m_indices is None:
+            m_indices = _new((M_total,), torch.int32, X, stream)
+        if row_map is None:
+            row_map = _new(_dims(ids, 2, "ids"), torch.int32, X, stream)
+    st = _calls().moe_dispatch(X, ids, codes, scales, m_indices, row_map, G, M_total, first_expert, False,
+                               _handle(stream))
+    if st != 0:
+        T, H = _dims(X, 2, "X")
+        k = _dims(ids, 2, "ids")[1]
+        _refuse("fp8gemm_moe_dispatch_contiguous", st, (X, "X", (torch.bfloat16,), (T, H)), (ids, "ids", (torch.int32,), (T, k)),
+                (codes, "codes", _code_types(), (M_total, H)), (scales, "scales", (torch.float32,), (H // 128, M_total)),
+                (m_indices, "m_indices", (torch.int32,), (M_total,)), (row_map, "row_map", (torch.int32,), (T, k)))
     return codes, scales, m_indices, row_map
 
 
-def _combine_shapes(Y, weights, row_map, T):
-    """(k, rows of Y) of a combine; Y [R,H] or [G,M_max,H]."""
-    pairs = weights if weights is not None else row_map
-    if pairs is None:
+def _pairs(weights, row_map):
+    """[T,k] of a combine."""
+    if weights is None and row_map is None:
         raise ValueError("weights or row_map must be given")
-    if pairs.dim() != 2:
-        raise ValueError("weights and row_map must be [T,k]")
-    if T is not None and pairs.shape[0] != T:
-        raise ValueError("weights and row_map must have a row per token")
-    R = None
-    if Y is not None:
-        if Y.dim() not in (2, 3):
-            raise ValueError("Y must be [R,H] or [G,M_max,H]")
-        R = Y.shape[0] if Y.dim() == 2 else Y.shape[0] * Y.shape[1]
-    return pairs.shape[0], pairs.shape[1], R
+    return _dims(row_map if weights is None else weights, 2, "row_map" if weights is None else "weights")
+
+
+def _rows_shape(Y):
+    if len(Y.shape) not in (2, 3):
+        raise ValueError("Y must be [R,H] or [G,M_max,H]")
+    return Y.shape
 
 
 def moe_combine(Y, weights=None, row_map=None, out=None, stream=None):
     """out[t] = sum_j weights[t,j] * Y[row_map[t,j]]: Y bf16 [R,H] (or [G,M_max,H]), weights fp32
     [T,k] (None: ones), row_map int32 [T,k] with -1 left out (None: row t * k + j) -> bf16 [T,H]."""
-    torch = _torch()
-    T, k, R = _combine_shapes(Y, weights, row_map, None)
-    dev, H = Y.get_device(), Y.shape[-1]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=Y.device)
-    _call("fp8gemm_moe_combine", dev, stream, _take(Y, torch.bfloat16, Y.shape, dev, "Y"),
-          None if weights is None else _take(weights, torch.float32, (T, k), dev, "weights"),
-          None if row_map is None else _take(row_map, torch.int32, (T, k), dev, "row_map"),
-          _take(out, torch.bfloat16, (T, H), dev, "out"), T, H, k, R)
+        out = _new((_pairs(weights, row_map)[0], _rows_shape(Y)[-1]), _torch().bfloat16, Y, stream)
+    st = _calls().moe_combine(Y, weights, row_map, out, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, k = _pairs(weights, row_map)
+        _refuse("fp8gemm_moe_combine", st, (Y, "Y", (torch.bfloat16,), _rows_shape(Y)),
+                (weights, "weights", (torch.float32,), (T, k)), (row_map, "row_map", (torch.int32,), (T, k)),
+                (out, "out", (torch.bfloat16,), (T, Y.shape[-1])))
     return out
 
 
@@ -694,39 +712,29 @@ def moe_combine_backward(dout, Y, weights=None, row_map=None, dY=None, dweights=
     """Gradients of moe_combine: dout bf16 [T,H], Y bf16 [R,H] (or [G,M_max,H]) -> (dY of Y's shape,
     dweights fp32 [T,k]).  Rows of dY that no pair names are left untouched (zeros when allocated
     here)."""
-    torch = _torch()
-    dev = _device_of(dout, 2, "dout")
-    T, H = dout.shape
-    T, k, R = _combine_shapes(Y, weights, row_map, T)
-    if Y.shape[-1] != H:
-        raise ValueError("Y must have dout's columns")
     if dY is None:
-        dY = torch.zeros_like(Y)
+        dY = _new(_rows_shape(Y), Y.dtype, Y, stream, zero=True)
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-    _call("fp8gemm_moe_combine_backward", dev, stream, _take(dout, torch.bfloat16, (T, H), dev, "dout"),
-          _take(Y, torch.bfloat16, Y.shape, dev, "Y"),
-          None if weights is None else _take(weights, torch.float32, (T, k), dev, "weights"),
-          None if row_map is None else _take(row_map, torch.int32, (T, k), dev, "row_map"),
-          _take(dY, torch.bfloat16, Y.shape, dev, "dY"), _take(dweights, torch.float32, (T, k), dev, "dweights"),
-          T, H, k, R)
+        dweights = _new(_pairs(weights, row_map), _torch().float32, Y, stream)
+    st = _calls().moe_combine_backward(dout, Y, weights, row_map, dY, dweights, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, k = _pairs(weights, row_map)
+        H = _rows_shape(Y)[-1]
+        _refuse("fp8gemm_moe_combine_backward", st, (dout, "dout", (torch.bfloat16,), (T, H)),
+                (Y, "Y", (torch.bfloat16,), Y.shape), (weights, "weights", (torch.float32,), (T, k)),
+                (row_map, "row_map", (torch.int32,), (T, k)), (dY, "dY", (torch.bfloat16,), Y.shape),
+                (dweights, "dweights", (torch.float32,), (T, k)))
     return dY, dweights
 
 
-def _w4_format(W, scales, zeros, lead, N, K, device):
-    """(addresses of W, scales, zeros, format, group): E8M0 scales (uint8) are MXFP4, bf16 ones INT4."""
+def _w4_weights(W, scales, zeros, lead, N, K):
+    """What _refuse looks for in 4-bit weights [*lead,N,K/2] with their scales and zeros."""
     torch = _torch()
-    if scales.dim() != len(lead) + 2 or scales.shape[-1] == 0 or K % scales.shape[-1] != 0:
-        raise ValueError("scales must have one value per group of K")
-    groups = scales.shape[-1]
-    shape = (*lead, N, groups)
-    pw = _take(W, torch.uint8, W.shape, device, "W")
-    if scales.dtype is torch.uint8:
-        if zeros is not None:
-            raise ValueError("MXFP4 weights have no zeros")
-        return pw, _take(scales, torch.uint8, shape, device, "scales"), None, 0, K // groups
-    ps = _take(scales, torch.bfloat16, shape, device, "scales")
-    return pw, ps, None if zeros is None else _take(zeros, torch.uint8, shape, device, "zeros"), 1, K // groups
+    if zeros is not None and scales.dtype is torch.uint8:
+        raise ValueError("MXFP4 weights have no zeros")
+    return ((W, "W", (torch.uint8,), (*lead, N, K // 2)), (scales, "scales", (torch.uint8, torch.bfloat16), (*lead, N, None)),
+            (zeros, "zeros", (torch.uint8,), scales.shape))
 
 
 def w4_gemv(X, W, scales, zeros=None, out=None, stream=None):
@@ -734,17 +742,15 @@ def w4_gemv(X, W, scales, zeros=None, out=None, stream=None):
     the low nibble) -> bf16 [M,N].  ``scales`` uint8 [N,K/32]: MXFP4 (E2M1 codes, E8M0 scales);
     bf16 [N,K/group], group 32, 64 or 128: INT4, V = (code - zero) * scale with ``zeros`` uint8
     [N,K/group] (None: 8)."""
-    torch = _torch()
-    dev = _device_of(X, 2, "X")
-    M, K = X.shape
-    if W.dim() != 2 or 2 * W.shape[1] != K:
-        raise ValueError("W must be [N,K/2]")
-    N = W.shape[0]
-    pw, ps, pz, fmt, group = _w4_format(W, scales, zeros, (), N, K, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    _call("fp8gemm_w4_gemv", dev, stream, _take(X, torch.bfloat16, (M, K), dev, "X"), pw, ps, pz,
-          _take(out, torch.bfloat16, (M, N), dev, "out"), M, N, K, fmt, group)
+        out = _new((_dims(X, 2, "X")[0], _dims(W, 2, "W")[0]), _torch().bfloat16, X, stream)
+    st = _calls().w4_gemv(X, W, scales, zeros, out, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        M, K = _dims(X, 2, "X")
+        N = _dims(W, 2, "W")[0]
+        _refuse("fp8gemm_w4_gemv", st, (X, "X", (torch.bfloat16,), (M, K)), *_w4_weights(W, scales, zeros, (), N, K),
+                (out, "out", (torch.bfloat16,), (M, N)))
     return out
 
 
@@ -753,23 +759,21 @@ def w4_gemv_experts(X, W, scales, ids, zeros=None, first_expert: int = 0, swiglu
     [E,N,K/group], ids int32 [T,k] -> bf16 [T*k,N].  X bf16 [T,K], or [T*k,K] with a row per pair.
     ``swiglu``: silu(rows [0,N/2)) * rows [N/2,N) -> [T*k,N/2].  Pairs without an expert among the E
     (id - first_expert) get zeros."""
-    torch = _torch()
-    dev = _device_of(X, 2, "X")
-    _device_of(ids, 2, "ids")
-    T, k = ids.shape
-    rows, K = X.shape
-    if rows != T and rows != T * k:
-        raise ValueError("X must have a row per token or per pair")
-    if W.dim() != 3 or 2 * W.shape[2] != K:
-        raise ValueError("W must be [E,N,K/2]")
-    E, N = W.shape[0], W.shape[1]
-    if swiglu and N % 2:
-        raise ValueError("swiglu needs gate and up rows")
-    pw, ps, pz, fmt, group = _w4_format(W, scales, zeros, (E,), N, K, dev)
-    nout = N // 2 if swiglu else N
     if out is None:
-        out = torch.empty((T * k, nout), dtype=torch.bfloat16, device=X.device)
-    _call("fp8gemm_w4_gemv_experts", dev, stream, _take(X, torch.bfloat16, (rows, K), dev, "X"), pw, ps, pz,
-          _take(ids, torch.int32, (T, k), dev, "ids"), _take(out, torch.bfloat16, (T * k, nout), dev, "out"),
-          T, k, E, N, K, fmt, group, first_expert, int(rows != T), int(swiglu))
+        T, k = _dims(ids, 2, "ids")
+        N = _dims(W, 3, "W")[1]
+        out = _new((T * k, N // 2 if swiglu else N), _torch().bfloat16, X, stream)
+    st = _calls().w4_gemv_experts(X, W, scales, zeros, ids, out, first_expert, swiglu, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, k = _dims(ids, 2, "ids")
+        E, N, _ = _dims(W, 3, "W")
+        rows, K = _dims(X, 2, "X")
+        if st < 0 and rows not in (T, T * k):
+            raise ValueError("X must have a row per token or per pair")
+        if st < 0 and swiglu and N % 2:
+            raise ValueError("swiglu needs gate and up rows")
+        _refuse("fp8gemm_w4_gemv_experts", st, (X, "X", (torch.bfloat16,), (rows, K)),
+                *_w4_weights(W, scales, zeros, (E,), N, K), (ids, "ids", (torch.int32,), (T, k)),
+                (out, "out", (torch.bfloat16,), (T * k, N // 2 if swiglu else N)))
     return out

@@ -29,6 +29,9 @@ SOURCES = [os.path.join(CSRC, "fp8gemm_kernels.hip"), os.path.join(CSRC, "stream
            os.path.join(CSRC, "w4_kernels.hip"),
            os.path.join(CSRC, "fp8gemm_api.cpp"), os.path.join(CSRC, "moe_api.cpp"),
            os.path.join(CSRC, "fp8gemm_jit.cpp")]
+# the Python module of the short path from torch tensors to the library (host code)
+NATIVE_LIB = os.path.join(HERE, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
 # headers of the tiled kernel, compiled into the library as text for the run-time build
 JIT_HEADERS = ["fp8gemm_args.h", "fp8gemm_device.h", "fp8gemm_tiled.h"]
 JIT_DELIM = "FP8GEMM_SRC"
@@ -90,6 +93,22 @@ def jit_sources_inc() -> str:
             "static const char* const kJitSources[] = {\n%s};\n" % ",\n".join(texts))
 
 
+def build_native(tmp: str) -> None:
+    """_native.so: needs libfp8gemm.so beside it (found by $ORIGIN) and torch loaded before it."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), sysconfig.get_paths()["include"]]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE] +
+         [x for d in include for x in ("-isystem", d)] +
+         [NATIVE_SOURCE, "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_hip",
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, NATIVE_LIB)
+
+
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
     gen = tempfile.mkdtemp(prefix="fp8gemm_gen")
@@ -107,12 +126,13 @@ def build(verbose: bool = False) -> str:
         os.replace(tmp, LIB)
         _run([HIPCC, "--offload-arch=" + ARCH] + COMMON + DEVICE_FLAGS + ["-shared", "-o", tmp, PROBE_SOURCE])
         os.replace(tmp, PROBE_LIB)
+        build_native(tmp)
     finally:
         if os.path.exists(tmp):
             os.remove(tmp)
         shutil.rmtree(gen, ignore_errors=True)
     if verbose:
-        print("built", LIB, "and", PROBE_LIB)
+        print("built", LIB, NATIVE_LIB, "and", PROBE_LIB)
     return LIB
 
 

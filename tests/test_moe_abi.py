@@ -124,3 +124,17 @@ def test_binding_rejects_bad_tensors():
                    torch.zeros(4, 2, dtype=torch.uint8))
     with pytest.raises(ValueError):
         fg.moe_dispatch_masked(torch.zeros(2, 128, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int32), 2, 8)
+
+
+def test_short_path_refuses_anything():
+    """The compiled calls take any arguments without touching memory: wrong counts, types and host tensors
+    come back as a refusal."""
+    import torch
+    calls = fg._calls()
+    host = torch.zeros(4, 8)
+    for name, n in (("route_topk", 12), ("route_topk_backward", 8), ("moe_dispatch", 11), ("moe_combine", 5),
+                    ("moe_combine_backward", 7), ("w4_gemv", 6), ("w4_gemv_experts", 9)):
+        f = getattr(calls, name)
+        for count in (0, 1, n - 1, n, n + 1):
+            for value in (None, 3, "x", host, torch.zeros(0), 1 << 70, float("nan")):
+                assert f(*[value] * count) == -1
