@@ -272,7 +272,7 @@ int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const fl
  * A pair past the capacity is dropped (row -1; masked_m is at most M_max) and flags
  * FP8GEMM_DEVERR_BAD_COUNT.  Rows of A and entries of sa that no pair goes to are left untouched.
  * X must hold finite values.  H: a positive multiple of 128; k <= 32, G <= 1024.  X and A 16-byte
- * aligned.  Batches of more than 2048 pairs use the stream's workspace (see fp8gemm_prepare_stream). */
+ * aligned.  Batches of more than 8192 pairs use the stream's workspace (see fp8gemm_prepare_stream). */
 int fp8gemm_moe_dispatch_masked(const void* X, const int32_t* ids, void* A, float* sa, int32_t* masked_m,
                                 int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_max,
                                 int32_t first_expert, void* stream);
