@@ -72,7 +72,7 @@ CASES = [(1, 1, 1, 128, 1, 0), (1, 8, 16, 256, 1, 0), (3, 2, 5, 384, 2, 1), (130
 
 @pytest.mark.parametrize("T,k,G,H,M_max,first", CASES)
 def test_dispatch_masked(T, k, G, H, M_max, first):
-    """One launch and three, ragged and crowded experts, other ranks' experts, rows past the capacity."""
+    """One launch and four, ragged and crowded experts, other ranks' experts, rows past the capacity."""
     bits, X = tokens(T, H, T + G)
     ids = pick(T, k, max(G + 2 * first, k), seed=T * k)
     e, rank, count = ranks(ids, G, first)
@@ -252,7 +252,7 @@ def test_combine_bad_rows_and_other_forms():
 
 
 def test_dispatch_combine_round_trip_on_a_captured_stream():
-    """Dispatch (three launches, on the stream's workspace) and combine in a graph: replays, with eager
+    """Dispatch and combine in a graph on a stream of their own: replays, with eager
     work and other ids between them, equal the eager calls."""
     T, k, G, H = 600, 4, 20, 256
     bits, X = tokens(T, H, 9)
