@@ -123,6 +123,22 @@ int w4_tiles_per_wave(int64_t nout, int64_t K, int cols, int64_t busy, int cus) 
     return tiles >= 2 * slots ? 2 : 1;
 }
 
+// Rows of X that a pass over an expert's matrix takes; a more crowded expert takes more passes.  A token's
+// picks are distinct as a rule, so an expert has at most T pairs, and pairs / E on average.  Rows that LDS
+// has no room for beside a second workgroup (76 KB), or a wave of its own (64 KB), cost more than a few
+// experts' second passes, as long as two deviations above the average fit.  Measured, all rows that 4 + 2
+// averages allow and fewer, us: MXFP4 with SwiGLU, 16 tokens, 8 of 32 experts of 4096 x 4096, 12 rows 116, 9
+// rows 82, 8 rows (waves of their own) 65; INT4, 13 tokens, 7 of 20 experts of 1360 x 3456, 13 rows 27.1, 11
+// rows 19.3; but 11 tokens, 4 of 6 experts of 488 x 2880, 11 rows 8.1, 9 rows 11.5.
+int w4_expert_rows(int64_t T, int64_t pairs, int64_t E, int64_t K) {
+    const double mean = (double)pairs / (double)E;
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(T, 16), 4 + 2 * ((pairs + E - 1) / E));
+    const int64_t least = (int64_t)std::ceil(mean + 2.0 * std::sqrt(mean));
+    for (const int64_t room : {int64_t(65536) / (2 * K), int64_t(76 * 1024) / (2 * ((K + 127) / 128 * 128) + 16)})
+        if (room >= least) return (int)std::min(most, room);
+    return (int)most;
+}
+
 }  // namespace
 
 extern "C" {
@@ -367,10 +383,8 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
     HostDevice d;
     st = host_device(&d);
     if (st != FP8GEMM_OK) return st;
-    // rows of X that a pass over an expert's matrix takes; a token's picks are distinct as a rule, so an
-    // expert has at most T pairs, and pairs / E on average.  A more crowded one takes more passes.
-    a.cols = (int32_t)std::min<int64_t>(std::min<int64_t>(T, 16), 4 + 2 * ((a.pairs + E - 1) / E));
     const int64_t busy = std::min<int64_t>(a.pairs, E);
+    a.cols = w4_expert_rows(T, a.pairs, E, K);
     a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.cus);
     host_set_config(format == FP8GEMM_W4_MXFP4
                         ? "w4_gemv_experts mxfp4 group=%lld pairs=%lld N=%lld K=%lld tiles_per_wave=%lld by_pair=%lld"

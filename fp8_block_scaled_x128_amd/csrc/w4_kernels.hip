@@ -10,9 +10,10 @@
 //
 // A workgroup owns 16 RN rows of V and all of K.  Its waves take pairs of steps (a step is 128
 // values of K, 64 bytes of a row; a pair is one 128-byte line) in turn, each with all RN row
-// tiles, and keep PP pairs in registers on their way: 64 KB per workgroup of 8 waves.  X's values
-// stand in LDS, all of them or, past 128 KB, in chunks.  The waves' fp32 sums meet in LDS and are
-// added in wave order.  Splitting K over workgroups was measured and dropped: the exchange of sums
+// tiles, and keep PP pairs in registers on their way, up to 64 KB per workgroup of 8 waves.  X's
+// values stand in LDS, all of them or by chunks: read from the caches step by step by the lanes that
+// need them they cost 27.8 us for 13 x 7168 x 16384 (MXFP4), from LDS 22.5.  The waves' fp32 sums
+// meet in LDS and are added in wave order.  Splitting K over workgroups was measured and dropped: the exchange of sums
 // costs 2 us, more than the idle CUs of a small matrix do.
 //
 // In a step lane (n, j) = (lane % 16, lane / 16) loads 16 bytes of row n: its chunk j of 32 values.
@@ -26,6 +27,7 @@
 //   sum_k x from one more matrix-core step against ones.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8gemm_device.h"
 #include "fp8gemm_internal.h"
@@ -40,7 +42,16 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kStep = 128;                 // K values per wave and step: four runs of 32
-constexpr int kXSteps = 512;               // steps x rows of X that stand in LDS at a time: 128 KB
+
+// X past this many bytes stands in LDS by chunks of kXSteps steps x rows (256 bytes each).  64 KB chunks leave
+// room for a second workgroup on the CU, which hides the chunk's change; INT4 in groups of 32 and 64 has too
+// few registers for that beside X's values on their way, and takes 128 KB.  Measured, 64 and 128 KB, us:
+// MXFP4 12 x 16384 x 4096 12.1 and 16.2, 16 x 32768 x 7168 38.5 and 42.3, 13 x 7168 x 16384 22.5 and 23.2;
+// INT4 in 128s 12 x 16384 x 4096 13.6 and 19.3, but in 32s 19.2 and 11.6 for 16 x 7168 x 4096 (spills).
+template <int GROUP, bool MX>
+constexpr int kXSteps = MX || GROUP == 128 ? 256 : 512;
+template <int GROUP, bool MX>
+constexpr int kXBytes = MX || GROUP == 128 ? 76 * 1024 : 130 * 1024;
 
 enum Mode { kOne = 0, kExperts = 1, kExpertsSwiglu = 2 };
 
@@ -101,11 +112,14 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// GROUP: values per scale; MX: MXFP4; PAIR: a pair's scales (and zero points) are adjacent and
-// aligned, one load each, else one load per group; RN: 16-row tiles of V; PP: pairs of steps in flight per wave; MULTI: X stands in LDS by chunks; MODE: see Mode (with SwiGLU
-// tile 0 holds gate rows and tile 1 the matching up rows).
+// GROUP: values per scale; MX: MXFP4; PAIR: a pair's scales (and zero points) are adjacent and aligned, one
+// load each, else each lane loads its own (MXFP4) or a part for the lanes of its row (INT4; in K with whole
+// pairs that takes 36 us for 1 x 32768 x 7168 in groups of 64, against 33); RN: 16-row tiles of V; PP: pairs of
+// steps in flight per wave; ALONE: a wave has all of K of its tiles, else the workgroup's waves share a tile's K;
+// MULTI: X stands in LDS by chunks; MODE: see Mode (with SwiGLU tile 0 holds gate rows and tile 1 the matching
+// up rows).
 template <int GROUP, bool MX, bool PAIR, bool ZEROS, int RN, int PP, bool ALONE, bool MULTI, int MODE>
-__global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 2 : 4) void w4_kernel(W4Args a) {
+__global__ __launch_bounds__(kThreads, (MULTI && kXSteps<GROUP, MX> == 512 ? 2 : 4)) void w4_kernel(W4Args a) {
     constexpr int PER = kStep / GROUP;             // scales per step
     constexpr int SBYTES = 2 * PER * (MX ? 1 : 2); // bytes of a pair's scales
     constexpr bool SWIGLU = MODE == kExpertsSwiglu;
@@ -175,8 +189,10 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
         for (int m0 = 0; m0 < ncols; m0 += a.cols) {     // kOne: once
             const int here = min(ncols - m0, a.cols);
 
-            constexpr int SREGS = PAIR ? (SBYTES + 3) / 4 : MX ? 2 : 2 * PER;
-            constexpr int ZREGS = !ZEROS ? 1 : PAIR ? (2 * PER + 3) / 4 : 2 * PER;
+            // registers of a pair's scales; without PAIR INT4's are spread over the four lanes of a row, lane j
+            // having group j of the pair (of a step in groups of 32, group j % 2 in groups of 128)
+            constexpr int SREGS = PAIR ? (SBYTES + 3) / 4 : MX || GROUP == 32 ? 2 : 1;
+            constexpr int ZREGS = !ZEROS ? 1 : PAIR ? (2 * PER + 3) / 4 : SREGS;
             struct Slot {
                 v4u w[2][RN];
                 uint32_t s[RN][SREGS], z[RN][ZREGS];
@@ -237,13 +253,15 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 2 * PER; ++i) {
-                            const int g = step * PER + i, in = g < a.groups ? n : 0;
+                        for (int i = 0; i < SREGS; ++i) {
+                            // past the end of the row (where the next row's stand) 0
+                            const int g = step * PER + i * 4, mine = GROUP == 128 ? j & 1 : j;
+                            const bool in = mine < a.groups - g;
                             b.s[r][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                                buffer(sp, in * group_row), vs, in ? g * 2 : 0, 0);
+                                buffer(sp, n * group_row), in ? vs + mine * 2 : n * group_row, n ? g * 2 : 0, 0);
                             if constexpr (ZEROS)
                                 b.z[r][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                    buffer(zp, in * a.groups), vz, in ? g : 0, 0);
+                                    buffer(zp, n * a.groups), in ? vz + mine : n * a.groups, n ? g : 0, 0);
                         }
                     }
                 }
@@ -255,7 +273,7 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
             const int row_units = chunk * (kStep / 8), xrow = a.xstride / 16;
             const auto xbuf = buffer(MODE == kOne ? a.X + (int64_t)blockIdx.y * 16 * a.K : a.X,
                                      MODE == kOne ? ncols * a.K * 2 : a.xrows * a.K * 2);
-            constexpr int XU = MULTI ? kXSteps * 16 / kThreads : 2;   // units a thread moves at a time (MULTI: the chunk)
+            constexpr int XU = MULTI ? kXSteps<GROUP, MX> * 16 / kThreads : 2;   // units a thread moves at a time (MULTI: the chunk)
             v4u xv[XU];
             auto fetch = [&](int first_step, int u0) {
 #pragma unroll
@@ -315,6 +333,24 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
                     for (int r = 0; r < RN; ++r) {
                         v4u wt = b.w[h][r];
                         transpose4(wt);
+                        // the step's scales (and zero points below them) from the lanes that hold them
+                        uint32_t sz[4];
+                        if constexpr (!PAIR) {
+                            const uint32_t mine = b.s[r][SREGS == 2 ? h : 0] << 16 | (ZEROS ? b.z[r][SREGS == 2 ? h : 0] : 8u);
+                            auto low = [](uint32_t v, uint32_t* o) {     // of lanes j = 0 and 1, or of 2 and 3
+                                auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+                                o[0] = p[0];
+                                o[1] = p[1];
+                            };
+                            if constexpr (GROUP == 128) {
+                                low(mine, sz);                           // the pair's two groups
+                                sz[0] = sz[h];
+                            } else {
+                                auto p = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);
+                                if constexpr (GROUP == 64) low(p[h], sz);
+                                else low(p[0], sz), low(p[1], sz + 2);
+                            }
+                        }
                         v4f g;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -326,8 +362,8 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
                                 s = gi % 2 ? b.s[r][gi / 2] & 0xFFFF0000u : b.s[r][gi / 2] << 16;
                                 if constexpr (ZEROS) z = (b.z[r][gi / 4] >> (8 * (gi % 4))) & 0xFFu;
                             } else {
-                                s = b.s[r][gi] << 16;
-                                if constexpr (ZEROS) z = b.z[r][gi];
+                                s = sz[i / CPG] & 0xFFFF0000u;
+                                if constexpr (ZEROS) z = sz[i / CPG] & 0xFFu;
                             }
                             const float scale = __uint_as_float(s), shift = -(16.0f + (float)z);
 #pragma unroll
@@ -342,7 +378,6 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
             // Rounds of the ring: it is refilled pair by pair for the next round, or the wave's next tile.
             // Where X takes several chunks, the next one's values are asked for ahead of the last refills of
             // the present one, so that waiting for them does not empty the ring.
-            const int rounds = (steps + CS - 1) / CS;
             auto pair_step = [&](int u) { return (ALONE ? u : u * kWaves + wave) * 2; };
             int tile = ALONE ? tile0 + wave : tile0;
             int u0 = thread();
@@ -361,40 +396,46 @@ __global__ __launch_bounds__(kThreads, MULTI || (!MX && GROUP == 32 && !PAIR) ? 
                 const int n0 = tile * kTileRows;
 #pragma unroll
                 for (int r = 0; r < RN; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-                for (int g = 0; g < rounds; ++g) {
-                    const int base = g * CS;
-                    const bool last = g + 1 == rounds;
-                    const bool more = MULTI && !last && base + CS == first + chunk;
-                    if constexpr (MULTI) {
-                        if (more) fetch(base + CS, thread());
-                    }
-                    if (!last || (ALONE && tile + kWaves < tile_end)) {
-                        const int next = last ? 0 : base + CS, next_n0 = last ? n0 + kWaves * kTileRows : n0;
+                // (whole rounds, a chunk's last and the tile's last stand apart, each free of the others' conditions:
+                // fewer registers, and waits for no more loads than are needed)
+                int base = 0;
+                auto whole_round = [&]() {
 #pragma unroll
-                        for (int u = 0; u < PP; ++u) {
-                            const int step = base + pair_step(u);
-                            if (step < steps) compute(ring[u], 0, step - first);
-                            if (step + 1 < steps) compute(ring[u], 1, step + 1 - first);
-                            load(ring[u], next + pair_step(u), next_n0);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < PP; ++u) {
-                            const int step = base + pair_step(u);
-                            if (step < steps) compute(ring[u], 0, step - first);
-                            if (step + 1 < steps) compute(ring[u], 1, step + 1 - first);
-                        }
+                    for (int u = 0; u < PP; ++u) {
+                        const int step = base + pair_step(u);
+                        compute(ring[u], 0, step - first);
+                        compute(ring[u], 1, step + 1 - first);
+                        load(ring[u], step + CS, n0);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    if constexpr (MULTI) {
-                        if (more) {
-                            lds_barrier();               // the chunk has been read
-                            stage(thread());
-                            lds_barrier();
-                            first = base + CS;
-                        }
+                };
+                if constexpr (MULTI) {
+                    for (; first + chunk < steps; first = base) {
+                        for (; base + CS < first + chunk; base += CS) whole_round();
+                        fetch(base + CS, thread());
+                        __builtin_amdgcn_sched_barrier(0);
+                        whole_round();
+                        base += CS;
+                        lds_barrier();                   // the chunk has been read
+                        stage(thread());
+                        lds_barrier();
                     }
                 }
+                for (; base + CS < steps; base += CS) whole_round();
+                auto last_round = [&](auto refill) {
+#pragma unroll
+                    for (int u = 0; u < PP; ++u) {
+                        const int step = base + pair_step(u);
+                        if (step < steps) compute(ring[u], 0, step - first);
+                        if (step + 1 < steps) compute(ring[u], 1, step + 1 - first);
+                        if constexpr (refill.value) {
+                            load(ring[u], pair_step(u), n0 + kWaves * kTileRows);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                };
+                if (ALONE && tile + kWaves < tile_end) last_round(std::true_type());
+                else last_round(std::false_type());
 
                 auto finish = [&](int m, int n, float v, float up) {
                     if constexpr (SWIGLU) v = v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v)) * up;
@@ -452,11 +493,12 @@ void launch_one(W4Args a, unsigned y, hipStream_t s) {
         return std::max((size_t)a.cols * a.xstride, red);
     };
     if constexpr (!ALONE) {
-        if (a.cols * steps > kXSteps) {
-            // INT4 has fewer registers for X's values on their way: half the chunk and the ring
-            constexpr int PM = MX ? PP : (PP + 1) / 2, room = MX ? kXSteps : kXSteps / 2, round = kWaves * PM * 2;
-            static_assert(room / (RN == 1 ? 4 : 16) >= round, "X's chunk has room for a round");
-            const size_t bytes = lds(room / a.cols / round * round);
+        if (a.cols * (steps * kStep * 2 + 16) > kXBytes<GROUP, MX>) {
+            // pairs in flight: what registers hold beside X's values on their way
+            constexpr int X = kXSteps<GROUP, MX>, PM = RN == 2 ? (X == 256 ? 1 : PP) : MX ? PP : (PP + 1) / 2;
+            constexpr int round = kWaves * PM * 2;
+            static_assert(X / (RN == 1 ? 4 : 16) >= round, "X's chunk has room for a round");
+            const size_t bytes = lds(X / a.cols / round * round);
             hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, PM, ALONE, true, MODE>), grid, block, bytes, s, a);
             return;
         }
@@ -465,18 +507,18 @@ void launch_one(W4Args a, unsigned y, hipStream_t s) {
     hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, PP, ALONE, false, MODE>), grid, block, bytes, s, a);
 }
 
-// Scales that take more registers (groups of 32, or a load per group) leave room for half the pairs in flight.
+// The scales of groups of 32 take more registers, which leaves room for fewer pairs in flight.
 template <int RN, int PP, bool ALONE, int MODE, bool Z>
 void launch_int4(const W4Args& a, int group, unsigned y, hipStream_t s) {
     constexpr int PH = (PP + 1) / 2;
     // a pair's scales are 16, 8 or 4 bytes, its zero points 8, 4 or 2, at that many bytes' alignment (at most 4)
     const bool pair = a.K % (group == 32 || (group == 64 && !Z) ? 128 : 256) == 0;
     if (group == 32 && pair) launch_one<32, false, true, Z, RN, PH, ALONE, MODE>(a, y, s);
-    else if (group == 32) launch_one<32, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else if (group == 32) launch_one<32, false, false, Z, RN, (PP == 4 ? 3 : 1), ALONE, MODE>(a, y, s);
     else if (group == 64 && pair) launch_one<64, false, true, Z, RN, PP, ALONE, MODE>(a, y, s);
-    else if (group == 64) launch_one<64, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else if (group == 64) launch_one<64, false, false, Z, RN, PP, ALONE, MODE>(a, y, s);
     else if (pair) launch_one<128, false, true, Z, RN, PP, ALONE, MODE>(a, y, s);
-    else launch_one<128, false, false, Z, RN, PH, ALONE, MODE>(a, y, s);
+    else launch_one<128, false, false, Z, RN, PP, ALONE, MODE>(a, y, s);
 }
 
 // PP: pairs in flight of MXFP4, PI of INT4.
@@ -498,8 +540,7 @@ void launch_w4(const W4Args& a, int rn, int group, bool mxfp4, hipStream_t s) {
 }
 
 // (INT4 with the experts' bookkeeping has registers for one pair in flight and two workgroups per CU: us, 8
-// pairs of 4096 x 7168 with SwiGLU, groups of 64 with zero points, one pair 39, two with spills 43, two in
-// one workgroup per CU 46)
+// pairs of 4096 x 7168 with SwiGLU, groups of 64 with zero points, one pair 30.6, two 33.8)
 void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, hipStream_t s) {
     const unsigned y = a.by_slot ? a.pairs : a.E + 1;
     if (swiglu && a.tiles_per_wave > 0) launch_mode<2, 2, 2, true, kExpertsSwiglu>(a, group, mxfp4, y, s);

@@ -6,6 +6,7 @@ import pytest
 
 import oracle
 from test_gpu_permute import SENT, dev, pick, ranks, tokens
+from test_gpu_w4 import FORMATS, bf16, close, expert_reference, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -186,3 +187,42 @@ def test_w4_experts_past_32_bits(T, k):
         v = torch.stack((b - 16 * hi, hi), 2).view(N, K) - 8
         want = (2.0 * (v * X[p // k].double()).sum(1)).float().to(torch.bfloat16)
         assert torch.equal(y[p], want), p
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(16, 50, 4224), (13, 33, 9344), (9, 70, 8192), (4, 40, 24704), (1, 17, 70016), (21, 16, 16384),
+                                   (12, 18, 6240)])
+def test_w4_long_rows(M, N, K, fmt, group, zeros):
+    """X in LDS by chunks: whole ones, a short last one, steps past the last pair."""
+    K = K // group * group
+    rng = np.random.default_rng(M * N + K)
+    W, S, Z, v = weights(rng, (N,), K, fmt, group, zeros)
+    X, x = bf16(rng.standard_normal((M, K)))
+    close(fg.w4_gemv(X, W, S, Z), x @ v.T, np.abs(x) @ np.abs(v).T)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 24600, 256), (16, 24580, 640), (3, 131100, 128), (2, 25000, 1408)])
+def test_w4_a_tile_per_wave(M, N, K, fmt, group, zeros):
+    """Many short rows: waves with tiles of their own, the last one ragged."""
+    rng = np.random.default_rng(M * N + K)
+    W, S, Z, v = weights(rng, (N,), K, fmt, group, zeros)
+    X, x = bf16(rng.standard_normal((M, K)))
+    y = fg.w4_gemv(X, W, S, Z)
+    assert not fg.last_config().endswith("tiles_per_wave=0")
+    close(y, x @ v.T, np.abs(x) @ np.abs(v).T)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("T,k,E,N,K,swiglu", [(16, 8, 8, 40, 4224, True), (12, 2, 3, 34, 9344, False), (16, 4, 40, 3000, 256, True),
+                                              (8, 3, 24, 5600, 128, False), (16, 2, 4, 32, 8192, False)])
+def test_w4_experts_long_and_many(T, k, E, N, K, swiglu, fmt, group, zeros):
+    """Experts with X by chunks, in several passes over a crowded expert, and with tiles of a wave's own."""
+    rng = np.random.default_rng(T * N + K)
+    W, S, Z, v = weights(rng, (E, N), K, fmt, group, zeros)
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    ids[:, 0] = E - 1                                  # every token picks one of them
+    ids[1, 0] = -1
+    X, x = bf16(rng.standard_normal((T, K)))
+    y = fg.w4_gemv_experts(X, W, S, dev(ids), Z, swiglu=swiglu)
+    close(y, *expert_reference(x, v, ids, 0, False, swiglu))
