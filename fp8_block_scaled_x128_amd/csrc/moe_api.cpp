@@ -113,14 +113,23 @@ int check_w4_ptrs(const void* X, const void* W, const void* scales, const uint8_
 // Tiles of 16 rows that a wave takes one after the other, each with all of K, or 0: a workgroup's 8
 // waves share a tile's K.  `busy` workgroup columns (row blocks of X, pairs or experts) have work.  A
 // wave of its own needs no exchange of sums but 6 waves per CU to fill it, and all of X in LDS (64 KB, so
-// that two workgroups share a CU).  Measured, shared K and own, us, MXFP4: 1 x 24576 x 1536 9.8 and 7.8,
-// 1 x 32768 x 512 8.2 and 4.9, 16 x 24576 x 1536 12.4 and 9.3, 128 pairs of 7168 x 2048 on 64 experts 155
-// and 80; but 1 x 16384 x 2048 7.8 and 8.1, 1 x 7168 x 2048 5.1 and 7.1, 1 x 32768 x 7168 26.7 and 27.2.
+// that two workgroups share a CU).  Measured, shared K and own, us, MXFP4: 1 x 24576 x 1536 8.4 and 7.1,
+// 1 x 32768 x 512 6.7 and 4.7, 16 x 24576 x 1536 10.7 and 8.6, 128 pairs of 7168 x 2048 on 64 experts 156
+// and 88; but 1 x 16384 x 2048 7.2 and 7.9, 1 x 7168 x 2048 4.9 and 6.9, 1 x 32768 x 7168 23.9 and 27.3.
 // Two tiles keep the loads going from one to the next where there are that many.
 int w4_tiles_per_wave(int64_t nout, int64_t K, int cols, int64_t busy, int cus) {
     const int64_t tiles = (nout + 15) / 16 * busy, slots = 16 * (int64_t)cus;
     if (tiles < 6 * (int64_t)cus || K > 4096 || cols * K * 2 > 65536) return 0;
     return tiles >= 2 * slots ? 2 : 1;
+}
+
+// Tiles of 16 rows that a workgroup takes at a time.  One, where that gives every CU no more than one
+// workgroup, or for few rows of X and rows of 6144 values and more of a single matrix (`lone`); two share X's
+// LDS traffic and the exchange of sums.  Measured, one and two, us, MXFP4: 16 x 2048 x 2048 5.0 and 5.7,
+// 1 x 4096 x 7168 6.2 and 7.7, 1 x 7168 x 16384 16.7 and 19.1, 1 x 32768 x 7168 23.9 and 26.5; but
+// 16 x 7168 x 2048 6.8 and 6.1, 1 x 14336 x 4096 10.9 and 10.0, a token's 8 experts of 2048 x 7168 18.3 and 13.5.
+int w4_row_tiles(int64_t nout, int64_t K, int cols, int64_t busy, bool lone, int cus) {
+    return (nout + 15) / 16 * busy <= cus || (lone && cols <= 4 && K >= 6144) ? 1 : 2;
 }
 
 // Rows of X that a pass over an expert's matrix takes; a more crowded expert takes more passes.  A token's
@@ -335,10 +344,7 @@ int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint
     if (st != FP8GEMM_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     a.cols = (int32_t)std::min<int64_t>(M, 16);
-    // up to 4 rows of X leave room for whole rows of 8192 values in LDS beside narrow tiles, which fill more
-    // CUs (us, 16 and 32 rows a tile: 1 x 4096 x 7168 6.7 and 8.6, 1 x 7168 x 16384 17.6 and 17.5); wide tiles
-    // share X's LDS traffic (and a short row's exchange: 1 x 7168 x 2048 5.7 and 5.1)
-    const int rn = a.cols > 4 || K < 4096 ? 2 : 1;
+    const int rn = w4_row_tiles(N, K, a.cols, (M + 15) / 16, true, d.cus);
     a.tiles_per_wave = w4_tiles_per_wave(N, K, a.cols, (M + 15) / 16, d.cus);
     host_set_config(format == FP8GEMM_W4_MXFP4 ? "w4_gemv mxfp4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld"
                                                : "w4_gemv int4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld",
@@ -386,11 +392,12 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
     const int64_t busy = std::min<int64_t>(a.pairs, E);
     a.cols = w4_expert_rows(T, a.pairs, E, K);
     a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.cus);
+    const int rn = swiglu ? 2 : w4_row_tiles(a.nout, K, a.cols, busy, false, d.cus);
     host_set_config(format == FP8GEMM_W4_MXFP4
-                        ? "w4_gemv_experts mxfp4 group=%lld pairs=%lld N=%lld K=%lld tiles_per_wave=%lld by_pair=%lld"
-                        : "w4_gemv_experts int4 group=%lld pairs=%lld N=%lld K=%lld tiles_per_wave=%lld by_pair=%lld",
-                    {group, a.pairs, N, K, a.tiles_per_wave, a.by_slot});
-    launch_w4_experts(a, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, static_cast<hipStream_t>(stream));
+                        ? "w4_gemv_experts mxfp4 group=%lld pairs=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld by_pair=%lld"
+                        : "w4_gemv_experts int4 group=%lld pairs=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld by_pair=%lld",
+                    {group, a.pairs, N, K, rn, a.tiles_per_wave, a.by_slot});
+    launch_w4_experts(a, rn, group, format == FP8GEMM_W4_MXFP4, swiglu != 0, static_cast<hipStream_t>(stream));
     return launched();
 }
 

@@ -127,6 +127,6 @@ struct W4Args {
 
 // rn: 16-row tiles of V per workgroup where its waves share K.
 void launch_w4(const W4Args& a, int rn, int group, bool mxfp4, hipStream_t s);
-void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, hipStream_t s);
+void launch_w4_experts(const W4Args& a, int rn, int group, bool mxfp4, bool swiglu, hipStream_t s);
 
 }  // namespace fp8gemm

@@ -494,12 +494,21 @@ void launch_one(W4Args a, unsigned y, hipStream_t s) {
     };
     if constexpr (!ALONE) {
         if (a.cols * (steps * kStep * 2 + 16) > kXBytes<GROUP, MX>) {
-            // pairs in flight: what registers hold beside X's values on their way
-            constexpr int X = kXSteps<GROUP, MX>, PM = RN == 2 ? (X == 256 ? 1 : PP) : MX ? PP : (PP + 1) / 2;
-            constexpr int round = kWaves * PM * 2;
-            static_assert(X / (RN == 1 ? 4 : 16) >= round, "X's chunk has room for a round");
-            const size_t bytes = lds(X / a.cols / round * round);
-            hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, PM, ALONE, true, MODE>), grid, block, bytes, s, a);
+            // pairs in flight: what registers hold beside X's values on their way, and a chunk of 16 rows holds
+            constexpr int X = kXSteps<GROUP, MX>, FEW = MX ? PP : (PP + 1) / 2, MANY = std::min(PP, X / 256);
+            auto go = [&](auto pm) {
+                constexpr int round = kWaves * pm.value * 2;
+                const size_t bytes = lds(X / a.cols / round * round);
+                hipLaunchKernelGGL((w4_kernel<GROUP, MX, PAIR, Z, RN, pm.value, ALONE, true, MODE>), grid, block, bytes, s, a);
+            };
+            static_assert(X / 4 >= kWaves * FEW * 2 && X / 16 >= kWaves * MANY * 2, "X's chunk has room for a round");
+            if constexpr (RN == 1) {
+                if (a.cols <= 4) {
+                    go(std::integral_constant<int, FEW>());
+                    return;
+                }
+            }
+            go(std::integral_constant<int, MANY>());
             return;
         }
     }
@@ -541,11 +550,12 @@ void launch_w4(const W4Args& a, int rn, int group, bool mxfp4, hipStream_t s) {
 
 // (INT4 with the experts' bookkeeping has registers for one pair in flight and two workgroups per CU: us, 8
 // pairs of 4096 x 7168 with SwiGLU, groups of 64 with zero points, one pair 30.6, two 33.8)
-void launch_w4_experts(const W4Args& a, int group, bool mxfp4, bool swiglu, hipStream_t s) {
+void launch_w4_experts(const W4Args& a, int rn, int group, bool mxfp4, bool swiglu, hipStream_t s) {
     const unsigned y = a.by_slot ? a.pairs : a.E + 1;
     if (swiglu && a.tiles_per_wave > 0) launch_mode<2, 2, 2, true, kExpertsSwiglu>(a, group, mxfp4, y, s);
     else if (swiglu) launch_mode<2, 2, 1, false, kExpertsSwiglu>(a, group, mxfp4, y, s);
     else if (a.tiles_per_wave > 0) launch_mode<1, 4, 4, true, kExperts>(a, group, mxfp4, y, s);
+    else if (rn == 1) launch_mode<1, 3, 2, false, kExperts>(a, group, mxfp4, y, s);
     else launch_mode<2, 2, 1, false, kExperts>(a, group, mxfp4, y, s);
 }
 
