@@ -36,7 +36,10 @@ struct RouteArgs {
     int64_t T;
     int32_t E, k;
     int32_t n_group, topk_group, group_top, group_size;
-    int32_t group_lanes;        // lanes whose chunks make up a group, 0 if a group is not 1, 2, 4 or 8 chunks
+    int32_t group_lanes;        // lanes (1, 2, 4 or 8) whose chunks hold a group, 0 if groups do not fit so
+    int32_t group_pad;          // places left free after each group's experts in its lanes' chunks
+    int32_t group_shift;        // log2 of a group's places (with group_pad)
+    FastDiv div_group;          // by group_size (with group_pad)
     int32_t renorm;
     float scale;
 };

@@ -299,3 +299,14 @@ def test_given_outputs_other_stream_and_refusals():
         fg.route_topk(x, 97)
     with pytest.raises(fg.Fp8GemmError):
         fg.route_topk(x, 4, n_group=5)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,k", [(266, 2, 1, 2, 10), (376, 8, 3, 2, 32), (20, 2, 1, 1, 10),
+                                                              (28, 4, 2, 2, 12), (208, 16, 5, 1, 20), (999, 3, 2, 2, 6)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_groups_of_odd_sizes(E, n_group, topk_group, group_top, k, dtype):
+    """Groups with lanes to themselves and places left free, odd sizes, more picks than a group has."""
+    for score in ("softmax", "sigmoid"):
+        logits, b = draw(37, E, dtype, E + k, True, score, n_group, topk_group, group_top, k)
+        logits[3, E // 2:] = -np.inf                   # a row with whole groups masked
+        check(logits, k, dtype, bias=b, score=score, n_group=n_group, topk_group=topk_group, group_top=group_top, renorm=False)
