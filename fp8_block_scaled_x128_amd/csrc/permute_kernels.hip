@@ -72,11 +72,12 @@ __device__ __forceinline__ Codes<C> quantize(const v4u (&x)[C]) {
     return o;
 }
 
-// Local expert of a pair, or -1 (no pick, or another rank's expert).
-__device__ __forceinline__ int local_expert(const DispatchArgs& a, int pair) {
-    const int64_t id = (int64_t)a.ids[pair] - a.first;   // any int32 id and first stay in range
-    return a.ids[pair] >= 0 && id >= 0 && id < a.G ? (int)id : -1;
+// Local expert of a pick, or -1 (no pick, or another rank's expert).
+__device__ __forceinline__ int expert_of(const DispatchArgs& a, int pick) {
+    const int64_t id = (int64_t)pick - a.first;          // any int32 pick and first stay in range
+    return pick >= 0 && id >= 0 && id < a.G ? (int)id : -1;
 }
+__device__ __forceinline__ int local_expert(const DispatchArgs& a, int pair) { return expert_of(a, a.ids[pair]); }
 
 __device__ __forceinline__ int padded(int n) { return (n + 127) & ~127; }
 
@@ -112,13 +113,13 @@ __device__ __forceinline__ void store_scales(const DispatchArgs& a, int kb0, int
     }
 }
 
-// m_indices of this token's share of the contiguous layout's rows: the expert whose rows [first,
+// m_indices of this workgroup's share of the contiguous layout's rows: the expert whose rows [first,
 // first + count) hold the row, or -1.
 template <typename First, typename Count>
-__device__ __forceinline__ void fill_indices(const DispatchArgs& a, int64_t t, First first, Count count) {
-    const int64_t per = (a.cap + a.T - 1) / a.T;
-    const int64_t end = min((t + 1) * per, (int64_t)a.cap);
-    for (int64_t r = t * per + threadIdx.x; r < end; r += blockDim.x) {
+__device__ __forceinline__ void fill_indices(const DispatchArgs& a, First first, Count count) {
+    const int64_t per = (a.cap + gridDim.x - 1) / gridDim.x;
+    const int64_t end = min((blockIdx.x + 1) * per, (int64_t)a.cap);
+    for (int64_t r = blockIdx.x * per + threadIdx.x; r < end; r += blockDim.x) {
         int lo = 0, hi = a.G;            // the last expert whose first row is not past r
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -132,7 +133,7 @@ __device__ __forceinline__ void fill_indices(const DispatchArgs& a, int64_t t, F
 // One launch: workgroup (t, s) counts every pair's expert, and those before token t, in LDS.
 __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a, int spans) {
     __shared__ int all[kDispatchMaxGroups], before[kDispatchMaxGroups];
-    __shared__ int first[kDispatchMaxGroups + 1];
+    __shared__ int first[kDispatchMaxGroups], wave_total[kThreads / 64];
     __shared__ int rows[kDispatchMaxTopk], mine[kDispatchMaxTopk];
     __shared__ float scales[kSpan / 128];
     const int64_t t = blockIdx.x / spans;
@@ -143,28 +144,46 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     for (int e = threadIdx.x; e < a.G; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
     const int p0 = (int)t * a.k;
-    for (int p = threadIdx.x; p < a.pairs; p += kThreads) {
-        const int e = local_expert(a, p);
-        if (e >= 0) {
-            atomicAdd(&all[e], 1);
-            if (p < p0) atomicAdd(&before[e], 1);
+    constexpr int kDeep = 8;             // picks a thread has on their way
+    for (int p1 = threadIdx.x; p1 < a.pairs; p1 += kThreads * kDeep) {
+        int pick[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) pick[i] = p1 + i * kThreads < a.pairs ? a.ids[p1 + i * kThreads] : -1;
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int e = expert_of(a, pick[i]);
+            if (e >= 0) {
+                atomicAdd(&all[e], 1);
+                if (p1 + i * kThreads < p0) atomicAdd(&before[e], 1);
+            }
         }
     }
     if (threadIdx.x < a.k) mine[threadIdx.x] = local_expert(a, p0 + threadIdx.x);
     __syncthreads();
-    if (a.contiguous && threadIdx.x < 64) {   // first rows: a running sum over 64 experts at a time
+    if (a.contiguous) {                  // first rows: a running sum over 256 experts at a time, 64 a wave
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         int carry = 0;
-        for (int e0 = 0; e0 < a.G; e0 += 64) {
+        for (int e0 = 0; e0 < a.G; e0 += kThreads) {
             const int e = e0 + threadIdx.x;
             const int n = e < a.G ? padded(all[e]) : 0;
             int sum = n;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int up = __shfl_up(sum, o, 64);
-                if ((int)threadIdx.x >= o) sum += up;
+                if (lane >= o) sum += up;
             }
-            if (e < a.G) first[e] = carry + sum - n;
-            carry += __shfl(sum, 63, 64);
+            int row = carry + sum - n;
+            if (a.G > 64) {
+                if (lane == 63) wave_total[wave] = sum;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kThreads / 64; ++w) {
+                    row += w < wave ? wave_total[w] : 0;
+                    carry += wave_total[w];
+                }
+                if (e0 + kThreads < a.G) __syncthreads();
+            }
+            if (e < a.G) first[e] = row;
         }
     }
     __syncthreads();
@@ -180,12 +199,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         rows[threadIdx.x] = row;
         if (s == 0) a.row_map[p0 + threadIdx.x] = row;
     }
-    if (s == 0) {
-        if (a.contiguous) {
-            fill_indices(a, t, [&](int e) { return first[e]; }, [&](int e) { return all[e]; });
-        } else if (t == 0) {
-            for (int e = threadIdx.x; e < a.G; e += kThreads) a.where[e] = min(all[e], a.cap);
-        }
+    if (a.contiguous) {
+        fill_indices(a, [&](int e) { return first[e]; }, [&](int e) { return all[e]; });
+    } else if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < a.G; e += kThreads) a.where[e] = min(all[e], a.cap);
     }
     __syncthreads();
     const Codes<1> q = quantize(x);
@@ -361,7 +378,7 @@ __global__ __launch_bounds__(1024) void dispatch_copy_kernel(DispatchArgs a) {
         if (a.by_row && row >= 0) sc.token[row] = (int32_t)t;
     }
     __syncthreads();
-    if (a.contiguous) fill_indices(a, t, [&](int e) { return sc.first[e]; }, [&](int e) { return sc.total[e]; });
+    if (a.contiguous) fill_indices(a, [&](int e) { return sc.first[e]; }, [&](int e) { return sc.total[e]; });
     for (int col0 = 0; col0 < a.H; col0 += blockDim.x * 16, col += blockDim.x * 16) {
         if (col0) load(col);
         const Codes<2> q = quantize(x);
@@ -469,9 +486,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a, int sp
 
 // dY[row(t, j)] = w[t][j] dout[t] and dw[t][j] = <dout[t], Y[row(t, j)]>: one workgroup per token
 // passes over the row once for each kDeep picks, with the products' sums in registers.
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs a) {
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void combine_backward_kernel(CombineArgs a) {
     constexpr int kDeep = 8;
-    __shared__ float part[kThreads / 64][kDeep];
+    __shared__ float part[THREADS / 64][kDeep];
     const int64_t t = blockIdx.x;
     if (threadIdx.x < a.k && a.row_map && a.row_map[t * a.k + threadIdx.x] >= a.R)
         atomicOr(a.err, (int32_t)kDevErrBadIndex);
@@ -484,7 +502,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
             w[i] = row[i] >= 0 && a.weights ? a.weights[t * a.k + j0 + i] : 1.0f;
             dot[i] = 0.0f;
         }
-        for (int col = threadIdx.x * 8; col < a.H; col += kSpan) {
+        for (int col = threadIdx.x * 8; col < a.H; col += THREADS * 8) {
             const v4u d = *reinterpret_cast<const v4u*>(a.dout + t * a.H + col);
             v4u y[kDeep];
 #pragma unroll
@@ -516,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
         if (threadIdx.x < kDeep && j0 + (int)threadIdx.x < a.k) {
             float v = 0.0f;
 #pragma unroll
-            for (int w2 = 0; w2 < kThreads / 64; ++w2) v += part[w2][threadIdx.x];
+            for (int w2 = 0; w2 < THREADS / 64; ++w2) v += part[w2][threadIdx.x];
             a.dweights[t * a.k + j0 + threadIdx.x] = v;
         }
         __syncthreads();
@@ -559,8 +577,13 @@ void launch_combine(const CombineArgs& a, hipStream_t s) {
     else hipLaunchKernelGGL(combine_kernel<false>, grid, dim3(kThreads), 0, s, a, spans);
 }
 
+// 512 threads where a token's row is more than one pass of 256 and every CU has a token's workgroup to
+// itself.  Measured, 256 and 512, us, 7 picks: 11 x 7168 7.7 and 6.7, 256 x 2944 7.3 and 6.9; but 512 x 2944 10.2
+// and 10.3, 1000 x 2944 17.0 and 18.0, 256 x 2048 5.7 and 5.8.
 void launch_combine_backward(const CombineArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(combine_backward_kernel, dim3((unsigned)a.T), dim3(kThreads), 0, s, a);
+    const dim3 grid((unsigned)a.T);
+    if (a.H > kSpan && a.T <= 256) hipLaunchKernelGGL(combine_backward_kernel<512>, grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL(combine_backward_kernel<256>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace fp8gemm
