@@ -45,9 +45,9 @@ int check_dispatch(int64_t T, int64_t H, int32_t k, int32_t G, int64_t cap) {
 
 // Batches of at most this many pairs are ranked inside the copying launch, where every workgroup counts
 // all pairs; larger ones take four launches, whose time grows with the experts.  Measured, one launch and
-// four, us, k = 8: masked, 64 experts, H = 7168: 1024 pairs 5.2 and 14.4, 4096 12.3 and 19.6, 8192 28.1
-// and 27.2, 16384 82 and 40; 256 experts 8192 28.8 and 38.5; H = 2048 8192 12.9 and 17.2, 16384 27.1 and
-// 21.2.  Contiguous, 64 experts, H = 7168: 4096 13.1 and 20.7, 8192 30.1 and 27.1.
+// four, us, k = 8: masked, 64 experts, H = 7168: 1024 pairs 5.1 and 14.2, 8192 24.7 and 28.5, 16384 68 and 42;
+// H = 2048: 8192 10.7 and 17.1, 16384 23.9 and 21.4; contiguous, 256 experts, H = 7168: 8192 27.2 and 34.4,
+// 16384 71 and 48.
 constexpr int64_t kSmallPairs = 8192;
 
 int dispatch(DispatchArgs a, hipStream_t stream) {

@@ -7,6 +7,11 @@
 // (t, j) order, with the same expert, so the layout does not depend on timing.  Small batches
 // recompute the ranks in every workgroup of the one copying launch; large ones count chunks of
 // pairs, scan the counts, copy, and put the scales in place, in four launches.
+//
+// Bound: memory, with next to no arithmetic (the quantiser's is hidden).  4095 x 8 x 7168 on 64 experts
+// 69.3 us, 4.35 TB/s (count 5, scan 4, copy 52, scales 7); 128 x 8 x 7168 on 16 experts 5.2 us, a launch
+// and the pass over the picks; combine 4096 x 8 x 7168 103.6 us, 5.1 TB/s, and 128 x 8 x 7168 6.7 us from
+// the memory-side cache; its gradient 1000 x 6 x 2048 11.7 us, 4.5 TB/s.
 
 #include <algorithm>
 

@@ -13,6 +13,10 @@
 // power of two) hold a group, it is given those lanes' chunks to itself, with places left free after
 // it (32768 x 160 in 8 groups: 12.7 us, against 16.2 with groups scanned in LDS by a lane each, which
 // stays for the others).
+//
+// Bound: instructions, then memory: a lane spends about 20 on each expert's score and place and 30 on
+// each pick.  32768 x 256 fp32, bias, 4 of 8 groups, 8 picks: 13.3 us, 2.7 TB/s; a single token 4.2 us,
+// its picks' chain of dependent steps past a launch's 2.8 us; gradient 8191 x 160 bf16, 6 picks: 4.1 us.
 
 #include "fp8gemm_device.h"
 #include "fp8gemm_internal.h"
