@@ -379,12 +379,13 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
         p[q] = x[q] == kNegInf ? 0.0f : (SIGMOID ? sigmoid_f32(x[q]) : exp_f32(x[q] - m));
     if (a.renorm) {
         const float total = row16_sum_f(p[0] + p[1]);
-        const float r = total > 0.0f ? 1.0f / total : 0.0f;
-        const float mean = row16_sum_f(g[0] * (p[0] * r) + g[1] * (p[1] * r));
+        // (quotients, not products with 1 / total: a pick alone has a share of exactly 1, and no gradient)
+        const float share[2] = {total > 0.0f ? p[0] / total : 0.0f, total > 0.0f ? p[1] / total : 0.0f};
+        const float mean = row16_sum_f(g[0] * share[0] + g[1] * share[1]);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             // sigmoid: ds = (g - mean) / total, dx = ds s (1 - s); softmax: dx = (g - mean) s / total
-            float v = (g[q] - mean) * (p[q] * r);
+            float v = (g[q] - mean) * share[q];
             if constexpr (SIGMOID) v *= sigmoid_f32(-x[q]);
             if (id[q] >= 0) d[id[q]] = x[q] == kNegInf ? 0.0f : v;
         }

@@ -17,6 +17,13 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU runs deselect these 
 import fp8_block_scaled_x128_amd as fg  # noqa: E402
 
 
+@pytest.fixture(autouse=True)
+def error_word():
+    """Rows past a capacity set the device error word: it is left clear for the next test."""
+    yield
+    fg.read_device_error()
+
+
 @pytest.mark.parametrize("T,k,G,H,M_max", [(1025, 8, 256, 256, 60), (1024, 8, 64, 128, 200), (8193, 1, 1, 128, 8200),
                                            (23000, 3, 70, 128, 2000), (1400, 6, 1024, 2176, 30), (9000, 1, 5, 16512, 4000)])
 def test_dispatch_around_the_choice(T, k, G, H, M_max):

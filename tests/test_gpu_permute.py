@@ -19,6 +19,13 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU runs deselect these 
 
 import fp8_block_scaled_x128_amd as fg  # noqa: E402
 
+
+@pytest.fixture(autouse=True)
+def error_word():
+    """Rows past a capacity set the device error word: it is left clear for the next test."""
+    yield
+    fg.read_device_error()
+
 SENT = 0x7F          # an E4M3 NaN: the library never writes it
 
 

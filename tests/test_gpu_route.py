@@ -310,3 +310,14 @@ def test_groups_of_odd_sizes(E, n_group, topk_group, group_top, k, dtype):
         logits, b = draw(37, E, dtype, E + k, True, score, n_group, topk_group, group_top, k)
         logits[3, E // 2:] = -np.inf                   # a row with whole groups masked
         check(logits, k, dtype, bias=b, score=score, n_group=n_group, topk_group=topk_group, group_top=group_top, renorm=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_one_renormalised_pick_has_no_gradient(score, dtype):
+    """Its weight is the scale whatever the logits are: the gradient is zero, not rounding noise."""
+    rng = np.random.default_rng(2)
+    logits = dev(rng.standard_normal((500, 96)).astype(np.float32), dtype)
+    ids, w = fg.route_topk(logits, 1, score=score, scale=2.5)
+    dx = fg.route_topk_backward(logits, ids, dev(rng.standard_normal((500, 1)).astype(np.float32)), score=score, scale=2.5)
+    assert bool((w == 2.5).all()) and bool((dx == 0).all())
