@@ -12,9 +12,9 @@
 // values of K, 64 bytes of a row; a pair is one 128-byte line) in turn, each with all RN row
 // tiles, and keep PP pairs in registers on their way, up to 64 KB per workgroup of 8 waves.  X's
 // values stand in LDS, all of them or by chunks: read from the caches step by step by the lanes that
-// need them they cost 27.8 us for 13 x 7168 x 16384 (MXFP4), from LDS 22.5.  The waves' fp32 sums
-// meet in LDS and are added in wave order.  Splitting K over workgroups was measured and dropped: the exchange of sums
-// costs 2 us, more than the idle CUs of a small matrix do.
+// need them they cost 27.8 us for 13 x 7168 x 16384 (MXFP4), from LDS 22.1.  The waves' fp32 sums
+// meet in LDS and are added in wave order.  Splitting K over workgroups was measured and dropped:
+// the exchange of sums costs 2 us, more than the idle CUs of a small matrix do.
 //
 // 1 x 32768 x 7168 MXFP4 24 us, 5.2 TB/s; 1 x 4096 x 7168 INT4 in 128s 7.5 us, a launch, the way of X into
 // LDS and the exchange of sums around 3.2 us of weights; 13 x 7168 x 16384 MXFP4 20 us, 224 workgroups on

@@ -294,8 +294,8 @@ int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_
 int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* weights, const int32_t* row_map, void* dY,
                                  float* dweights, int64_t T, int64_t H, int32_t k, int64_t R, void* stream);
 
-/* Y[m][n] = bf16(sum_k X[m][k] V[n][k]) for few rows of X (the weights are read once per 16 rows), V decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N]
- * bf16, W [N][K/2] bytes, the even element of a row in the low nibble:
+/* Y[m][n] = bf16(sum_k X[m][k] V[n][k]) for few rows of X (the weights are read once per 16 rows), V
+ * decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N] bf16, W [N][K/2] bytes, the even element of a row in the low nibble:
  *   FP8GEMM_W4_MXFP4: E2M1 codes, scales uint8 [N][K/32] (E8M0), the B and sb of
  *     fp8gemm_fp8fp4_grouped_masked; group = 32, zeros NULL.  Products are exact: a decoded value is
  *     a bf16 value.  Scales below 2^-120 may flush; 255 gives unspecified results.
@@ -313,7 +313,8 @@ int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint
  *   swiglu: rows [0, N/2) of a matrix are the gate, [N/2, N) the up projection, and Y [T * k][N/2] =
  *     bf16(silu(gate) * up), both in fp32; N even.
  * A pair without an expert here (id negative or outside) gets a row of zeros.  Pairs that share an
- * expert share one reading of its matrix, up to 4 plus twice the pairs per expert (16 at most) at a time.  X below 2^31 bytes. */
+ * expert share one reading of its matrix, several at a time (16 at most; fewer where LDS has no room
+ * for their rows of X).  X below 2^31 bytes. */
 int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, const uint8_t* zeros, const int32_t* ids,
                             void* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t format, int32_t group,
                             int32_t first_expert, int32_t x_per_pair, int32_t swiglu, void* stream);
