@@ -14,6 +14,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <unordered_map>
 #include <vector>
@@ -29,6 +30,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 
 struct Workspace {
+    std::mutex mu;                                       // held by a call from its first launch on it to its last
     float* partials = nullptr;
     size_t partial_bytes = 0;
     int32_t* counters = nullptr;
@@ -43,7 +45,7 @@ struct DeviceState {
     int32_t* err = nullptr;                              // device error word (static device memory)
     ScratchPointers scratch;                             // static split-K scratch of fp8gemm_nt_noalloc
     std::vector<int> occupancy;                          // per kernel-table entry
-    std::unordered_map<hipStream_t, Workspace> ws;       // split-K workspace per stream
+    std::unordered_map<hipStream_t, std::unique_ptr<Workspace>> ws;
 };
 
 DeviceState g_dev[kMaxDevices];
@@ -144,15 +146,19 @@ size_t workspace_counters(int cus) { return std::max<size_t>((size_t)cus, 4096);
 // valid pointers for the life of the process.  Counters are zeroed at allocation and every
 // launch leaves them at zero.  No allocation is made while the stream is capturing (the stream
 // must be prepared before: fp8gemm_prepare_stream or an earlier split-K call).
-int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t counters,
-              Workspace** out) {
-    std::lock_guard<std::mutex> lock(d->mu);
+// `hold` locks the workspace: the caller keeps it until its last launch is enqueued.  One launch is
+// ordered against others by the stream; a call of several that pass values through the workspace
+// (a large dispatch) needs every other thread's launches on it to stay out from between them.
+int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t counters, Workspace** out,
+              std::unique_lock<std::mutex>* hold) {
+    std::unique_lock<std::mutex> lock(d->mu);
     auto it = d->ws.find(stream);
     if (it == d->ws.end()) {
         hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &cs) != hipSuccess) return FP8GEMM_ERR_HIP;
         if (cs != hipStreamCaptureStatusNone) return FP8GEMM_ERR_UNSUPPORTED;
-        Workspace w;
+        auto made = std::make_unique<Workspace>();
+        Workspace& w = *made;
         const size_t bytes = workspace_partial_bytes(d->cus);
         const size_t n = workspace_counters(d->cus);
         if (hipMalloc(&w.partials, bytes) != hipSuccess) return FP8GEMM_ERR_HIP;
@@ -168,10 +174,12 @@ int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t c
         }
         w.partial_bytes = bytes;
         w.counter_count = n;
-        it = d->ws.emplace(stream, w).first;
+        it = d->ws.emplace(stream, std::move(made)).first;
     }
-    Workspace& w = it->second;
+    Workspace& w = *it->second;
+    lock.unlock();                                       // a workspace is never removed; other streams go on
     if (w.partial_bytes < partial_bytes || w.counter_count < counters) return FP8GEMM_ERR_UNSUPPORTED;
+    if (hold) *hold = std::unique_lock<std::mutex>(w.mu);
     *out = &w;
     return FP8GEMM_OK;
 }
@@ -371,6 +379,7 @@ int launch(int layout, KernelArgs& a, int64_t expected_rows, hipStream_t stream,
     a.ws = nullptr;
     a.counters = nullptr;
     int64_t slots = (int64_t)cus * (jk ? jk->occupancy : d->occupancy[c.entry]);
+    std::unique_lock<std::mutex> hold;                   // the workspace, until the launch is enqueued
 
     // Stream-K for the tiles after the last full round of whole tiles (dense 256-row tiles, which
     // take no K split): instead of a last, partly idle round, the leftover tiles' K blocks are
@@ -404,7 +413,7 @@ int launch(int layout, KernelArgs& a, int64_t expected_rows, hipStream_t stream,
             // a stream with no workspace that is being captured keeps whole tiles (UNSUPPORTED
             // from workspace: nothing may be allocated during capture)
             Workspace* w = nullptr;
-            st = workspace(d, stream, need, (size_t)R, &w);
+            st = workspace(d, stream, need, (size_t)R, &w, &hold);
             if (st != FP8GEMM_OK && st != FP8GEMM_ERR_UNSUPPORTED) return st;
             if (st == FP8GEMM_OK) {
                 streamk = true;
@@ -427,7 +436,7 @@ int launch(int layout, KernelArgs& a, int64_t expected_rows, hipStream_t stream,
             a.counters = d->scratch.counters;
         } else {
             Workspace* w = nullptr;
-            st = workspace(d, stream, partial_bytes, (size_t)tiles, &w);
+            st = workspace(d, stream, partial_bytes, (size_t)tiles, &w, &hold);
             if (st != FP8GEMM_OK) return st;
             a.ws = w->partials;
             a.counters = w->counters;
@@ -565,12 +574,12 @@ int host_device(HostDevice* out) {
     return FP8GEMM_OK;
 }
 
-int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch) {
+int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch, std::unique_lock<std::mutex>* hold) {
     DeviceState* d = nullptr;
     int st = device_state(&d);
     if (st != FP8GEMM_OK) return st;
     Workspace* w = nullptr;
-    st = workspace(d, stream, bytes, 0, &w);
+    st = workspace(d, stream, bytes, 0, &w, hold);
     if (st != FP8GEMM_OK) return st;
     *scratch = w->partials;
     return FP8GEMM_OK;
@@ -836,7 +845,7 @@ int fp8gemm_prepare_stream(void* stream) {
     int st = device_state(&d);
     if (st != FP8GEMM_OK) return st;
     Workspace* w = nullptr;
-    return workspace(d, static_cast<hipStream_t>(stream), 0, 0, &w);
+    return workspace(d, static_cast<hipStream_t>(stream), 0, 0, &w, nullptr);
 }
 
 int fp8gemm_set_num_cus(int n) {

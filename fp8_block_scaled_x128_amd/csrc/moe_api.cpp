@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "fp8gemm.h"
 #include "fp8gemm_internal.h"
@@ -59,14 +60,15 @@ int dispatch(DispatchArgs a, hipStream_t stream) {
     a.pairs = (int32_t)(a.T * a.k);
     a.div_k = make_fastdiv((uint32_t)a.k);
     const bool large = a.pairs > kSmallPairs;
+    std::unique_lock<std::mutex> hold;       // counts, ranks and scales go from launch to launch in the workspace
     if (large) {
         a.chunks = (a.pairs + kDispatchChunk - 1) / kDispatchChunk;
         const size_t words = (size_t)a.G * a.chunks + 2 * (size_t)a.G + (size_t)a.pairs;
         const size_t rows = (size_t)(a.contiguous ? 1 : a.G) * a.cap;
         void* p = nullptr;
         // the turned scales where their scratch fits the workspace
-        a.by_row = host_stream_scratch(stream, (words + (size_t)a.T * a.nkb + rows) * sizeof(int32_t), &p) == FP8GEMM_OK;
-        if (!a.by_row) st = host_stream_scratch(stream, words * sizeof(int32_t), &p);
+        a.by_row = host_stream_scratch(stream, (words + (size_t)a.T * a.nkb + rows) * sizeof(int32_t), &p, &hold) == FP8GEMM_OK;
+        if (!a.by_row) st = host_stream_scratch(stream, words * sizeof(int32_t), &p, &hold);
         if (st != FP8GEMM_OK) return st;
         a.scratch = static_cast<int32_t*>(p);
     }

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <mutex>
 
 #include "fp8gemm_args.h"
 
@@ -18,8 +19,9 @@ struct HostDevice {
     int32_t* err = nullptr;     // device error word
 };
 int host_device(HostDevice* out);                                       // status code
-// The stream's library-owned workspace (see fp8gemm.h): `bytes` of scratch, status code.
-int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch);
+// The stream's library-owned workspace (see fp8gemm.h): `bytes` of scratch, status code.  `hold` keeps
+// other threads' calls off it and is kept until the last launch that uses it is enqueued.
+int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch, std::unique_lock<std::mutex>* hold);
 // The calling thread's last configuration: a static format of %lld fields and at most 8 values.
 void host_set_config(const char* fmt, std::initializer_list<long long> values);
 

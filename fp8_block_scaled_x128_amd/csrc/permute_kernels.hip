@@ -90,7 +90,7 @@ __device__ __forceinline__ int padded(int n) { return (n + 127) & ~127; }
 // row in the contiguous layout.
 __device__ __forceinline__ int place(const DispatchArgs& a, int e, int rank, int64_t first) {
     const int64_t row = a.contiguous ? first + rank : (int64_t)e * a.cap + rank;
-    return rank < a.cap && (!a.contiguous || row < a.cap) ? (int)row : -1;
+    return (uint32_t)rank < (uint32_t)a.cap && (!a.contiguous || row < a.cap) ? (int)row : -1;
 }
 
 // Store a lane's codes at column `col` of the rows[0..k) that are not -1, past the caches (nothing reads
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_scales_kernel(DispatchArgs 
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        v[i] = token[i] >= 0 && kb0 + kb < a.nkb ? sc.scales[(int64_t)token[i] * a.nkb + kb0 + kb] : 0.0f;
+        v[i] = token[i] >= 0 && token[i] < a.T && kb0 + kb < a.nkb ? sc.scales[(int64_t)token[i] * a.nkb + kb0 + kb] : 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) tile[r1 + i * kPass][kb] = v[i];
     __syncthreads();
