@@ -289,7 +289,8 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
             next = max(next, v);
         }
         next = row16_max_i(next);
-        cm = l == w ? next : cm;
+        // (with nothing left to pick, w is some chunk, perhaps of a group that was struck out: it stays out)
+        cm = l == w && best != kLowest ? next : cm;
         const bool keep_it = l == j;
         pick = keep_it ? w * V + found : pick;
         key = keep_it ? best : key;
