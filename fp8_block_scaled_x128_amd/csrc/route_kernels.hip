@@ -39,7 +39,22 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     else return clean(static_cast<const float*>(p)[i]);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+// 1 / (1 + e^-x) with e^-|x| alone, so that scores below 2^-126 are not lost in the reciprocal.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    const float e = exp_f32(-__builtin_fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    return x < 0.0f ? e * r : r;
+}
+
+// The score of a pick with logit x up to a factor common to a token's picks, of which `most` is the largest
+// logit.  Renormalised weights are shares: taken from these values, of which the largest is 1/2 at least, they
+// are finite and exact to rounding where the scores themselves come near the end of the type.
+template <bool SIGMOID>
+__device__ __forceinline__ float share_f32(float x, float most) {
+    if constexpr (!SIGMOID) return exp_f32(x - most);
+    const float e = exp_f32(-__builtin_fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    return x < 0.0f ? exp_f32(x - fminf(most, 0.0f)) * r : r;
+}
+constexpr float kNoScore = -104.0f;   // e^x rounds to 0 in 32 bits from here on
 
 // Choice values (not -0) as integers that order as they do: the cross-lane steps of integer maxima
 // are single instructions.
@@ -305,25 +320,33 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     if (key0 == kLowest) pick0 = -1;      // nothing left to choose
     if (key1 == kLowest) pick1 = -1;
 
-    // weights: the picked experts' scores without the bias
-    auto weight = [&](int pick, int key) {
-        if (pick < 0) return 0.0f;
-        return score(a.bias ? load_logit<BF16>(a.logits, base + pick) : value_of(key));
+    // weights: the picked experts' scores without the bias, or their shares
+    auto logit = [&](int pick, int key) {
+        if (pick < 0) return kNegInf;
+        return a.bias ? load_logit<BF16>(a.logits, base + pick) : value_of(key);
     };
-    const float w0 = weight(pick0, key0), w1 = a.k > 16 ? weight(pick1, key1) : 0.0f;
-    float f = a.scale;
+    const float x0 = logit(pick0, key0), x1 = a.k > 16 ? logit(pick1, key1) : kNegInf;
+    float w0, w1 = 0.0f;
     if (a.renorm) {
+        const float most = row16_max_f(fmaxf(x0, x1));
+        const bool none = most - m < kNoScore;           // no pick, or every one's score is 0 (m is 0 for sigmoid)
+        w0 = share_f32<SIGMOID>(x0, most);
+        if (a.k > 16) w1 = share_f32<SIGMOID>(x1, most);
         const float sum = row16_sum_f(w0 + w1);
-        f = sum > 0.0f ? a.scale / sum : 0.0f;
+        w0 = none ? 0.0f : w0 / sum;                     // (not times scale / sum, which may pass the type's range)
+        if (a.k > 16) w1 = none ? 0.0f : w1 / sum;
+    } else {
+        w0 = pick0 < 0 ? 0.0f : score(x0);
+        if (a.k > 16) w1 = pick1 < 0 ? 0.0f : score(x1);
     }
     if (live) {
         if (l < a.k) {
             a.ids[token * a.k + l] = pick0;
-            a.weights[token * a.k + l] = w0 * f;
+            a.weights[token * a.k + l] = w0 * a.scale;
         }
         if (16 + l < a.k) {
             a.ids[token * a.k + 16 + l] = pick1;
-            a.weights[token * a.k + 16 + l] = w1 * f;
+            a.weights[token * a.k + 16 + l] = w1 * a.scale;
         }
     }
 }
@@ -371,13 +394,14 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
         }
         sum = row16_sum_f(sum);
     } else {
-        m = row16_max_f(fmaxf(x[0], x[1]));   // a softmax over the picks is all that renormalised scores need
+        m = row16_max_f(fmaxf(x[0], x[1]));   // renormalised scores need the picks alone
         if (m == kNegInf) m = 0.0f;
     }
     float p[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-        p[q] = x[q] == kNegInf ? 0.0f : (SIGMOID ? sigmoid_f32(x[q]) : exp_f32(x[q] - m));
+        p[q] = x[q] == kNegInf ? 0.0f : SIGMOID && !a.renorm ? sigmoid_f32(x[q]) : share_f32<SIGMOID>(x[q], m);
+    if (SIGMOID && a.renorm && m < kNoScore) p[0] = p[1] = 0.0f;   // the weights are 0 there
     if (a.renorm) {
         const float total = row16_sum_f(p[0] + p[1]);
         // (quotients, not products with 1 / total: a pick alone has a share of exactly 1, and no gradient)

@@ -238,7 +238,9 @@ int fp8gemm_moe_expert_masked(const void* A, const float* sa, const void* W1, co
  *     score is the sum of its group_top (1 or 2) largest c, and only the experts of the
  *     topk_group groups of largest score can be chosen.
  *   ids[t] = the k largest c in descending order; weights[t][j] = s[ids[t][j]], divided by their
- *     sum with `renorm` (0 where the sum is 0), times `scale`.
+ *     sum with `renorm`, times `scale`.  The quotients are formed from the picked logits' differences, so
+ *     that they keep their accuracy where the scores are tiny; they are 0 where the largest picked score
+ *     is below 2^-150 (of 1 for sigmoid, of the token's largest score for softmax).
  * Equal values go to the lower index, for groups and experts.  A NaN counts as -infinity and
  * +infinity as the largest finite value, in logits and bias.  An expert whose logit or bias is
  * -infinity cannot be chosen; where fewer than k can, the remaining ids are -1 and weights 0.
@@ -256,7 +258,8 @@ int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, floa
  *   sigmoid, renorm    dlogits[j] = (g_j - sum g p) p_j (1 - s_j)
  *   softmax            dlogits[e] = s_e ([e picked] g_e - sum g s), every expert
  *   softmax, renorm    dlogits[j] = (g_j - sum g p) p_j
- * and 0 elsewhere.  ids as route_topk wrote them: an id outside [0, E) contributes nothing; the
+ * and 0 elsewhere.  p is formed as route_topk's quotients are (sigmoid: 0 where those are 0; softmax: from
+ * the picked logits alone, wherever the token's others lie).  ids as route_topk wrote them: an id outside [0, E) contributes nothing; the
  * ids of a token are distinct (else its row is unspecified). */
 int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int64_t T,
                                 int32_t E, int32_t k, int32_t dtype, int32_t score, int32_t renorm, float scale,
