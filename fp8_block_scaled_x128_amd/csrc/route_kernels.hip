@@ -39,6 +39,16 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     else return clean(static_cast<const float*>(p)[i]);
 }
 
+// e^x within 2 units in the last place where it is above 2^-126, which it may replace by 0 below: the
+// hardware's 2^h, h = x log2(e) rounded, times 1 + r with r = x - h log(2) what the rounding left out.
+__device__ __forceinline__ float exp_normal_f32(float x) {
+    x = __builtin_amdgcn_fmed3f(x, -88.0f, 88.0f);
+    const float h = x * 1.44269504088896341f;
+    const float r = __builtin_fmaf(h, 1.90465429995776804e-9f, __builtin_fmaf(h, -0.693147182464599609f, x));
+    const float e = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(e, r, e);
+}
+
 // 1 / (1 + e^-x) with e^-|x| alone, so that scores below 2^-126 are not lost in the reciprocal.
 __device__ __forceinline__ float sigmoid_f32(float x) {
     const float e = exp_f32(-__builtin_fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
@@ -167,13 +177,12 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     }
     auto score = [&](float x) { return SIGMOID ? sigmoid_f32(x) : exp_f32(x - m) * inv; };
     // choice values: score + bias; without a bias the logits, which order as the scores do and stay
-    // apart where scores round to the same value.  The score in them is formed by the hardware's 2^x alone:
-    // the argument's rounding, |x| 2^-24, moves a sigmoid by s (1 - s) times that and a probability by s
-    // times it, under 2e-8 for every x, less than the sum's own rounding.
-    constexpr float kLog2e = 1.44269504088896341f;
+    // apart where scores round to the same value.  The scores in them are as exact as the weights', except
+    // that those below 2^-126 may count as 0 (a bias of any use is far above): scores by the weights' functions,
+    // which keep those apart, cost 14.3 us for 32768 x 256 instead of 13.2.
     auto choice_score = [&](float x) {
-        if constexpr (SIGMOID) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
-        else return __builtin_amdgcn_exp2f((x - m) * kLog2e) * inv;
+        if constexpr (SIGMOID) return __builtin_amdgcn_rcpf(1.0f + exp_normal_f32(-x));
+        else return exp_normal_f32(x - m) * inv;
     };
     int key[V];
     if (a.bias) {

@@ -233,7 +233,8 @@ int fp8gemm_moe_expert_masked(const void* A, const float* sa, const void* W1, co
  *   s = softmax(logits) over the E experts, or sigmoid(logits);
  *   c = s + bias: the value experts are chosen by.  The bias balances the experts' load and does
  *     not enter the weights.  Without a bias the choice goes by the logits, which order as s does
- *     also where scores round to the same value.
+ *     also where scores round to the same value.  A score in c is within 8 units in the last place, and
+ *     may be 0 below 2^-126: experts whose c are closer than that may stand in either order.
  *   With n_group > 1 the experts are n_group groups of E / n_group consecutive ones; a group's
  *     score is the sum of its group_top (1 or 2) largest c, and only the experts of the
  *     topk_group groups of largest score can be chosen.
@@ -258,9 +259,10 @@ int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, floa
  *   sigmoid, renorm    dlogits[j] = (g_j - sum g p) p_j (1 - s_j)
  *   softmax            dlogits[e] = s_e ([e picked] g_e - sum g s), every expert
  *   softmax, renorm    dlogits[j] = (g_j - sum g p) p_j
- * and 0 elsewhere.  p is formed as route_topk's quotients are (sigmoid: 0 where those are 0; softmax: from
- * the picked logits alone, wherever the token's others lie).  ids as route_topk wrote them: an id outside [0, E) contributes nothing; the
- * ids of a token are distinct (else its row is unspecified). */
+ * and 0 elsewhere.  p is formed as route_topk's quotients are (sigmoid: 0 where those are 0;
+ * softmax: from the picked logits alone, wherever the token's others lie).  ids as route_topk wrote
+ * them: an id outside [0, E) contributes nothing; the ids of a token are distinct (else its row is
+ * unspecified). */
 int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int64_t T,
                                 int32_t E, int32_t k, int32_t dtype, int32_t score, int32_t renorm, float scale,
                                 void* stream);

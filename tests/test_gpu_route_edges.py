@@ -1,5 +1,5 @@
-"""GPU: the router where little can be chosen and where scores are tiny, against the 64-bit implementation
-of the operator's own tests.
+"""GPU: the router where little can be chosen, where scores are tiny, and where the choice is close,
+against the 64-bit implementation of the operator's own tests.
 
 Scores are within 4 units in the last place (2^-21) of the exact ones, a share of renormalised weights
 adds a sum of at most 32 terms and a quotient: relative error below 2^-19.  A score below 2^-126 is
@@ -87,3 +87,26 @@ def test_gradient_of_tiny_scores():
     dx = fg.route_topk_backward(dev(x), dev(ids, "int32"), dev(g), score="sigmoid", renorm=True, scale=2.5)
     ref, mag = gradient(x, ids, g, "sigmoid", True, 2.5)
     assert (np.abs(dx.cpu().numpy() - ref) <= 2.0 ** -18 * mag).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choice_between_close_values(score):
+    """One expert with a tiny score against one whose bias is that score 1.5e-6 of it up or down: three
+    times the scores' and the sum's rounding (4.8e-7 + 0.6e-7), so the choice is decided."""
+    rng = np.random.default_rng(4)
+    R = 120
+    x = (-50 - 36 * rng.random(R)).astype(np.float32)
+    E = 2 * R + 1                                       # the last is out of service, softmax's largest
+    logits = np.full((R, E), -INF, np.float32)
+    bias = np.zeros(E, np.float32)
+    s = 1 / (1 + np.exp(-x.astype(np.float64))) if score == "sigmoid" else np.exp(x.astype(np.float64)) / (1 + np.exp(x.astype(np.float64)))
+    side = np.where(rng.random(R) < 0.5, 1.0, -1.0)
+    at = np.arange(R)
+    logits[at, 2 * at] = x
+    logits[at, 2 * at + 1] = -103.0                     # its own score is below 1e-8 of the other's
+    bias[2 * at + 1] = (s * (1 + 1.5e-6 * side)).astype(np.float32)
+    logits[:, E - 1] = 0.0
+    bias[E - 1] = -INF
+    ids, _ = fg.route_topk(dev(logits), 2, bias=dev(bias), score=score)
+    want = np.where(side > 0, 2 * at + 1, 2 * at)
+    assert np.array_equal(ids[:, 0].cpu().numpy(), want)
