@@ -29,7 +29,10 @@
 //   transpose the words across the four lanes of a row, so that matrix-core step i takes 32
 //   consecutive values.  Codes become the bf16 values 16 + q by inserting them below the
 //   exponent of 16 (exact); the group's sum is then (sum - (16 + z) sum_k x) * scale in fp32, with
-//   sum_k x from one more matrix-core step against ones.
+//   sum_k x from one more matrix-core step against ones.  An infinite x, or |x| near the end of the type, makes
+//   the two sums cancel to NaN or pass fp32's range where sum x (q - z) does not: an output that is not finite
+//   is formed once more, from q - z (a test of each output; nothing else where all are finite: 13 x 7168 x
+//   16384 in 128s takes 25 us, 233 with an infinity in one row, 886 with NaN throughout).
 
 #include <algorithm>
 #include <type_traits>
@@ -82,6 +85,32 @@ __device__ __forceinline__ v4u decode_u4(uint32_t w) {
     o[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
     o[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
     return o;
+}
+// A row of X times a row of codes as the definition has it, q - z first, by a wave: a lane's groups are
+// `lane`, lane + 64, ..., and the lanes' sums are added.
+template <int GROUP, bool ZEROS>
+__device__ __forceinline__ float dot_u4(const uint16_t* x, const uint8_t* w, const uint16_t* scales, const uint8_t* zeros,
+                                        int groups, int lane) {
+    float acc = 0.0f;
+#pragma unroll 1
+    for (int g = lane; g < groups; g += 64) {
+        const float z = ZEROS ? (float)zeros[g] : 8.0f;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int k = g * GROUP; k < (g + 1) * GROUP; k += 8) {
+            const uint32_t q = *reinterpret_cast<const uint32_t*>(w + k / 2);
+            const v4u v = *reinterpret_cast<const v4u*>(x + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum = __builtin_fmaf(__uint_as_float(v[i] << 16), (float)((q >> (8 * i)) & 15u) - z, sum);
+                sum = __builtin_fmaf(__uint_as_float(v[i] & 0xFFFF0000u), (float)((q >> (8 * i + 4)) & 15u) - z, sum);
+            }
+        }
+        acc = __builtin_fmaf(bf16_to_f32(scales[g]), sum, acc);
+    }
+    acc = row16_sum_f(acc);
+    acc += __shfl_xor(acc, 16, 64);
+    return acc + __shfl_xor(acc, 32, 64);
 }
 // 8 bf16 values brought into the same order.
 __device__ __forceinline__ v4u order_u4(const v4u& x) {
@@ -442,7 +471,28 @@ __global__ __launch_bounds__(kThreads, (MULTI && kXSteps<GROUP, MX> == 512 ? 2 :
                 if (ALONE && tile + kWaves < tile_end) last_round(std::true_type());
                 else last_round(std::false_type());
 
-                auto finish = [&](int m, int n, float v, float up) {
+                // output (m, n) of this lane, if it has one (called by whole waves)
+                auto finish = [&](bool there, int m, int n, float v, float up) {
+                    if constexpr (!MX) {
+                        auto wild = [](float f) { return !(__builtin_fabsf(f) < __builtin_inff()); };
+                        for (uint64_t b = __ballot(there && (wild(v) || (SWIGLU && wild(up)))); b; b &= b - 1) {
+                            const int from = __builtin_ctzll(b), mf = __builtin_amdgcn_readlane(m, from);
+                            int64_t row = (int64_t)blockIdx.y * 16 + mf;
+                            if constexpr (MODE != kOne) {
+                                const int p = cols[m0 + mf];
+                                row = a.per_pair ? p : (int)fast_div(p, a.div_k);
+                            }
+#pragma unroll 1
+                            for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+                                const int64_t at = matrix + n0 + __builtin_amdgcn_readlane(n, from) + h * a.half;
+                                const float d = dot_u4<GROUP, ZEROS>(a.X + row * a.K, a.W + at * row_bytes,
+                                                                     static_cast<const uint16_t*>(a.scales) + at * a.groups,
+                                                                     ZEROS ? a.zeros + at * a.groups : nullptr, a.groups, lane);
+                                if (lane == from) (h ? up : v) = d;
+                            }
+                        }
+                    }
+                    if (!there) return;
                     if constexpr (SWIGLU) v = v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v)) * up;
                     const int64_t row = MODE == kOne ? (int64_t)blockIdx.y * 16 + m : cols[m0 + m];
                     a.Y[row * a.nout + n0 + n] = f32_to_bf16(v);
@@ -452,8 +502,8 @@ __global__ __launch_bounds__(kThreads, (MULTI && kXSteps<GROUP, MX> == 512 ? 2 :
                     for (int r = 0; r < (SWIGLU ? 1 : RN); ++r)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            if (j * 4 + q < here && n0 + r * 16 + ln < n_end)
-                                finish(j * 4 + q, r * 16 + ln, acc[r][q], acc[RN - 1][q]);
+                            finish(j * 4 + q < here && n0 + r * 16 + ln < n_end, j * 4 + q, r * 16 + ln, acc[r][q],
+                                   acc[RN - 1][q]);
                 } else {
                     // the waves' sums, added in wave order
                     lds_barrier();
@@ -463,14 +513,15 @@ __global__ __launch_bounds__(kThreads, (MULTI && kXSteps<GROUP, MX> == 512 ? 2 :
                     lds_barrier();
                     for (int o = thread(); o < kTileRows * 16; o += kThreads) {
                         const int n = o % kTileRows, m = o / kTileRows;
-                        if (n0 + n >= n_end || m >= here) continue;
+                        const bool there = n0 + n < n_end && m < here;
                         auto total = [&](int r) {
                             float v = 0.0f;
+                            if (!there) return v;
 #pragma unroll
                             for (int w = 0; w < kWaves; ++w) v += red[w][r][(m >> 2) * 16 + (n & 15)][m & 3];
                             return v;
                         };
-                        finish(m, n, total(SWIGLU ? 0 : n >> 4), SWIGLU ? total(1) : 0.0f);
+                        finish(there, m, n, total(SWIGLU ? 0 : n >> 4), SWIGLU ? total(1) : 0.0f);
                     }
                     break;                               // one tile
                 }

@@ -309,7 +309,10 @@ int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* w
  *     a bf16 value.  Scales below 2^-120 may flush; 255 gives unspecified results.
  *   FP8GEMM_W4_INT4: codes q in 0..15, V = (q - z) * s, scales bf16 [N][K/group], zeros uint8
  *     [N][K/group] (0..15; NULL: 8), group 32, 64 or 128.  A group's sum of x * (q - z) is formed first,
- *     exactly up to fp32 rounding, then scaled.
+ *     in fp32, then scaled.  It is taken as sum x (16 + q) - (16 + z) sum x, so its error is up to 2^-16
+ *     of sum 31 |x|, also where the weights are small or 0.  An output that is not finite is formed once
+ *     more from q - z: infinities, NaN and values near the end of the type follow V (and a row full of
+ *     them takes many times as long).
  * K: a positive multiple of the group (else BAD_SHAPE), at most 2^22; M <= 2^20, N <= 2^24.  X, W and Y 16-byte
  * aligned, scales and zeros 4-byte aligned. */
 int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint8_t* zeros, void* Y, int64_t M, int64_t N,
