@@ -20,6 +20,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxBytes = int64_t(1) << 40;
 constexpr int64_t kMaxPairs = int64_t(1) << 30;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of a launch, in one dimension
 constexpr int64_t kMaxK4 = int64_t(1) << 22;      // 64 rows of a matrix stay below 2^31 bytes
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -32,15 +33,7 @@ int check_route(int64_t T, int32_t E, int32_t k, int32_t dtype, int32_t score, f
     if ((dtype != FP8GEMM_F32 && dtype != FP8GEMM_BF16) ||
         (score != FP8GEMM_SCORE_SOFTMAX && score != FP8GEMM_SCORE_SIGMOID) || !std::isfinite(scale))
         return FP8GEMM_ERR_BAD_SHAPE;
-    if (E > kRouteMaxExperts || k > kRouteMaxTopk || T > kMaxRows) return FP8GEMM_ERR_UNSUPPORTED;
-    return FP8GEMM_OK;
-}
-
-int check_dispatch(int64_t T, int64_t H, int32_t k, int32_t G, int64_t cap) {
-    if (T < 0 || k <= 0 || G <= 0 || cap < 0 || H <= 0 || H % 128 != 0) return FP8GEMM_ERR_BAD_SHAPE;
-    if (k > kDispatchMaxTopk || G > kDispatchMaxGroups || T >= kMaxPairs / k ||
-        H > (int64_t(1) << 24) || 2 * T * H >= kMaxBytes || T * ((H + 2047) / 2048) > kMaxRows)
-        return FP8GEMM_ERR_UNSUPPORTED;
+    if (E > kRouteMaxExperts || k > kRouteMaxTopk || T > kMaxThreads / 16 - 16) return FP8GEMM_ERR_UNSUPPORTED;
     return FP8GEMM_OK;
 }
 
@@ -50,6 +43,15 @@ int check_dispatch(int64_t T, int64_t H, int32_t k, int32_t G, int64_t cap) {
 // H = 2048: 8192 10.7 and 17.1, 16384 23.9 and 21.4; contiguous, 256 experts, H = 7168: 8192 27.2 and 34.4,
 // 16384 71 and 48.
 constexpr int64_t kSmallPairs = 8192;
+
+int check_dispatch(int64_t T, int64_t H, int32_t k, int32_t G, int64_t cap) {
+    if (T < 0 || k <= 0 || G <= 0 || cap < 0 || H <= 0 || H % 128 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (k > kDispatchMaxTopk || G > kDispatchMaxGroups || T >= kMaxPairs / k ||
+        H > (int64_t(1) << 24) || 2 * T * H >= kMaxBytes)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    const int64_t threads = T * k <= kSmallPairs ? row_spans((int)H) * kRowThreads : dispatch_copy_threads((int)H);
+    return T * threads > kMaxThreads ? FP8GEMM_ERR_UNSUPPORTED : FP8GEMM_OK;
+}
 
 int dispatch(DispatchArgs a, hipStream_t stream) {
     HostDevice d;
@@ -81,10 +83,10 @@ int dispatch(DispatchArgs a, hipStream_t stream) {
     return launched();
 }
 
-int check_combine(int64_t T, int64_t H, int32_t k, int64_t R, const int32_t* row_map) {
+int check_combine(int64_t T, int64_t H, int32_t k, int64_t R, const int32_t* row_map, bool backward) {
     if (T < 0 || k <= 0 || R < 0 || H <= 0 || H % 8 != 0) return FP8GEMM_ERR_BAD_SHAPE;
     if (k > kCombineMaxTopk || T > kMaxRows / k || R > kMaxRows || H > (int64_t(1) << 24) || 2 * T * H >= kMaxBytes ||
-        2 * R * H >= kMaxBytes || T * ((H + 2047) / 2048) > kMaxRows)
+        2 * R * H >= kMaxBytes || T * (backward ? 1 : row_spans((int)H)) * kRowThreads > kMaxThreads)
         return FP8GEMM_ERR_UNSUPPORTED;
     if (!row_map && R < T * k) return FP8GEMM_ERR_BAD_SHAPE;
     return FP8GEMM_OK;
@@ -270,7 +272,7 @@ int fp8gemm_moe_dispatch_contiguous(const void* X, const int32_t* ids, void* A, 
 
 int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_map, void* out, int64_t T, int64_t H,
                         int32_t k, int64_t R, void* stream) {
-    int st = check_combine(T, H, k, R, row_map);
+    int st = check_combine(T, H, k, R, row_map, false);
     if (st != FP8GEMM_OK) return st;
     if (T == 0) return FP8GEMM_OK;
     if (!out || (R > 0 && !Y)) return FP8GEMM_ERR_NULL_PTR;
@@ -295,7 +297,7 @@ int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_
 
 int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* weights, const int32_t* row_map, void* dY,
                                  float* dweights, int64_t T, int64_t H, int32_t k, int64_t R, void* stream) {
-    int st = check_combine(T, H, k, R, row_map);
+    int st = check_combine(T, H, k, R, row_map, true);
     if (st != FP8GEMM_OK) return st;
     if (T == 0) return FP8GEMM_OK;
     if (!dout || (R > 0 && (!dY || (dweights && !Y)))) return FP8GEMM_ERR_NULL_PTR;

@@ -61,6 +61,11 @@ void launch_route_topk(const RouteArgs& a, bool bf16, bool sigmoid, hipStream_t 
 void launch_route_backward(const RouteBackwardArgs& a, bool bf16, bool sigmoid, hipStream_t s);
 
 // ---- token permutation ----
+// The row passes: a workgroup of kRowThreads takes kRowSpan bf16 values of a row, 16 bytes a thread.
+constexpr int kRowThreads = 256, kRowSpan = kRowThreads * 8;
+inline int64_t row_spans(int H) { return (H + kRowSpan - 1) / kRowSpan; }
+// Threads of the large dispatch's workgroup per token: 16 values each, in whole waves.
+inline int dispatch_copy_threads(int H) { return H >= 16384 ? 1024 : (H / 16 + 63) / 64 * 64; }
 constexpr int kDispatchMaxGroups = 1024;
 constexpr int kDispatchMaxTopk = 32;
 

@@ -24,9 +24,9 @@ namespace {
 
 // Workgroup size of the row passes with 16 bytes of bf16 per thread: 16 lanes own a 128-value block, and
 // a wave's load is 1 KB of consecutive memory.
-constexpr int kThreads = 256;
+constexpr int kThreads = kRowThreads;
 constexpr int64_t kCacheBytes = 256 << 20;   // the memory-side cache
-constexpr int kSpan = kThreads * 8;      // elements of a row one workgroup handles per pass
+constexpr int kSpan = kRowSpan;          // elements of a row one workgroup handles per pass
 
 // Correctly rounded x / s for one E4M3 conversion: with r = RN(1/s) and q = RN(x r), one
 // residual step gives RN(x / s) (Markstein, "Computation of elementary functions on the IBM RISC
@@ -546,12 +546,10 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(CombineArgs a
     }
 }
 
-int spans_of(int H) { return (H + kSpan - 1) / kSpan; }
-
 }  // namespace
 
 void launch_dispatch(const DispatchArgs& a, bool large, hipStream_t s) {
-    const int spans = spans_of(a.H);
+    const int spans = (int)row_spans(a.H);
     const dim3 grid((unsigned)(a.T * spans));
     if (a.T == 0) {
         const int n = a.contiguous ? a.cap : a.G;
@@ -566,8 +564,7 @@ void launch_dispatch(const DispatchArgs& a, bool large, hipStream_t s) {
     }
     hipLaunchKernelGGL(dispatch_count_kernel, dim3((unsigned)a.chunks), dim3(kThreads), 0, s, a);
     hipLaunchKernelGGL(dispatch_scan_kernel, dim3(1), dim3(1024), 0, s, a);
-    const int threads = std::min(1024, (a.H / 16 + 63) / 64 * 64);
-    hipLaunchKernelGGL(dispatch_copy_kernel, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, a);
+    hipLaunchKernelGGL(dispatch_copy_kernel, dim3((unsigned)a.T), dim3((unsigned)dispatch_copy_threads(a.H)), 0, s, a);
     if (a.by_row) {
         const int64_t tiles = (int64_t)(a.contiguous ? 1 : a.G) * ((a.cap + kTurnRows - 1) / kTurnRows);
         const dim3 turn((unsigned)tiles, (unsigned)((a.nkb + kTurnBlocks - 1) / kTurnBlocks));
@@ -576,7 +573,7 @@ void launch_dispatch(const DispatchArgs& a, bool large, hipStream_t s) {
 }
 
 void launch_combine(const CombineArgs& a, hipStream_t s) {
-    const int spans = spans_of(a.H);
+    const int spans = (int)row_spans(a.H);
     const dim3 grid((unsigned)(a.T * spans));
     if (2 * a.T * a.k * a.H > kCacheBytes) hipLaunchKernelGGL(combine_kernel<true>, grid, dim3(kThreads), 0, s, a, spans);
     else hipLaunchKernelGGL(combine_kernel<false>, grid, dim3(kThreads), 0, s, a, spans);

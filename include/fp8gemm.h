@@ -82,9 +82,10 @@ typedef enum fp8gemm_status {
     FP8GEMM_ERR_MISALIGNED = 3,  /* A, B or D not 16-byte aligned, or a scale/index vector not 4-byte aligned */
     FP8GEMM_ERR_UNSUPPORTED = 4, /* a size beyond the supported range (an operand of 2^40 bytes or more, K > 2^24,
                                     2^30 or more output tiles x K splits in one launch, 2^31 or more
-                                    128-value blocks in one quantiser call, a forced launch shape whose
-                                    split-K partials exceed the stream's workspace), or a split-K call
-                                    on an unprepared stream during graph capture */
+                                    128-value blocks in one quantiser call, a launch of 2^32 threads or more,
+                                    a forced launch shape whose split-K partials, or a dispatch whose counts,
+                                    exceed the stream's workspace), or a call that needs the workspace of
+                                    an unprepared stream during graph capture */
     FP8GEMM_ERR_LAUNCH = 5,      /* the HIP launch failed (hipGetLastError after the launch) */
     FP8GEMM_ERR_HIP = 6          /* a HIP runtime call failed (device query, workspace allocation, copy) */
 } fp8gemm_status;
@@ -245,7 +246,7 @@ int fp8gemm_moe_expert_masked(const void* A, const float* sa, const void* W1, co
  * Equal values go to the lower index, for groups and experts.  A NaN counts as -infinity and
  * +infinity as the largest finite value, in logits and bias.  An expert whose logit or bias is
  * -infinity cannot be chosen; where fewer than k can, the remaining ids are -1 and weights 0.
- * E <= 1024, k <= 32, n_group <= 64 (else UNSUPPORTED); k at most the experts of topk_group
+ * E <= 1024, k <= 32, n_group <= 64, T <= 2^28 - 17 (else UNSUPPORTED); k at most the experts of topk_group
  * groups, group_top at most a group's size (else BAD_SHAPE).  logits need the alignment of their
  * type only. */
 int fp8gemm_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights, int64_t T, int32_t E,
@@ -280,7 +281,10 @@ int fp8gemm_route_topk_backward(const void* logits, const int32_t* ids, const fl
  * A pair past the capacity is dropped (row -1; masked_m is at most M_max) and flags
  * FP8GEMM_DEVERR_BAD_COUNT.  Rows of A and entries of sa that no pair goes to are left untouched.
  * X must hold finite values.  H: a positive multiple of 128; k <= 32, G <= 1024.  X and A 16-byte
- * aligned.  Batches of more than 8192 pairs use the stream's workspace (see fp8gemm_prepare_stream). */
+ * aligned.  Batches of more than 8192 pairs use the stream's workspace (see fp8gemm_prepare_stream),
+ * which has to hold T * k + G * ceil(T * k / 1024) + 2 G words (on 256 CUs 16.7 million pairs for 1024
+ * experts), and T times min(1024, H / 16 rounded up to 64) has to be below 2^32; for fewer pairs T times
+ * ceil(H / 2048) below 2^24 (else UNSUPPORTED). */
 int fp8gemm_moe_dispatch_masked(const void* X, const int32_t* ids, void* A, float* sa, int32_t* masked_m,
                                 int32_t* row_map, int64_t T, int64_t H, int32_t k, int32_t G, int64_t M_max,
                                 int32_t first_expert, void* stream);
@@ -292,7 +296,8 @@ int fp8gemm_moe_dispatch_contiguous(const void* X, const int32_t* ids, void* A, 
  * j; pairs whose row is -1 are left out (a token without any gets zeros).  Y [R][H] bf16 (any
  * grouped output, flattened), out [T][H] bf16.  weights NULL: ones (also the gradient of a
  * dispatch with respect to X); row_map NULL: row t * k + j.  A row of R or more is left out and
- * flags FP8GEMM_DEVERR_BAD_INDEX.  H: a positive multiple of 8; k <= 32; Y, out 16-byte aligned. */
+ * flags FP8GEMM_DEVERR_BAD_INDEX.  H: a positive multiple of 8; k <= 32 and T * ceil(H / 2048) < 2^24
+ * (the gradients: T < 2^24; else UNSUPPORTED); Y, out 16-byte aligned. */
 int fp8gemm_moe_combine(const void* Y, const float* weights, const int32_t* row_map, void* out, int64_t T, int64_t H,
                         int32_t k, int64_t R, void* stream);
 

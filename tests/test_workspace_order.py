@@ -21,9 +21,9 @@ def compiled(tmp_path):
     return so
 
 
-def in_a_process(tmp_path, name):
-    """Run a function of this file where the recording calls are found before the real ones."""
-    r = subprocess.run([sys.executable, os.path.abspath(__file__), name, compiled(tmp_path)], capture_output=True, text=True,
+def in_a_process(tmp_path, name, file=__file__):
+    """Run a function of a test file where the recording calls are found before the real ones."""
+    r = subprocess.run([sys.executable, os.path.abspath(file), name, compiled(tmp_path)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
 
