@@ -14,9 +14,10 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <map>
 #include <memory>
 #include <mutex>
-#include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "fp8gemm.h"
@@ -37,6 +38,14 @@ struct Workspace {
     size_t counter_count = 0;
 };
 
+// A stream as the device sees it: the per-thread default stream is another one in every host thread.
+using StreamKey = std::pair<hipStream_t, uint64_t>;
+StreamKey stream_key(hipStream_t stream) {
+    static std::atomic<uint64_t> threads{0};
+    thread_local const uint64_t me = ++threads;
+    return {stream, stream == hipStreamPerThread ? me : 0};
+}
+
 struct DeviceState {
     std::mutex mu;
     bool ready = false;
@@ -45,7 +54,7 @@ struct DeviceState {
     int32_t* err = nullptr;                              // device error word (static device memory)
     ScratchPointers scratch;                             // static split-K scratch of fp8gemm_nt_noalloc
     std::vector<int> occupancy;                          // per kernel-table entry
-    std::unordered_map<hipStream_t, std::unique_ptr<Workspace>> ws;
+    std::map<StreamKey, std::unique_ptr<Workspace>> ws;
 };
 
 DeviceState g_dev[kMaxDevices];
@@ -152,7 +161,8 @@ size_t workspace_counters(int cus) { return std::max<size_t>((size_t)cus, 4096);
 int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t counters, Workspace** out,
               std::unique_lock<std::mutex>* hold) {
     std::unique_lock<std::mutex> lock(d->mu);
-    auto it = d->ws.find(stream);
+    const StreamKey key = stream_key(stream);
+    auto it = d->ws.find(key);
     if (it == d->ws.end()) {
         hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &cs) != hipSuccess) return FP8GEMM_ERR_HIP;
@@ -174,7 +184,7 @@ int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t c
         }
         w.partial_bytes = bytes;
         w.counter_count = n;
-        it = d->ws.emplace(stream, std::move(made)).first;
+        it = d->ws.emplace(key, std::move(made)).first;
     }
     Workspace& w = *it->second;
     lock.unlock();                                       // a workspace is never removed; other streams go on

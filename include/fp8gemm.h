@@ -35,7 +35,8 @@
  *     The launch configuration itself depends on the shape, the device's CU count and the CU
  *     cap, so a different cap (or stream-K turned off) may sum the same products in another
  *     order, within the same tolerance.
- *   - Stream workspace: each stream has its own library-owned workspace (fp32 partial tiles
+ *   - Stream workspace: each stream (hipStreamPerThread: each host thread's, held until the
+ *     process ends) has its own library-owned workspace (fp32 partial tiles
  *     and arrival counters, CUs x 512 KiB + 16 KiB on the stream's device).  It serves the
  *     K splits of decode-sized launches, the stream-K schedule of large dense launches (the
  *     256-row tiles left over after the last full round of tiles, shared out over every CU

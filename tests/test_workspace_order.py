@@ -116,5 +116,27 @@ def test_streams_do_not_wait_for_each_other(tmp_path):
     in_a_process(tmp_path, "_streams_do_not_wait")
 
 
+def _per_thread_stream(so):
+    """The per-thread default stream is a stream of its own in every host thread, with its own workspace (two
+    allocations); other streams' are shared by the threads."""
+    r = Recorded(so)
+    r.hip.record_pause(0)
+    per_thread = 2                                   # hipStreamPerThread
+    for stream, workspaces in ((0x1230, 1), (per_thread, 3), (None, 1)):
+        before = r.hip.record_allocations()
+        for _ in range(2):
+            assert r.split_k(stream) == 0 and r.dispatch(stream) == 0
+        threads = [threading.Thread(target=lambda: (r.split_k(stream), r.dispatch(stream), r.split_k(stream))) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(120)
+        assert r.hip.record_allocations() - before == 2 * workspaces, stream
+
+
+def test_the_per_thread_stream_has_a_workspace_per_thread(tmp_path):
+    in_a_process(tmp_path, "_per_thread_stream")
+
+
 if __name__ == "__main__":
     globals()[sys.argv[1]](sys.argv[2])
