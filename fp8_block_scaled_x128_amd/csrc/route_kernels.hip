@@ -159,14 +159,17 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     load_row<BF16, V, P>(a.logits, base, a.E, l, s);
 
     // scores: sigmoid(x), or exp(x - m) * inv with m and inv = 1 / sum of the token's softmax; the sum
-    // is formed only where scores are used as such (a renormalised weight cancels it)
-    float m = 0.0f, inv = 1.0f;
+    // is formed only where scores are used as such (a renormalised weight cancels it).  Any m serves that keeps
+    // the powers in range: 0 where the largest logit is 0 to 60, as x - m loses up to |x - m| 2^-24 of a score.
+    float m = 0.0f, top = 0.0f, inv = 1.0f;
     if constexpr (!SIGMOID) {
         m = kNegInf;
 #pragma unroll
         for (int i = 0; i < V; ++i) m = fmaxf(m, s[i]);
         m = row16_max_f(m);
         if (m == kNegInf) m = 0.0f;   // a row with no finite logit: every score is 0
+        top = m;
+        if (m >= 0.0f && m <= 60.0f) m = 0.0f;
         if (!a.renorm || a.bias || (a.n_group > 1 && a.group_top == 2)) {
             float sum = 0.0f;
 #pragma unroll
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(WAVES * 64) void route_topk_kernel(RouteArgs a) {
     float w0, w1 = 0.0f;
     if (a.renorm) {
         const float most = row16_max_f(fmaxf(x0, x1));
-        const bool none = most - m < kNoScore;           // no pick, or every one's score is 0 (m is 0 for sigmoid)
+        const bool none = most - top < kNoScore;         // no pick, or every one's score is 0 (top is 0 for sigmoid)
         w0 = share_f32<SIGMOID>(x0, most);
         if (a.k > 16) w1 = share_f32<SIGMOID>(x1, most);
         const float sum = row16_sum_f(w0 + w1);

@@ -235,8 +235,9 @@ int fp8gemm_moe_expert_masked(const void* A, const float* sa, const void* W1, co
  *   s = softmax(logits) over the E experts, or sigmoid(logits);
  *   c = s + bias: the value experts are chosen by.  The bias balances the experts' load and does
  *     not enter the weights.  Without a bias the choice goes by the logits, which order as s does
- *     also where scores round to the same value.  A score in c is within 8 units in the last place, and
- *     may be 0 below 2^-126: experts whose c are closer than that may stand in either order.
+ *     also where scores round to the same value.  A score in c is within 8 units in the last place (softmax
+ *     whose largest logit is not in [0, 60]: and 2^-24 |logit - largest| of itself), and may be 0 below
+ *     2^-126: experts whose c are closer than that may stand in either order.
  *   With n_group > 1 the experts are n_group groups of E / n_group consecutive ones; a group's
  *     score is the sum of its group_top (1 or 2) largest c, and only the experts of the
  *     topk_group groups of largest score can be chosen.

@@ -110,3 +110,25 @@ def test_choice_between_close_values(score):
     ids, _ = fg.route_topk(dev(logits), 2, bias=dev(bias), score=score)
     want = np.where(side > 0, 2 * at + 1, 2 * at)
     assert np.array_equal(ids[:, 0].cpu().numpy(), want)
+
+
+def test_choice_between_close_values_far_below_the_largest():
+    """The same for softmax below a largest logit that is not 0: the score's two powers and the quotient make
+    7e-7 at most, less than half of the difference."""
+    rng = np.random.default_rng(5)
+    R = 120
+    x = (-46 - 24 * rng.random(R)).astype(np.float32)
+    E = 2 * R + 1
+    top = np.float32(11.7)
+    logits = np.full((R, E), -INF, np.float32)
+    bias = np.zeros(E, np.float32)
+    s = np.exp(x.astype(np.float64)) / (np.exp(x.astype(np.float64)) + np.exp(float(top)))
+    side = np.where(rng.random(R) < 0.5, 1.0, -1.0)
+    at = np.arange(R)
+    logits[at, 2 * at] = x
+    logits[at, 2 * at + 1] = -100.0
+    bias[2 * at + 1] = (s * (1 + 1.5e-6 * side)).astype(np.float32)
+    logits[:, E - 1] = top
+    bias[E - 1] = -INF
+    ids, _ = fg.route_topk(dev(logits), 2, bias=dev(bias), score="softmax")
+    assert np.array_equal(ids[:, 0].cpu().numpy(), np.where(side > 0, 2 * at + 1, 2 * at))
