@@ -424,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_scales_kernel(DispatchArgs 
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        v[i] = token[i] >= 0 && token[i] < a.T && kb0 + kb < a.nkb ? sc.scales[(int64_t)token[i] * a.nkb + kb0 + kb] : 0.0f;
+        v[i] = (uint32_t)token[i] < (uint32_t)a.T && kb0 + kb < a.nkb ? sc.scales[(int64_t)token[i] * a.nkb + kb0 + kb] : 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) tile[r1 + i * kPass][kb] = v[i];
     __syncthreads();

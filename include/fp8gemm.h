@@ -313,7 +313,8 @@ int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* w
  * decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N] bf16, W [N][K/2] bytes, the even element of a row in the low nibble:
  *   FP8GEMM_W4_MXFP4: E2M1 codes, scales uint8 [N][K/32] (E8M0), the B and sb of
  *     fp8gemm_fp8fp4_grouped_masked; group = 32, zeros NULL.  Products are exact: a decoded value is
- *     a bf16 value.  Scales below 2^-120 may flush; 255 gives unspecified results.
+ *     a bf16 value, infinite from 2^128 on (scale bytes 253 and 254).  Scales below 2^-120 may flush;
+ *     255 gives unspecified results.
  *   FP8GEMM_W4_INT4: codes q in 0..15, V = (q - z) * s, scales bf16 [N][K/group], zeros uint8
  *     [N][K/group] (0..15; NULL: 8), group 32, 64 or 128.  A group's sum of x * (q - z) is formed first,
  *     in fp32, then scaled.  It is taken as sum x (16 + q) - (16 + z) sum x, so its error is up to 2^-16
