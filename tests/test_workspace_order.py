@@ -23,6 +23,9 @@ def compiled(tmp_path):
 
 def in_a_process(tmp_path, name, file=__file__):
     """Run a function of a test file where the recording calls are found before the real ones."""
+    lib = os.path.join(os.path.dirname(HERE), "fp8_block_scaled_x128_amd", "libfp8gemm.so")
+    if not os.path.exists(lib):
+        subprocess.check_call([sys.executable, "-m", "fp8_block_scaled_x128_amd.build"], cwd=os.path.dirname(HERE))
     r = subprocess.run([sys.executable, os.path.abspath(file), name, compiled(tmp_path)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
