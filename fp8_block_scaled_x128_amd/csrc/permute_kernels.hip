@@ -9,9 +9,9 @@
 // pairs, scan the counts, copy, and put the scales in place, in four launches.
 //
 // Bound: memory, with next to no arithmetic (the quantiser's is hidden).  4095 x 8 x 7168 on 64 experts
-// 69.3 us, 4.35 TB/s (count 5, scan 4, copy 52, scales 7); 128 x 8 x 7168 on 16 experts 5.2 us, a launch
-// and the pass over the picks; combine 4096 x 8 x 7168 103.6 us, 5.1 TB/s, and 128 x 8 x 7168 6.7 us from
-// the memory-side cache; its gradient 1000 x 6 x 2048 11.7 us, 4.5 TB/s.
+// 66 to 71 us, 4.2 to 4.6 TB/s (count 5, scan 5, copy 53, scales 6); 128 x 8 x 7168 on 16 experts 5.1 us, a
+// launch and the pass over the picks; combine 4096 x 8 x 7168 102.4 us, 5.15 TB/s, and 128 x 8 x 7168 6.8 us
+// with Y's rows in the memory-side cache; its gradient 1000 x 6 x 2048 11.6 us, 4.6 TB/s.
 
 #include <algorithm>
 

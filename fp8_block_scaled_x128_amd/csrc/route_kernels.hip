@@ -11,12 +11,13 @@
 // whole chunks take their scores from the chunks' two best values, merged across the group's
 // lanes, and strike out whole chunk maxima.  Where 16 lanes divided by the groups (rounded up to a
 // power of two) hold a group, it is given those lanes' chunks to itself, with places left free after
-// it (32768 x 160 in 8 groups: 12.7 us, against 16.2 with groups scanned in LDS by a lane each, which
-// stays for the others).
+// it (32768 x 160 bf16 softmax, bias, 3 of 8 groups, 6 picks: 14.4 us, against 16.9 with groups scanned in
+// LDS by a lane each, which stays for the others).
 //
-// Bound: instructions, then memory: a lane spends about 20 on each expert's score and place and 30 on
-// each pick.  32768 x 256 fp32, bias, 4 of 8 groups, 8 picks: 13.3 us, 2.7 TB/s; a single token 4.2 us,
-// its picks' chain of dependent steps past a launch's 2.8 us; gradient 8191 x 160 bf16, 6 picks: 4.1 us.
+// Bound: instructions, then memory: 32768 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 picks: 13.2 us,
+// 2.7 TB/s, 850 vector instructions a wave of 4 tokens, about 30 of them for each pick and the rest for a
+// lane's 16 experts' scores, keys and places; a single token 4.4 us, its picks' chain of dependent steps past
+// a launch's 2.8 us; gradient 8191 x 160 bf16, 6 picks: 4.1 us.
 
 #include "fp8gemm_device.h"
 #include "fp8gemm_internal.h"

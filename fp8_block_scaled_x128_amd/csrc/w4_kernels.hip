@@ -12,14 +12,15 @@
 // values of K, 64 bytes of a row; a pair is one 128-byte line) in turn, each with all RN row
 // tiles, and keep PP pairs in registers on their way, up to 64 KB per workgroup of 8 waves.  X's
 // values stand in LDS, all of them or by chunks: read from the caches step by step by the lanes that
-// need them they cost 27.8 us for 13 x 7168 x 16384 (MXFP4), from LDS 22.1.  The waves' fp32 sums
+// need them they cost 27.8 us for 13 x 7168 x 16384 (MXFP4), from LDS 22.  The waves' fp32 sums
 // meet in LDS and are added in wave order.  Splitting K over workgroups was measured and dropped:
 // the exchange of sums costs 2 us, more than the idle CUs of a small matrix do.
 //
-// 1 x 32768 x 7168 MXFP4 24 us, 5.2 TB/s; 1 x 4096 x 7168 INT4 in 128s 7.5 us, a launch, the way of X into
-// LDS and the exchange of sums around 3.2 us of weights; 13 x 7168 x 16384 MXFP4 20 us, 224 workgroups on
-// 256 CUs; 8 experts' 4096 x 7168 for a token, MXFP4 with SwiGLU, 28 us, 4.5 TB/s; 128 pairs of 7168 x 2048
-// on 64 experts, INT4 in 64s with zero points, 106 us, 4.3 TB/s, its decoding 5 lane operations a weight.
+// 1 x 32768 x 7168 MXFP4 24 us, 5.2 TB/s; 1 x 4096 x 7168 INT4 in 128s 7.6 us, a launch, the way of X into
+// LDS and the exchange of sums around 3.1 us of weights; 13 x 7168 x 16384 MXFP4 22 us: 224 workgroups on
+// 256 CUs, and 98 MB of X through L2 into their LDS beside 66 from HBM; 8 experts' 4096 x 7168 for a token,
+// MXFP4 with SwiGLU, 28 us, 4.5 TB/s; 128 pairs of 7168 x 2048 on 64 experts, INT4 in 64s with zero points,
+// 107 us, 4.2 TB/s, its decoding 5 lane operations a weight.
 //
 // In a step lane (n, j) = (lane % 16, lane / 16) loads 16 bytes of row n: its chunk j of 32 values.
 //   MXFP4: the lane decodes its 32 values with their scale in the conversion instruction (two
@@ -54,8 +55,8 @@ constexpr int kStep = 128;                 // K values per wave and step: four r
 // X past this many bytes stands in LDS by chunks of kXSteps steps x rows (256 bytes each).  64 KB chunks leave
 // room for a second workgroup on the CU, which hides the chunk's change; INT4 in groups of 32 and 64 has too
 // few registers for that beside X's values on their way, and takes 128 KB.  Measured, 64 and 128 KB, us:
-// MXFP4 12 x 16384 x 4096 12.1 and 16.2, 16 x 32768 x 7168 38.5 and 42.3, 13 x 7168 x 16384 22.5 and 23.2;
-// INT4 in 128s 12 x 16384 x 4096 13.6 and 19.3, but in 32s 19.2 and 11.6 for 16 x 7168 x 4096 (spills).
+// MXFP4 12 x 16384 x 4096 12.1 and 16.3, 16 x 32768 x 7168 38.4 and 42.5, 13 x 7168 x 16384 22.8 and 23.6;
+// INT4 in 128s 12 x 16384 x 4096 13.8 and 19.2, but in 32s 20.1 and 11.4 for 16 x 7168 x 4096 (spills).
 template <int GROUP, bool MX>
 constexpr int kXSteps = MX || GROUP == 128 ? 256 : 512;
 template <int GROUP, bool MX>

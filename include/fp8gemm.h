@@ -310,7 +310,8 @@ int fp8gemm_moe_combine_backward(const void* dout, const void* Y, const float* w
                                  float* dweights, int64_t T, int64_t H, int32_t k, int64_t R, void* stream);
 
 /* Y[m][n] = bf16(sum_k X[m][k] V[n][k]) for few rows of X (the weights are read once per 16 rows), V
- * decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N] bf16, W [N][K/2] bytes, the even element of a row in the low nibble:
+ * decoded from 4-bit codes, the sum in fp32.  X [M][K] bf16, Y [M][N] bf16, W [N][K/2] bytes, the even
+ * element of a row in the low nibble:
  *   FP8GEMM_W4_MXFP4: E2M1 codes, scales uint8 [N][K/32] (E8M0), the B and sb of
  *     fp8gemm_fp8fp4_grouped_masked; group = 32, zeros NULL.  Products are exact: a decoded value is
  *     a bf16 value, infinite from 2^128 on (scale bytes 253 and 254).  Scales below 2^-120 may flush;
