@@ -17,6 +17,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -167,24 +168,25 @@ int workspace(DeviceState* d, hipStream_t stream, size_t partial_bytes, size_t c
         hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &cs) != hipSuccess) return FP8GEMM_ERR_HIP;
         if (cs != hipStreamCaptureStatusNone) return FP8GEMM_ERR_UNSUPPORTED;
-        auto made = std::make_unique<Workspace>();
-        Workspace& w = *made;
-        const size_t bytes = workspace_partial_bytes(d->cus);
-        const size_t n = workspace_counters(d->cus);
-        if (hipMalloc(&w.partials, bytes) != hipSuccess) return FP8GEMM_ERR_HIP;
-        // on a failure, release what was allocated (the first error is the one reported)
-        if (hipMalloc(&w.counters, n * sizeof(int32_t)) != hipSuccess) {
-            (void)hipFree(w.partials);
+        try {
+            it = d->ws.emplace(key, std::make_unique<Workspace>()).first;
+        } catch (const std::bad_alloc&) {
             return FP8GEMM_ERR_HIP;
         }
-        if (hipMemset(w.counters, 0, n * sizeof(int32_t)) != hipSuccess) {
+        Workspace& w = *it->second;
+        w.partial_bytes = workspace_partial_bytes(d->cus);
+        w.counter_count = workspace_counters(d->cus);
+        if (hipMalloc(&w.partials, w.partial_bytes) != hipSuccess ||
+            hipMalloc(&w.counters, w.counter_count * sizeof(int32_t)) != hipSuccess ||
+            hipMemset(w.counters, 0, w.counter_count * sizeof(int32_t)) != hipSuccess) {
+            // nothing stays: what was allocated is released, and the runtime's last error, which the status
+            // reports, is taken back (the next launch's check would find it)
             (void)hipFree(w.partials);
             (void)hipFree(w.counters);
+            (void)hipGetLastError();
+            d->ws.erase(it);
             return FP8GEMM_ERR_HIP;
         }
-        w.partial_bytes = bytes;
-        w.counter_count = n;
-        it = d->ws.emplace(key, std::move(made)).first;
     }
     Workspace& w = *it->second;
     lock.unlock();                                       // a workspace is never removed; other streams go on

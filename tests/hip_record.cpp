@@ -20,7 +20,10 @@ std::mutex mu;
 std::vector<Launch> launches;
 std::atomic<uint64_t> next_address{uint64_t(1) << 40};
 std::atomic<int> allocations{0};
+std::atomic<int> frees{0};
+std::atomic<int> fail_after{-1};                 // allocations that still succeed, or -1: all do
 std::atomic<int> pause_us{500};
+thread_local hipError_t last_error = hipSuccess; // as the runtime keeps it: until it is asked for
 
 struct Config {
     dim3 grid, block;
@@ -42,6 +45,8 @@ int64_t record_launches(int64_t first, int64_t* out, int64_t room) {
 }
 void record_pause(int us) { pause_us = us; }
 int record_allocations() { return allocations; }
+int record_frees() { return frees; }
+void record_fail_after(int n) { fail_after = n; }
 
 hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t shared, hipStream_t stream) {
     config = {grid, block, shared, stream};
@@ -63,7 +68,11 @@ hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t, h
     if (pause_us > 0) usleep(pause_us);
     return hipSuccess;
 }
-hipError_t hipGetLastError() { return hipSuccess; }
+hipError_t hipGetLastError() {
+    const hipError_t e = last_error;
+    last_error = hipSuccess;
+    return e;
+}
 hipError_t hipGetDevice(int* device) {
     *device = 0;
     return hipSuccess;
@@ -82,11 +91,15 @@ hipError_t hipGetSymbolAddress(void** address, const void*) {
     return hipSuccess;
 }
 hipError_t hipMalloc(void** p, size_t) {
+    if (fail_after >= 0 && fail_after-- == 0) return last_error = hipErrorOutOfMemory;
     ++allocations;
     *p = reinterpret_cast<void*>(next_address.fetch_add(uint64_t(1) << 32));
     return hipSuccess;
 }
-hipError_t hipFree(void*) { return hipSuccess; }
+hipError_t hipFree(void* p) {
+    if (p) ++frees;
+    return hipSuccess;
+}
 hipError_t hipMemset(void*, int, size_t) { return hipSuccess; }
 hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* status) {
     *status = hipStreamCaptureStatusNone;

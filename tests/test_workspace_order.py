@@ -141,5 +141,26 @@ def test_the_per_thread_stream_has_a_workspace_per_thread(tmp_path):
     in_a_process(tmp_path, "_per_thread_stream")
 
 
+def _failed_allocation(so):
+    """Where a workspace cannot be allocated the call reports it, nothing is kept, and the next calls go on."""
+    r = Recorded(so)
+    r.hip.record_pause(0)
+    for first in (0, 1):                             # the partials' allocation fails; the counters' does
+        stream = 0x1000 + first
+        r.hip.record_fail_after(first)
+        before, frees, n = r.hip.record_allocations(), r.hip.record_frees(), len(r.launches())
+        assert r.split_k(stream) == 6                # FP8GEMM_ERR_HIP
+        assert len(r.launches()) == n and r.hip.record_allocations() - before == r.hip.record_frees() - frees == first
+        r.hip.record_fail_after(-1)
+        route = r.lib.fp8gemm_route_topk(FAKE, None, FAKE, FAKE, 4, 64, 2, 0, 0, 1, 1, 1, 1, 1.0, stream)
+        assert route == 0                            # the failure before is not its own
+        assert r.dispatch(stream) == 0 and r.split_k(stream) == 0
+        assert r.hip.record_allocations() - before == first + 2
+
+
+def test_a_failed_allocation_leaves_nothing(tmp_path):
+    in_a_process(tmp_path, "_failed_allocation")
+
+
 if __name__ == "__main__":
     globals()[sys.argv[1]](sys.argv[2])
