@@ -20,6 +20,8 @@ C ABI declared in include/fp8gemm.h.  torch supplies device memory and the curre
     dY, dw = moe_combine_backward(dout, Y, w, rows)              # and its gradients
     Y = w4_gemv(X, W4, scales, zeros)                            # few rows times 4-bit weights
     Y = w4_gemv_experts(X, W4, scales, ids, zeros, swiglu=True)  # the same, by the router's ids
+    H = gated_ffn(X, W, act="silu", pre=pre)                     # act(X Wg^T) * (X Wu^T) in bf16
+    dX, dW = gated_ffn_backward(dH, X, W, pre)                   # and its gradients
 
 A and B are E4M3 codes (torch.float8_e4m3fn or uint8), sa one fp32 scale per 1x128 block of a
 row of A stored K-block-major (sa[kb, m], shape [K/128, M]), sb one per 128x128 block of B (page "DeepSeek開源第三彈：V3/R1訓練推理關鍵秘籍，核心代碼僅
@@ -35,7 +37,8 @@ __all__ = ["gemm_nt", "gemm_nt_noalloc", "gemm_nt_specialized", "specialize_nt",
            "grouped_contiguous", "grouped_masked", "quantize_1x128",
            "quantize_1x128_masked", "fp8fp4_grouped_masked", "swiglu_quantize_1x128", "swiglu_quantize_1x128_masked",
            "moe_expert_masked", "route_topk", "route_topk_backward", "moe_dispatch_masked",
-           "moe_dispatch_contiguous", "moe_combine", "moe_combine_backward", "w4_gemv", "w4_gemv_experts", "init", "prepare_stream", "set_num_cus",
+           "moe_dispatch_contiguous", "moe_combine", "moe_combine_backward", "w4_gemv", "w4_gemv_experts",
+           "gated_ffn", "gated_ffn_backward", "init", "prepare_stream", "set_num_cus",
            "last_config", "read_device_error", "status_string", "lib", "library_path",
            "Fp8GemmError", "STATUS", "DEVERR_BAD_INDEX", "DEVERR_BAD_COUNT"]
 
@@ -77,6 +80,8 @@ SIGNATURES = {
     "fp8gemm_moe_combine_backward": (ctypes.c_int, [_P] * 6 + [_I64, _I64, _I32, _I64, _P]),
     "fp8gemm_w4_gemv": (ctypes.c_int, [_P] * 5 + [_I64, _I64, _I64, _I32, _I32, _P]),
     "fp8gemm_w4_gemv_experts": (ctypes.c_int, [_P] * 6 + [_I64, _I32, _I32, _I64, _I64] + [_I32] * 5 + [_P]),
+    "fp8gemm_gated_ffn": (ctypes.c_int, [_P] * 4 + [_I64, _I64, _I64, _I32, _P]),
+    "fp8gemm_gated_ffn_backward": (ctypes.c_int, [_P] * 7 + [_I64, _I64, _I64, _I32, _P]),
     "fp8gemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8gemm_init": (ctypes.c_int, []),
     "fp8gemm_prepare_stream": (ctypes.c_int, [_P]),
@@ -777,3 +782,65 @@ def w4_gemv_experts(X, W, scales, ids, zeros=None, first_expert: int = 0, swiglu
                 *_w4_weights(W, scales, zeros, (E,), N, K), (ids, "ids", (torch.int32,), (T, k)),
                 (out, "out", (torch.bfloat16,), (T * k, N // 2 if swiglu else N)))
     return out
+
+
+# ---- gated feed-forward block -------------------------------------------------------------------
+
+_ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError('act must be "silu" or "gelu_tanh"')
+    return _ACTS[act]
+
+
+def _gated_sizes(X, W):
+    """(M, I, K) of X [M,K] and W [2I,K]."""
+    M, K = _dims(X, 2, "X")
+    rows = _dims(W, 2, "W")[0]
+    if rows % 2:
+        raise ValueError("W must have gate and up rows")
+    return M, rows // 2, K
+
+
+def gated_ffn(X, W, act="silu", pre=None, out=None, stream=None):
+    """act(X Wg^T) * (X Wu^T): X bf16 [M,K], W bf16 [2I,K] (gate rows, then up rows) -> bf16 [M,I].
+    ``act``: "silu" or "gelu_tanh".  ``pre`` bf16 [M,2I], if given, receives the two products for
+    gated_ffn_backward.  I and K: multiples of 8."""
+    if out is None:
+        M, I, _ = _gated_sizes(X, W)
+        out = _new((M, I), _torch().bfloat16, X, stream)
+    st = _calls().gated_ffn(X, W, out, pre, _act(act), _handle(stream))
+    if st != 0:
+        M, I, K = _gated_sizes(X, W)
+        bf16 = (_torch().bfloat16,)
+        _refuse("fp8gemm_gated_ffn", st, (X, "X", bf16, (M, K)), (W, "W", bf16, (2 * I, K)), (out, "out", bf16, (M, I)),
+                (pre, "pre", bf16, (M, 2 * I)))
+    return out
+
+
+def gated_ffn_backward(dH, X, W, pre=None, act="silu", dX=None, dW=None, dpre=None, need_dX: bool = True,
+                       need_dW: bool = True, stream=None):
+    """Gradients of gated_ffn: dH bf16 [M,I] -> (dX bf16 [M,K], dW bf16 [2I,K]), None for one that is
+    not needed.  ``pre``: what gated_ffn kept (else the products are formed again).  ``dpre`` bf16
+    [M,2I] receives the gradient with respect to the two products (allocated here when None; may be
+    ``pre`` itself)."""
+    bf16 = _torch().bfloat16
+    M, I, K = _gated_sizes(X, W)
+    if dpre is None:
+        dpre = _new((M, 2 * I), bf16, X, stream)
+    if not need_dX:
+        dX = None
+    elif dX is None:
+        dX = _new((M, K), bf16, X, stream)
+    if not need_dW:
+        dW = None
+    elif dW is None:
+        dW = _new((2 * I, K), bf16, X, stream)
+    st = _calls().gated_ffn_backward(dH, X, W, pre, dpre, dX, dW, _act(act), _handle(stream))
+    if st != 0:
+        _refuse("fp8gemm_gated_ffn_backward", st, (dH, "dH", (bf16,), (M, I)), (X, "X", (bf16,), (M, K)),
+                (W, "W", (bf16,), (2 * I, K)), (pre, "pre", (bf16,), (M, 2 * I)), (dpre, "dpre", (bf16,), (M, 2 * I)),
+                (dX, "dX", (bf16,), (M, K)), (dW, "dW", (bf16,), (2 * I, K)))
+    return dX, dW

@@ -26,8 +26,9 @@ PROBE_SOURCE = os.path.join(HERE, "csrc", "read_probe.hip")
 SOURCES = [os.path.join(CSRC, "fp8gemm_kernels.hip"), os.path.join(CSRC, "stream_kernels.hip"),
            os.path.join(CSRC, "quantize_kernels.hip"), os.path.join(CSRC, "scratch.hip"),
            os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "permute_kernels.hip"),
-           os.path.join(CSRC, "w4_kernels.hip"),
+           os.path.join(CSRC, "w4_kernels.hip"), os.path.join(CSRC, "gated_kernels.hip"),
            os.path.join(CSRC, "fp8gemm_api.cpp"), os.path.join(CSRC, "moe_api.cpp"),
+           os.path.join(CSRC, "ffn_api.cpp"),
            os.path.join(CSRC, "fp8gemm_jit.cpp")]
 # the Python module of the short path from torch tensors to the library (host code)
 NATIVE_LIB = os.path.join(HERE, "_native.so")

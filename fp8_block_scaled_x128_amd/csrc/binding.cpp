@@ -289,10 +289,46 @@ PyObject* w4_gemv_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// (X, W, out, pre, act, stream)
+PyObject* gated_ffn(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Call c(args, n, 6);
+        const at::Tensor *x = c.tensor(0), *w = c.tensor(1);
+        if (!x || !w || x->dim() != 2 || w->dim() != 2 || w->size(0) % 2) return PyLong_FromLong(kRefused);
+        const int64_t M = x->size(0), K = x->size(1), I = w->size(0) / 2;
+        void* X = c.data(0, kBFloat16, {M, K});
+        void* W = c.data(1, kBFloat16, {2 * I, K});
+        void* H = c.data(2, kBFloat16, {M, I});
+        void* pre = c.data(3, kBFloat16, {M, 2 * I}, true);
+        const int32_t act = c.small(4);
+        return c.run(5, [&](void* s) { return fp8gemm_gated_ffn(X, W, H, pre, M, I, K, act, s); });
+    });
+}
+
+// (dH, X, W, pre, dpre, dX, dW, act, stream)
+PyObject* gated_ffn_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Call c(args, n, 9);
+        const at::Tensor *x = c.tensor(1), *w = c.tensor(2);
+        if (!x || !w || x->dim() != 2 || w->dim() != 2 || w->size(0) % 2) return PyLong_FromLong(kRefused);
+        const int64_t M = x->size(0), K = x->size(1), I = w->size(0) / 2;
+        void* dH = c.data(0, kBFloat16, {M, I});
+        void* X = c.data(1, kBFloat16, {M, K});
+        void* W = c.data(2, kBFloat16, {2 * I, K});
+        void* pre = c.data(3, kBFloat16, {M, 2 * I}, true);
+        void* dpre = c.data(4, kBFloat16, {M, 2 * I});
+        void* dX = c.data(5, kBFloat16, {M, K}, true);
+        void* dW = c.data(6, kBFloat16, {2 * I, K}, true);
+        const int32_t act = c.small(7);
+        return c.run(8, [&](void* s) { return fp8gemm_gated_ffn_backward(dH, X, W, pre, dpre, dX, dW, M, I, K, act, s); });
+    });
+}
+
 #define FP8GEMM_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP8GEMM_METHOD(route_topk), FP8GEMM_METHOD(route_topk_backward), FP8GEMM_METHOD(moe_dispatch),
                          FP8GEMM_METHOD(moe_combine), FP8GEMM_METHOD(moe_combine_backward), FP8GEMM_METHOD(w4_gemv),
-                         FP8GEMM_METHOD(w4_gemv_experts), {nullptr, nullptr, 0, nullptr}};
+                         FP8GEMM_METHOD(w4_gemv_experts), FP8GEMM_METHOD(gated_ffn), FP8GEMM_METHOD(gated_ffn_backward),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,230 @@
+// ffn_api.cpp -- C ABI of the gated feed-forward block in bf16 and its gradients.  Argument validation,
+// launch-shape choice and launch (host code); meaning and layouts: include/fp8gemm.h.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <mutex>
+
+#include "ffn_internal.h"
+#include "fp8gemm.h"
+#include "fp8gemm_internal.h"
+#include "moe_internal.h"
+
+using namespace fp8gemm;
+
+namespace {
+
+constexpr int64_t kMaxBytes = int64_t(1) << 40;
+constexpr int64_t kMaxWidth = int64_t(1) << 20;         // values of a row of X, W or dpre: a tile stays below 2^31 bytes
+constexpr int64_t kMaxUnits = int64_t(1) << 22;         // workgroups of a launch: below 2^32 threads
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_ERR_LAUNCH; }
+
+struct Choice {
+    int shape, splits;
+};
+
+// FP8GEMM_FORCE_CONFIG=product:BMxBN:SPLIT
+bool forced(Choice* c) {
+    const char* s = std::getenv("FP8GEMM_FORCE_CONFIG");
+    int bm, bn, split;
+    if (!s || std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3) return false;
+    for (int i = 0; i < kTileShapes; ++i)
+        if (kTiles[i].bm == bm && kTiles[i].bn == bn) {
+            *c = {i, std::max(1, split)};
+            return true;
+        }
+    return false;
+}
+
+// Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K.
+Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
+    Choice best{0, 1};
+    if (forced(&best)) return best;
+    // us of a slice on a CU full of such workgroups
+    constexpr double kSlice[kTileShapes] = {1.45, 0.95, 0.62};
+    double least = 1e30;
+    for (int i = 0; i < kTileShapes; ++i) {
+        const TileShape& t = kTiles[i];
+        const int64_t width = gated ? t.bn / 2 : t.bn;
+        const int64_t tiles = ((rows + t.bm - 1) / t.bm) * ((cols + width - 1) / width);
+        for (int64_t s = 1; s <= 16 && s * 4 <= std::max<int64_t>(slices, 4); ++s) {
+            const int64_t units = tiles * s, slots = (int64_t)cus * t.per_cu;
+            if (s > 1 && units > slots) break;
+            const double per = (double)((slices + s - 1) / s);
+            const double cost = (double)((units + slots - 1) / slots) * (per * kSlice[i] + 3.0) + (s > 1 ? 3.0 + 0.3 * s : 0.0);
+            if (cost < least) {
+                least = cost;
+                best = {i, (int)s};
+            }
+        }
+    }
+    return best;
+}
+
+// Sizes, order of the tiles and workspace of a product; `hold` keeps the workspace until the launch is enqueued.
+int plan(ProductArgs* a, Choice* c, bool gated, int cus, hipStream_t stream, std::unique_lock<std::mutex>* hold) {
+    a->slices = (a->K + kSliceK - 1) / kSliceK;
+    *c = choose(a->rows, a->cols, a->slices, gated, cus);
+    const TileShape& t = kTiles[c->shape];
+    const int width = gated ? t.bn / 2 : t.bn;
+    const int64_t tm = ((int64_t)a->rows + t.bm - 1) / t.bm, tn = ((int64_t)a->cols + width - 1) / width;
+    a->per_split = (a->slices + c->splits - 1) / c->splits;
+    a->splits = c->splits = (a->slices + a->per_split - 1) / a->per_split;       // none without a slice
+    if (tm > kMaxUnits / tn || tm * tn > kMaxUnits / a->splits) return FP8GEMM_ERR_UNSUPPORTED;
+    a->tiles_m = (int32_t)tm;
+    a->tiles_n = (int32_t)tn;
+    a->group_m = (int32_t)std::min<int64_t>(tm, 8);
+    a->div_splits = make_fastdiv((uint32_t)a->splits);
+    a->div_band_units = make_fastdiv((uint32_t)(a->group_m * tn));
+    a->div_band_h = make_fastdiv((uint32_t)a->group_m);
+    a->div_band_h_last = make_fastdiv((uint32_t)(tm - (tm - 1) / a->group_m * a->group_m));
+    if (a->splits == 1) return FP8GEMM_OK;
+    // (a call of several products takes the same workspace for each: the stream orders them)
+    return host_stream_workspace(stream, (size_t)(tm * tn) * a->splits * t.bm * t.bn * sizeof(float), (size_t)(tm * tn), &a->ws,
+                                 &a->counters, hold->owns_lock() ? nullptr : hold);
+}
+
+int check_gated(int64_t M, int64_t I, int64_t K, int32_t act) {
+    if (M < 0 || I <= 0 || K <= 0 || I % 8 != 0 || K % 8 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (act != FP8GEMM_ACT_SILU && act != FP8GEMM_ACT_GELU_TANH) return FP8GEMM_ERR_BAD_SHAPE;
+    if (K > kMaxWidth || I > kMaxWidth / 2 || M >= (int64_t(1) << 31) - 64 || 2 * M * K >= kMaxBytes || 4 * M * I >= kMaxBytes)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    return FP8GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t M, int64_t I, int64_t K, int32_t act,
+                      void* stream) {
+    int st = check_gated(M, I, K, act);
+    if (st != FP8GEMM_OK) return st;
+    if (M == 0) return FP8GEMM_OK;
+    if (!X || !W || !H) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(X, 16) || !aligned(W, 16) || !aligned(H, 16) || !aligned(pre, 16)) return FP8GEMM_ERR_MISALIGNED;
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    Choice c;
+    if (M <= kGatedRowsMax && (I + 8) * K * 2 < (int64_t(1) << 31) && !forced(&c)) {
+        GatedRowsArgs a{};
+        a.X = static_cast<const uint16_t*>(X);
+        a.W = static_cast<const uint16_t*>(W);
+        a.out = static_cast<uint16_t*>(H);
+        a.pre = static_cast<uint16_t*>(pre);
+        a.M = (int32_t)M;
+        a.I = (int32_t)I;
+        a.K = (int32_t)K;
+        a.gelu = act == FP8GEMM_ACT_GELU_TANH;
+        host_set_config("gated_ffn M=%lld I=%lld K=%lld rows", {M, I, K});
+        launch_gated_rows(a, s);
+        return launched();
+    }
+    ProductArgs a{};
+    a.P = static_cast<const uint16_t*>(X);
+    a.Q = static_cast<const uint16_t*>(W);
+    a.out = static_cast<uint16_t*>(H);
+    a.pre = static_cast<uint16_t*>(pre);
+    a.rows = (int32_t)M;
+    a.cols = (int32_t)I;
+    a.K = a.ldp = a.ldq = (int32_t)K;
+    a.gelu = act == FP8GEMM_ACT_GELU_TANH;
+    std::unique_lock<std::mutex> hold;
+    st = plan(&a, &c, true, d.cus, s, &hold);
+    if (st != FP8GEMM_OK) return st;
+    host_set_config("gated_ffn M=%lld I=%lld K=%lld tile=%lldx%lld split=%lld",
+                    {M, I, K, kTiles[c.shape].bm, kTiles[c.shape].bn, c.splits});
+    launch_product(a, kGated, c.shape, s);
+    return launched();
+}
+
+int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, const void* pre, void* dpre, void* dX, void* dW,
+                               int64_t M, int64_t I, int64_t K, int32_t act, void* stream) {
+    int st = check_gated(M, I, K, act);
+    if (st != FP8GEMM_OK) return st;
+    if (M > 0 && (!dH || !dpre || (!X && (!pre || dW)) || (!W && (!pre || dX)))) return FP8GEMM_ERR_NULL_PTR;
+    for (const void* p : {dH, X, W, pre, static_cast<const void*>(dpre), static_cast<const void*>(dX), static_cast<const void*>(dW)})
+        if (!aligned(p, 16)) return FP8GEMM_ERR_MISALIGNED;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M == 0) {
+        if (!dW) return FP8GEMM_OK;
+        launch_fill_zero(dW, 4 * I * K, s);
+        return launched();
+    }
+    if (2 * M * 2 * I >= kMaxBytes || (M * I / 8 + 255) / 256 > kMaxUnits * 4 - 1) return FP8GEMM_ERR_UNSUPPORTED;
+    HostDevice d;
+    st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    // every choice and the workspace before the first launch
+    std::unique_lock<std::mutex> hold;
+    Choice cp{0, 1}, cx{0, 1}, cw{0, 1};
+    ProductArgs ap{}, ax{}, aw{};
+    if (!pre) {
+        ap.P = static_cast<const uint16_t*>(X);
+        ap.Q = static_cast<const uint16_t*>(W);
+        ap.dH = static_cast<const uint16_t*>(dH);
+        ap.pre = static_cast<uint16_t*>(dpre);
+        ap.rows = (int32_t)M;
+        ap.cols = (int32_t)I;
+        ap.K = ap.ldp = ap.ldq = (int32_t)K;
+        ap.gelu = act == FP8GEMM_ACT_GELU_TANH;
+        st = plan(&ap, &cp, true, d.cus, s, &hold);
+        if (st != FP8GEMM_OK) return st;
+    }
+    if (dX) {
+        ax.P = static_cast<const uint16_t*>(dpre);
+        ax.Q = static_cast<const uint16_t*>(W);
+        ax.out = static_cast<uint16_t*>(dX);
+        ax.rows = (int32_t)M;
+        ax.cols = ax.ldq = (int32_t)K;
+        ax.K = ax.ldp = (int32_t)(2 * I);
+        st = plan(&ax, &cx, false, d.cus, s, &hold);
+        if (st != FP8GEMM_OK) return st;
+    }
+    if (dW) {
+        aw.P = static_cast<const uint16_t*>(dpre);
+        aw.Q = static_cast<const uint16_t*>(X);
+        aw.out = static_cast<uint16_t*>(dW);
+        aw.rows = aw.ldp = (int32_t)(2 * I);
+        aw.cols = aw.ldq = (int32_t)K;
+        aw.K = (int32_t)M;
+        st = plan(&aw, &cw, false, d.cus, s, &hold);
+        if (st != FP8GEMM_OK) return st;
+    }
+    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld again=%lld dX tile=%lld split=%lld dW tile=%lld split=%lld",
+                    {M, I, K, pre ? 0 : cp.splits, dX ? kTiles[cx.shape].bm : 0, cx.splits, dW ? kTiles[cw.shape].bm : 0, cw.splits});
+    if (pre) {
+        GatedGradArgs g{};
+        g.pre = static_cast<const uint16_t*>(pre);
+        g.dH = static_cast<const uint16_t*>(dH);
+        g.dpre = static_cast<uint16_t*>(dpre);
+        g.units = M * (I / 8);
+        g.I = (int32_t)I;
+        g.gelu = act == FP8GEMM_ACT_GELU_TANH;
+        g.div_row = make_fastdiv((uint32_t)(I / 8));
+        launch_gated_grad(g, s);
+    } else {
+        launch_product(ap, kGatedBack, cp.shape, s);
+    }
+    st = launched();
+    if (st == FP8GEMM_OK && dX) {
+        launch_product(ax, kTimesW, cx.shape, s);
+        st = launched();
+    }
+    if (st == FP8GEMM_OK && dW) {
+        launch_product(aw, kTurned, cw.shape, s);
+        st = launched();
+    }
+    return st;
+}
+
+}  // extern "C"

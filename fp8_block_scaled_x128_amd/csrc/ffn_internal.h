@@ -1,0 +1,80 @@
+// ffn_internal.h -- types shared by the kernels of the gated feed-forward block and the low-rank adapters
+// and their host code (ffn_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8gemm_args.h"
+
+namespace fp8gemm {
+
+// ---- tiled bf16 products ----
+// out[i][j] = sum_k P(i, k) Q(j, k); each operand either has k contiguous (rows of P are rows of memory) or is
+// "turned" (rows of memory are values of k).
+enum Product {
+    kGated = 0,        // P = X [M,K], Q = W [2I,K]: act(gate) * up, and the products themselves if `pre`
+    kGatedBack = 1,    // the same products, then their gradients from dH into `pre`
+    kTimesW = 2,       // P = dpre [M,2I], Q = W [2I,K] turned: dX
+    kTurned = 3,       // P = dpre [M,2I] turned, Q = X [M,K] turned: dW
+};
+constexpr int kProducts = 4;
+
+struct ProductArgs {
+    const uint16_t* P;
+    const uint16_t* Q;
+    const uint16_t* dH;         // kGatedBack: [rows][cols]
+    uint16_t* out;              // [rows][cols]
+    uint16_t* pre;              // kGated: [rows][2 cols] or null; kGatedBack: [rows][2 cols]
+    float* ws;                  // K splits: partial tiles [tile][split][BM * BN]
+    int32_t* counters;          // K splits: arrivals by tile, zero between launches
+    int32_t rows, cols;         // of out (kGated, kGatedBack: cols = I)
+    int32_t K;                  // contraction
+    int32_t ldp, ldq;           // values from one row of memory to the next
+    int32_t slices;             // ceil(K / 64)
+    int32_t tiles_m, tiles_n;
+    int32_t splits, per_split;  // slices of a split
+    int32_t group_m;            // M tiles of a band of the tile order
+    int32_t gelu;               // activation: silu, or gelu by its tanh form
+    FastDiv div_splits, div_band_units, div_band_h, div_band_h_last;
+};
+
+struct TileShape {
+    int bm, bn;                 // rows of P and of Q
+    int per_cu;                 // workgroups a CU holds
+};
+constexpr TileShape kTiles[] = {{256, 256, 1}, {128, 128, 2}, {64, 128, 2}};
+constexpr int kTileShapes = 3;
+constexpr int kSliceK = 64;
+
+void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s);
+
+// ---- the block for few rows ----
+struct GatedRowsArgs {
+    const uint16_t* X;          // [M][K]
+    const uint16_t* W;          // [2I][K]
+    uint16_t* out;              // [M][I]
+    uint16_t* pre;              // [M][2I] or null
+    int32_t M, I, K;
+    int32_t gelu;
+};
+constexpr int kGatedRowsMax = 64;   // rows of X that the kernel takes
+
+void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s);
+
+// ---- gradients of the products from kept ones ----
+struct GatedGradArgs {
+    const uint16_t* pre;        // [M][2I]
+    const uint16_t* dH;         // [M][I]
+    uint16_t* dpre;             // [M][2I]
+    int64_t units;              // M * I / 8
+    int32_t I;
+    int32_t gelu;
+    FastDiv div_row;            // by I / 8
+};
+void launch_gated_grad(const GatedGradArgs& a, hipStream_t s);
+
+// 16-byte units set to zero (a gradient over no rows).
+void launch_fill_zero(void* p, int64_t bytes, hipStream_t s);
+
+}  // namespace fp8gemm

@@ -597,6 +597,19 @@ int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch, std::u
     return FP8GEMM_OK;
 }
 
+int host_stream_workspace(hipStream_t stream, size_t bytes, size_t count, float** partials, int32_t** counters,
+                          std::unique_lock<std::mutex>* hold) {
+    DeviceState* d = nullptr;
+    int st = device_state(&d);
+    if (st != FP8GEMM_OK) return st;
+    Workspace* w = nullptr;
+    st = workspace(d, stream, bytes, count, &w, hold);
+    if (st != FP8GEMM_OK) return st;
+    *partials = w->partials;
+    *counters = w->counters;
+    return FP8GEMM_OK;
+}
+
 void host_set_config(const char* fmt, std::initializer_list<long long> values) {
     g_pending.fmt = fmt;
     int n = 0;

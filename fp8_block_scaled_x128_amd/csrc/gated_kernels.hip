@@ -1,0 +1,490 @@
+// gated_kernels.hip -- gfx950 kernels of the gated feed-forward block in bf16 and of its gradients:
+//   H = act(X Wg^T) * (X Wu^T)          W [2I,K] = gate rows, then up rows
+//   dg = dH u act'(g), du = dH act(g);  dX = [dg|du] W;  dW = [dg|du]^T X
+// The mathematics and the limits are stated in include/fp8gemm.h.
+
+#include <algorithm>
+
+#include "ffn_internal.h"
+#include "fp8gemm_device.h"
+#include "moe_device.h"
+
+namespace fp8gemm {
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ v4f mfma_bf16(const v4u& x, const v4u& y, const v4f& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, y), c, 0, 0, 0);
+}
+
+// Both activations are x times a logistic function of z(x): z = x (silu), or z = 2 sqrt(2/pi) (x + 0.044715 x^3)
+// (gelu's tanh form, since 0.5 (1 + tanh(z / 2)) = 1 / (1 + e^-z)).  1 / (1 + e^-z) within 3 units in the last
+// place: the exponential's error and the reciprocal's.
+constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;
+
+__device__ __forceinline__ float logistic(float x, bool gelu) {
+    const float z = gelu ? kGeluA * __builtin_fmaf(kGeluB * x * x, x, x) : x;
+    return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
+}
+__device__ __forceinline__ float activation(float x, bool gelu) { return x * logistic(x, gelu); }
+// act(x) and act'(x) = s + x s (1 - s) z'(x).  The second term vanishes long before |x| = 64; taken at the
+// bounded x it cannot overflow.
+__device__ __forceinline__ float activation_grad(float x, bool gelu, float* value) {
+    const float s = logistic(x, gelu);
+    const float xb = __builtin_amdgcn_fmed3f(x, -64.0f, 64.0f);
+    const float dz = gelu ? kGeluA * __builtin_fmaf(3.0f * kGeluB * xb, xb, 1.0f) : 1.0f;
+    *value = x * s;
+    return __builtin_fmaf(xb * s * (1.0f - s), dz, s);
+}
+
+__device__ __forceinline__ v2u pack4(const v4f& v) { return (v2u){pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)}; }
+__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Chunk permutation of a 128-byte LDS row, as in the FP8 kernel: 16-byte chunk c of row r stands at c ^ swz(r).
+__device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2); }
+// Permutation of the 32-byte runs (16 columns) of a turned row k of LDS: run u stands at u ^ turn(k).  A turned
+// fragment read takes, in a half-wave, four consecutive rows at k and four at k + 16: eight different runs
+// (four, in an operand of 64 columns).
+template <int ROWS>
+__device__ __forceinline__ int turn(int k) {
+    static_assert(ROWS == 64 || ROWS % 128 == 0, "runs of a row: four, or a multiple of eight");
+    return ((k & 3) | (((k >> 4) & 1) << 2)) & (ROWS / 16 - 1);
+}
+
+// One operand of a tile in LDS: ROWS rows (columns, if turned) of a slice of 64 values of k, ROWS * 128 bytes.
+//   straight: row r holds its 64 values, 128 bytes, chunks permuted by swz(r)
+//   turned:   row k holds ROWS values, runs permuted by turn(k)
+// Lane l's fragment of 16 rows, matrix-core step s of 2: row l % 16, the 8 values of k from 16 (l / 16) + 8 s.
+template <int ROWS, int NW, bool TURNED>
+struct Operand {
+    static constexpr int BYTES = ROWS * 128;
+    static constexpr int LOADS = BYTES / 1024 / NW;          // 1 KB loads of a wave and slice
+    static_assert(BYTES % (1024 * NW) == 0, "every wave loads the same number of KB");
+    static constexpr int ROW_BYTES = TURNED ? ROWS * 2 : 128;
+    static constexpr int PER_LOAD = 1024 / ROW_BYTES;        // rows of LDS in a load
+
+    // Row of LDS and 16-byte chunk of the source that lane `lane` moves in load q of wave `wave`.
+    static __device__ __forceinline__ int row(int wave, int q, int lane) {
+        return (wave * LOADS + q) * PER_LOAD + lane / (ROW_BYTES / 16);
+    }
+    static __device__ __forceinline__ int chunk(int r, int lane) {
+        const int p = lane % (ROW_BYTES / 16);
+        return TURNED ? p ^ (turn<ROWS>(r) << 1) : p ^ swz(r);
+    }
+};
+
+template <int BM, int BN, int WMW, int WNW, int STAGES, int KIND>
+struct Tile {
+    static constexpr bool PT = KIND == kTurned, QT = KIND == kTimesW || KIND == kTurned;
+    static constexpr bool GATED = KIND == kGated || KIND == kGatedBack;
+    static constexpr int NW = WMW * WNW, NT = 64 * NW;
+    static constexpr int WM = BM / WMW, WN = BN / WNW;
+    static constexpr int JM = WM / 16, IN = WN / 16;
+    using OpP = Operand<BM, NW, PT>;
+    using OpQ = Operand<BN, NW, QT>;
+    static constexpr int P_OFF = OpQ::BYTES;
+    static constexpr int STAGE_BYTES = OpQ::BYTES + OpP::BYTES;
+    static constexpr int NDMA = OpQ::LOADS + OpP::LOADS;
+    static_assert(NDMA * (STAGES - 1) < 64, "vmcnt range");
+    static constexpr int OUT_COLS = GATED ? BN / 2 : BN;     // columns of the output that a tile covers
+    // epilogue: a wave's rows in an LDS region of its own, an odd number of 16-byte units apart
+    static constexpr int W_COLS = OUT_COLS / WNW;
+    static constexpr int CPR = W_COLS / 8;
+    static constexpr int PITCH = 2 * W_COLS + (CPR % 2 == 0 ? 16 : 0);
+    static constexpr int STG = WM * PITCH;
+    static constexpr int SMEM = STAGES * STAGE_BYTES > NW * STG ? STAGES * STAGE_BYTES : NW * STG;
+    static_assert(SMEM <= 160 * 1024, "LDS budget");
+};
+
+template <int BM, int BN, int WMW, int WNW, int STAGES, int KIND>
+__global__ __launch_bounds__(WMW * WNW * 64, 2) void product_kernel(const ProductArgs a) {
+    using T = Tile<BM, BN, WMW, WNW, STAGES, KIND>;
+    using OpP = typename T::OpP;
+    using OpQ = typename T::OpQ;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
+    __shared__ int s_flag;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WMW, wn = wave / WMW;
+    const int row16 = lane & 15, grp = lane >> 4;
+    const uint32_t smem_base = lds_addr(smem);
+
+    // Workgroups are dealt to the 8 XCDs in turn: those of one XCD take consecutive units, which share operands
+    // in its L2.
+    const int U = gridDim.x, xcd = blockIdx.x & 7;
+    const int unit = xcd * (U >> 3) + min(xcd, U & 7) + (blockIdx.x >> 3);
+    // split fastest, then the M tile within a band of group_m of them, then the N tile
+    const uint32_t tile = fast_div((uint32_t)unit, a.div_splits);
+    const int split = unit - (int)tile * a.splits;
+    const uint32_t band = fast_div(tile, a.div_band_units);
+    const uint32_t inb = tile - band * a.div_band_units.d;
+    const int band_m0 = (int)band * a.group_m;
+    const FastDiv& bh = band_m0 + a.group_m <= a.tiles_m ? a.div_band_h : a.div_band_h_last;
+    const uint32_t tq = fast_div(inb, bh);
+    const int m0 = (band_m0 + (int)(inb - tq * bh.d)) * BM;
+    const int n0 = (int)tq * T::OUT_COLS;                    // first output column
+    const int s0 = split * a.per_split, nks = min(a.per_split, a.slices - s0);
+
+    // ---- what each lane loads: byte offsets from a slice's bases --------------------------------------------
+    // rows and columns past the end repeat the last (their results are not stored); `kvalid` values of k
+    auto p_off = [&](int q, int kvalid) -> uint32_t {
+        const int r = OpP::row(wave, q, lane), c = OpP::chunk(r, lane);
+        if constexpr (T::PT) return (uint32_t)min(r, kvalid - 1) * (uint32_t)(2 * a.ldp) + (uint32_t)(2 * min(m0 + 8 * c, a.rows - 8));
+        else return (uint32_t)min(r, a.rows - 1 - m0) * (uint32_t)(2 * a.ldp) + (uint32_t)(2 * min(8 * c, kvalid - 8));
+    };
+    auto q_off = [&](int q, int kvalid) -> uint32_t {
+        const int r = OpQ::row(wave, q, lane), c = OpQ::chunk(r, lane);
+        if constexpr (T::QT) return (uint32_t)min(r, kvalid - 1) * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(n0 + 8 * c, a.cols - 8));
+        // gate and up rows in turn, 16 each, so that a lane ends with a pair of them (up: qs below)
+        const int n = min(((r >> 5) << 4) + (r & 15), a.cols - 1 - n0);
+        return (uint32_t)n * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(8 * c, kvalid - 8));
+    };
+    uint32_t poff[OpP::LOADS], qoff[OpQ::LOADS];
+#pragma unroll
+    for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, 64);
+#pragma unroll
+    for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, 64);
+    const uint16_t* pbase = a.P + (T::PT ? (int64_t)s0 * 64 * a.ldp : (int64_t)m0 * a.ldp + (int64_t)s0 * 64);
+    const uint16_t* qbase = a.Q + (T::QT ? (int64_t)s0 * 64 * a.ldq : (int64_t)n0 * a.ldq + (int64_t)s0 * 64);
+    const int64_t pstep = T::PT ? (int64_t)64 * a.ldp : 64, qstep = T::QT ? (int64_t)64 * a.ldq : 64;
+    const int tail = a.K - (a.slices - 1) * 64;              // values of the last slice
+    const int tail_at = tail < 64 ? a.slices - 1 - s0 : -1;  // this unit's slice that is not whole
+
+    auto issue = [&](int i) {
+        const uint32_t st = smem_base + (uint32_t)((i % STAGES) * T::STAGE_BYTES);
+        const uint16_t* qs[2];                               // with turned rows, and of gate rows; of up rows
+        qs[0] = uniform_ptr(qbase + i * qstep);
+        qs[1] = T::GATED ? uniform_ptr(qbase + i * qstep + (int64_t)a.cols * a.ldq) : qs[0];
+        const uint16_t* ps = uniform_ptr(pbase + i * pstep);
+        const bool part = i == tail_at;
+#pragma unroll
+        for (int q = 0; q < OpQ::LOADS; ++q)
+            dma_x4(st + (wave * OpQ::LOADS + q) * 1024, T::GATED && ((wave * OpQ::LOADS + q) >> 1 & 1) ? qs[1] : qs[0], part ? q_off(q, tail) : qoff[q]);
+#pragma unroll
+        for (int q = 0; q < OpP::LOADS; ++q)
+            dma_x4(st + T::P_OFF + (wave * OpP::LOADS + q) * 1024, ps, part ? p_off(q, tail) : poff[q]);
+    };
+    // zeros in both operands for the values of k that the last slice does not have
+    auto clear_tail = [&](int i) {
+        uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
+        auto clear = [&](uint8_t* part, int rows, bool turned, int row_bytes) {
+            if (turned) {
+                for (int o = tail * row_bytes + tid * 16; o < 64 * row_bytes; o += T::NT * 16)
+                    *reinterpret_cast<v4u*>(part + o) = (v4u){0, 0, 0, 0};
+            } else {
+                for (int x = tid; x < rows * 8; x += T::NT)
+                    if ((x & 7) * 8 >= tail) *reinterpret_cast<v4u*>(part + (x >> 3) * 128 + (((x & 7) ^ swz(x >> 3)) << 4)) = (v4u){0, 0, 0, 0};
+            }
+        };
+        clear(st, BN, T::QT, OpQ::ROW_BYTES);
+        clear(st + T::P_OFF, BM, T::PT, OpP::ROW_BYTES);
+        __syncthreads();
+    };
+
+    v4f acc[T::IN][T::JM];
+#pragma unroll
+    for (int i = 0; i < T::IN; ++i)
+#pragma unroll
+        for (int j = 0; j < T::JM; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+    const int straight[2] = {((2 * grp) ^ swz(row16)) << 4, ((2 * grp + 1) ^ swz(row16)) << 4};
+    const int tk = 16 * grp + (row16 >> 2);                   // a turned read's row of LDS
+    const int tp = turn<BM>(tk), tqr = turn<BN>(tk);         // and its permutations
+    auto fragment = [&](const uint8_t* part, int row0, int s, bool turned, int row_bytes, int tx) -> v4u {
+        if (!turned) return *reinterpret_cast<const v4u*>(part + (row0 + row16) * 128 + straight[s]);
+        const uint8_t* p = part + (tk + 8 * s) * row_bytes + (((row0 >> 4) ^ tx) << 5) + (lane & 3) * 8;
+        typedef __attribute__((address_space(3))) v4s* lds_v4s;
+        const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p)));
+        const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * row_bytes)));
+        return (v4u){lo.x, lo.y, hi.x, hi.y};
+    };
+    auto compute = [&](int i) {
+        const uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            v4u pf[T::JM], qf[T::IN];
+#pragma unroll
+            for (int j = 0; j < T::JM; ++j) pf[j] = fragment(st + T::P_OFF, wm * T::WM + 16 * j, s, T::PT, OpP::ROW_BYTES, tp);
+#pragma unroll
+            for (int i2 = 0; i2 < T::IN; ++i2) qf[i2] = fragment(st, wn * T::WN + 16 * i2, s, T::QT, OpQ::ROW_BYTES, tqr);
+#pragma unroll
+            for (int i2 = 0; i2 < T::IN; ++i2)
+#pragma unroll
+                for (int j = 0; j < T::JM; ++j) acc[i2][j] = mfma_bf16(qf[i2], pf[j], acc[i2][j]);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        if (i < nks) issue(i);
+    for (int i = 0; i < nks; ++i) {
+        wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2, nks - 1 - i));
+        __syncthreads();
+        if (i + STAGES - 1 < nks) issue(i + STAGES - 1);
+        if (i == tail_at) clear_tail(i);
+        compute(i);
+    }
+
+    // ---- K splits: the last workgroup of a tile to arrive sums the partials in split order -------------------
+    // (written and read past the L2s of the XCDs, with agent-coherent accesses; the counter goes back to zero)
+    if (a.splits > 1) {
+        const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(
+            uniform_ptr(a.ws + (int64_t)tile * a.splits * (BM * BN)), 0, a.splits * BM * BN * 4, kBufferFlags);
+        const int own = (wave * (T::WM * T::WN) + lane * 4) * 4;
+#pragma unroll
+        for (int i2 = 0; i2 < T::IN; ++i2)
+#pragma unroll
+            for (int j = 0; j < T::JM; ++j)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i2][j]), ws,
+                                                       own + (split * BM * BN + (i2 * T::JM + j) * 256) * 4, 0, kSc1);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (tid == 0) {
+            const int old = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_flag = old == a.splits - 1;
+            if (old == a.splits - 1)
+                __hip_atomic_store(a.counters + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!s_flag) return;
+        for (int s = 0; s < a.splits; ++s) {
+#pragma unroll
+            for (int i2 = 0; i2 < T::IN; ++i2) {
+                v4f x[T::JM];
+#pragma unroll
+                for (int j = 0; j < T::JM; ++j)
+                    x[j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                        ws, own + (s * BM * BN + (i2 * T::JM + j) * 256) * 4, 0, kSc1));
+#pragma unroll
+                for (int j = 0; j < T::JM; ++j) acc[i2][j] = s == 0 ? x[j] : acc[i2][j] + x[j];
+            }
+        }
+    }
+
+    // ---- epilogue -------------------------------------------------------------------------------------------
+    // a lane holds 4 consecutive columns of row 16 j + row16 of its wave's rows, for each of its 16-column tiles
+    uint8_t* stg = smem + wave * T::STG;
+    const int wrow0 = m0 + wm * T::WM, wcol0 = n0 + wn * T::W_COLS;
+    // whole 16-byte chunks of rows from the wave's region (its own LDS operations run in order)
+    auto store = [&](uint16_t* dst, int64_t ld, int shift) {
+        wave_sync();
+#pragma unroll
+        for (int x0 = 0; x0 < T::WM * T::CPR; x0 += 64) {
+            const int x = x0 + lane, r = x / T::CPR, c = x % T::CPR;
+            if (r < T::WM && wrow0 + r < a.rows && wcol0 + 8 * c < a.cols)
+                *reinterpret_cast<v4u*>(dst + (int64_t)(wrow0 + r) * ld + shift + wcol0 + 8 * c) =
+                    *reinterpret_cast<const v4u*>(stg + r * T::PITCH + c * 16);
+        }
+        wave_sync();
+    };
+    auto put = [&](int i, int j, const v4f& v) {
+        *reinterpret_cast<v2u*>(stg + (16 * j + row16) * T::PITCH + (16 * i + 4 * grp) * 2) = pack4(v);
+    };
+    __syncthreads();                                         // every wave is past its last slice
+    if constexpr (!T::GATED) {
+#pragma unroll
+        for (int i = 0; i < T::IN; ++i)
+#pragma unroll
+            for (int j = 0; j < T::JM; ++j) put(i, j, acc[i][j]);
+        store(a.out, a.cols, 0);
+    } else if constexpr (KIND == kGated) {
+        if (a.pre) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int i = 0; i < T::IN / 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < T::JM; ++j) put(i, j, acc[2 * i + half][j]);
+                store(a.pre, 2 * (int64_t)a.cols, half * a.cols);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < T::IN / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < T::JM; ++j) {
+                v4f h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = activation(acc[2 * i][j][e], a.gelu) * acc[2 * i + 1][j][e];
+                put(i, j, h);
+            }
+        store(a.out, a.cols, 0);
+    } else {
+        // dg in the place of the gate's sums, du in the up's
+#pragma unroll
+        for (int i = 0; i < T::IN / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < T::JM; ++j) {
+                const int r = wrow0 + 16 * j + row16, n = wcol0 + 16 * i + 4 * grp;
+                v2u d = {0, 0};
+                if (r < a.rows && n < a.cols) d = *reinterpret_cast<const v2u*>(a.dH + (int64_t)r * a.cols + n);
+                const float dh[4] = {low_bf16(d.x), high_bf16(d.x), low_bf16(d.y), high_bf16(d.y)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float act;
+                    const float der = activation_grad(acc[2 * i][j][e], a.gelu, &act);
+                    acc[2 * i][j][e] = dh[e] * acc[2 * i + 1][j][e] * der;
+                    acc[2 * i + 1][j][e] = dh[e] * act;
+                }
+            }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < T::IN / 2; ++i)
+#pragma unroll
+                for (int j = 0; j < T::JM; ++j) put(i, j, acc[2 * i + half][j]);
+            store(a.pre, 2 * (int64_t)a.cols, half * a.cols);
+        }
+    }
+}
+
+// ---- the block for few rows -----------------------------------------------------------------------------
+// A workgroup has 8 output columns, whose 8 gate rows and 8 up rows of W are the 16 rows of one matrix-core
+// operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in
+// turn; their sums meet in LDS and are added in wave order.
+constexpr int kRowsWaves = 8;
+
+// 64 values of k of step `step` as this lane's 8 for matrix-core steps 0 and 1: 16 (lane / 16) + 8 s
+__device__ __forceinline__ v4u load16(const __amdgpu_buffer_rsrc_t& b, int offset) {
+    return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(b, offset, 0, 0));
+}
+
+template <int MT, int PF>
+__global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const GatedRowsArgs a) {
+    __shared__ v4f red[kRowsWaves][MT][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row16 = lane & 15, grp = lane >> 4;
+    const int n0 = blockIdx.x * 8;
+    const int K2 = a.K * 2, steps = (a.K + 63) / 64;
+
+    // gate rows n0.. and up rows I + n0..: one buffer from the first gate row to the last up row of the tile
+    const int64_t span = ((int64_t)a.I + min(8, a.I - n0)) * K2;
+    const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(uniform_ptr(a.W + (int64_t)n0 * a.K)), 0, (int)span, kBufferFlags);
+    const __amdgpu_buffer_rsrc_t xb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.X), 0, a.M * K2, kBufferFlags);
+    const int wrow = (min(row16 & 7, a.I - 1 - n0) + (row16 >> 3) * a.I) * K2 + grp * 32;
+    int xrow[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xrow[t] = min(t * 16 + row16, a.M - 1) * K2 + grp * 32;
+
+    v4f acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
+    struct Slot {
+        v4u w[2], x[2][MT];
+    };
+    Slot ring[PF];
+    auto load = [&](Slot& s, int step) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // past the end of K: past the buffer, which reads as zeros
+            const int k = step * 128 + h * 16;
+            const bool in = k + grp * 32 < K2;
+            s.w[h] = load16(wb, in ? wrow + k : -16);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s.x[h][t] = load16(xb, in ? xrow[t] + k : -16);
+        }
+    };
+#pragma unroll
+    for (int p = 0; p < PF; ++p) load(ring[p], wave + p * kRowsWaves);
+    for (int s0 = wave; s0 < steps; s0 += kRowsWaves * PF) {
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[t] = mfma_bf16(ring[p].w[h], ring[p].x[h][t], acc[t]);
+            load(ring[p], s0 + (p + PF) * kRowsWaves);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+    __syncthreads();
+    // output (row m, column n0 + c): gate sum in lane 16 (c / 4) + m % 16, element c % 4; up sum 32 lanes on
+    for (int x = tid; x < 8 * 16 * MT; x += kRowsWaves * 64) {
+        const int c = x & 7, m = x >> 3, t = m >> 4;
+        if (m >= a.M || n0 + c >= a.I) continue;
+        const int from = 16 * (c >> 2) + (m & 15);
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsWaves; ++w) {
+            g += red[w][t][from][c & 3];
+            u += red[w][t][from + 32][c & 3];
+        }
+        a.out[(int64_t)m * a.I + n0 + c] = f32_to_bf16(activation(g, a.gelu) * u);
+        if (a.pre) {
+            a.pre[(int64_t)m * 2 * a.I + n0 + c] = f32_to_bf16(g);
+            a.pre[(int64_t)m * 2 * a.I + a.I + n0 + c] = f32_to_bf16(u);
+        }
+    }
+}
+
+// ---- gradients of kept products: 8 values of a row a thread ---------------------------------------------
+__global__ __launch_bounds__(256) void gated_grad_kernel(const GatedGradArgs a) {
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (unit >= a.units) return;
+    const uint32_t per_row = (uint32_t)a.I / 8;
+    const int64_t row = unit < (int64_t(1) << 31) ? (int64_t)fast_div((uint32_t)unit, a.div_row) : unit / per_row;
+    const int n = (int)(unit - row * per_row) * 8;
+    const uint16_t* pre = a.pre + row * 2 * a.I + n;
+    const v4u g4 = *reinterpret_cast<const v4u*>(pre), u4 = *reinterpret_cast<const v4u*>(pre + a.I);
+    const v4u d4 = *reinterpret_cast<const v4u*>(a.dH + row * a.I + n);
+    v4u og, ou;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float act0, act1;
+        const float der0 = activation_grad(low_bf16(g4[i]), a.gelu, &act0);
+        const float der1 = activation_grad(high_bf16(g4[i]), a.gelu, &act1);
+        og[i] = pack_bf16x2(low_bf16(d4[i]) * low_bf16(u4[i]) * der0, high_bf16(d4[i]) * high_bf16(u4[i]) * der1);
+        ou[i] = pack_bf16x2(low_bf16(d4[i]) * act0, high_bf16(d4[i]) * act1);
+    }
+    uint16_t* dp = a.dpre + row * 2 * a.I + n;
+    *reinterpret_cast<v4u*>(dp) = og;
+    *reinterpret_cast<v4u*>(dp + a.I) = ou;
+}
+
+__global__ __launch_bounds__(256) void fill_zero_kernel(v4u* p, int64_t units) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += (int64_t)gridDim.x * 256) p[i] = (v4u){0, 0, 0, 0};
+}
+
+template <int KIND>
+void launch_kind(const ProductArgs& a, int shape, hipStream_t s) {
+    const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n * a.splits));
+    if (shape == 0) product_kernel<256, 256, 4, 2, 2, KIND><<<grid, 512, 0, s>>>(a);
+    else if (shape == 1) product_kernel<128, 128, 2, 2, 2, KIND><<<grid, 256, 0, s>>>(a);
+    else product_kernel<64, 128, 2, 2, 3, KIND><<<grid, 256, 0, s>>>(a);
+}
+
+}  // namespace
+
+void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s) {
+    switch (kind) {
+        case kGated: return launch_kind<kGated>(a, shape, s);
+        case kGatedBack: return launch_kind<kGatedBack>(a, shape, s);
+        case kTimesW: return launch_kind<kTimesW>(a, shape, s);
+        case kTurned: return launch_kind<kTurned>(a, shape, s);
+    }
+}
+
+void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((a.I + 7) / 8));
+    if (a.M <= 16) gated_rows_kernel<1, 4><<<grid, kRowsWaves * 64, 0, s>>>(a);
+    else if (a.M <= 32) gated_rows_kernel<2, 2><<<grid, kRowsWaves * 64, 0, s>>>(a);
+    else gated_rows_kernel<4, 2><<<grid, kRowsWaves * 64, 0, s>>>(a);
+}
+
+void launch_gated_grad(const GatedGradArgs& a, hipStream_t s) {
+    gated_grad_kernel<<<dim3((uint32_t)((a.units + 255) / 256)), 256, 0, s>>>(a);
+}
+
+void launch_fill_zero(void* p, int64_t bytes, hipStream_t s) {
+    const int64_t units = bytes / 16;
+    fill_zero_kernel<<<dim3((uint32_t)std::min<int64_t>((units + 255) / 256, 2048)), 256, 0, s>>>(static_cast<v4u*>(p), units);
+}
+
+}  // namespace fp8gemm

@@ -22,6 +22,9 @@ int host_device(HostDevice* out);                                       // statu
 // The stream's library-owned workspace (see fp8gemm.h): `bytes` of scratch, status code.  `hold` keeps
 // other threads' calls off it and is kept until the last launch that uses it is enqueued.
 int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch, std::unique_lock<std::mutex>* hold);
+// The same with `count` arrival counters, which are zero and are left at zero.
+int host_stream_workspace(hipStream_t stream, size_t bytes, size_t count, float** partials, int32_t** counters,
+                          std::unique_lock<std::mutex>* hold);
 // The calling thread's last configuration: a static format of %lld fields and at most 8 values.
 void host_set_config(const char* fmt, std::initializer_list<long long> values);
 

@@ -339,6 +339,32 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
                             void* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t format, int32_t group,
                             int32_t first_expert, int32_t x_per_pair, int32_t swiglu, void* stream);
 
+/* ---- gated feed-forward block in bf16, with its gradients ------------------------------------
+ * The first layer of a feed-forward block that is kept in bf16 (a shared expert, the dense layers)
+ * and trained: both projections, the activation and the product in one launch.
+ *   W [2I][K]: gate rows [0, I), up rows [I, 2I);  g = X Wg^T, u = X Wu^T, sums in fp32
+ *   H [M][I] = bf16(act(g) * u),  act(x) = x / (1 + e^-z):  FP8GEMM_ACT_SILU z = x,
+ *     FP8GEMM_ACT_GELU_TANH z = 2 sqrt(2 / pi) (x + 0.044715 x^3)
+ *   pre [M][2I] = bf16([g | u]) for the gradients, or NULL.
+ * X, W, H, pre bf16, dense, 16-byte aligned.  I and K: positive multiples of 8, K <= 2^20,
+ * I <= 2^19 (else UNSUPPORTED); M == 0 is a no-op.  H and pre overlap no input.  Some sizes split K
+ * over workgroups and use the stream's workspace (see fp8gemm_prepare_stream). */
+#define FP8GEMM_ACT_SILU 0
+#define FP8GEMM_ACT_GELU_TANH 1
+int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t M, int64_t I, int64_t K, int32_t act,
+                      void* stream);
+
+/* Gradients of the block, from dH [M][I] bf16:
+ *   dpre [M][2I] = bf16([dg | du]),  dg = dH u act'(g), du = dH act(g), formed in fp32;
+ *   dX [M][K] = bf16(dpre W),  dW [2I][K] = bf16(dpre^T X), sums in fp32 of the rounded dpre.
+ * With `pre` (as fp8gemm_gated_ffn wrote it) g and u are its bf16 values; with pre NULL they are
+ * formed again from X and W and not rounded.  dpre is written (a workspace, and the gradient with
+ * respect to the two projections); it may be `pre` itself.  dX or dW NULL: not formed; X may be
+ * NULL with `pre` and without dW, W with `pre` and without dX.  M == 0 sets dW to zeros.  Sizes,
+ * alignment and workspace as above. */
+int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, const void* pre, void* dpre, void* dX, void* dW,
+                               int64_t M, int64_t I, int64_t K, int32_t act, void* stream);
+
 /* Device-side precondition flags (bits of the device error word). */
 #define FP8GEMM_DEVERR_BAD_INDEX 1 /* contiguous: an m_indices entry outside [-1, G) or off its block's group;
                                       combine: a row_map entry of R or more */
