@@ -22,6 +22,7 @@ C ABI declared in include/fp8gemm.h.  torch supplies device memory and the curre
     Y = w4_gemv_experts(X, W4, scales, ids, zeros, swiglu=True)  # the same, by the router's ids
     H = gated_ffn(X, W, act="silu", pre=pre)                     # act(X Wg^T) * (X Wu^T) in bf16
     dX, dW = gated_ffn_backward(dH, X, W, pre)                   # and its gradients
+    Y = lora_add(Y, X, A, B, ids, scales)                        # low-rank adapters by row, beside a projection
 
 A and B are E4M3 codes (torch.float8_e4m3fn or uint8), sa one fp32 scale per 1x128 block of a
 row of A stored K-block-major (sa[kb, m], shape [K/128, M]), sb one per 128x128 block of B (page "DeepSeek開源第三彈：V3/R1訓練推理關鍵秘籍，核心代碼僅
@@ -38,7 +39,7 @@ __all__ = ["gemm_nt", "gemm_nt_noalloc", "gemm_nt_specialized", "specialize_nt",
            "quantize_1x128_masked", "fp8fp4_grouped_masked", "swiglu_quantize_1x128", "swiglu_quantize_1x128_masked",
            "moe_expert_masked", "route_topk", "route_topk_backward", "moe_dispatch_masked",
            "moe_dispatch_contiguous", "moe_combine", "moe_combine_backward", "w4_gemv", "w4_gemv_experts",
-           "gated_ffn", "gated_ffn_backward", "init", "prepare_stream", "set_num_cus",
+           "gated_ffn", "gated_ffn_backward", "lora_add", "init", "prepare_stream", "set_num_cus",
            "last_config", "read_device_error", "status_string", "lib", "library_path",
            "Fp8GemmError", "STATUS", "DEVERR_BAD_INDEX", "DEVERR_BAD_COUNT"]
 
@@ -82,6 +83,7 @@ SIGNATURES = {
     "fp8gemm_w4_gemv_experts": (ctypes.c_int, [_P] * 6 + [_I64, _I32, _I32, _I64, _I64] + [_I32] * 5 + [_P]),
     "fp8gemm_gated_ffn": (ctypes.c_int, [_P] * 4 + [_I64, _I64, _I64, _I32, _P]),
     "fp8gemm_gated_ffn_backward": (ctypes.c_int, [_P] * 7 + [_I64, _I64, _I64, _I32, _P]),
+    "fp8gemm_lora_add": (ctypes.c_int, [_P] * 8 + [_I64, _I32, _I32] + [_I64] * 5 + [_P]),
     "fp8gemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8gemm_init": (ctypes.c_int, []),
     "fp8gemm_prepare_stream": (ctypes.c_int, [_P]),
@@ -528,8 +530,8 @@ def _new(shape, dtype, like, stream, zero=False):
         return make(shape, dtype=dtype, device=like.device)
 
 
-def _require(t, name, dtypes, shape, device):
-    """Raise what is wrong with an argument."""
+def _require(t, name, dtypes, shape, device, strided=False):
+    """Raise what is wrong with an argument (``strided``: rows of a matrix may stand apart)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor, got %s" % (name, type(t).__name__))
@@ -542,22 +544,25 @@ def _require(t, name, dtypes, shape, device):
     if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
         raise ValueError("%s must have shape [%s], got %s" % (name, ",".join("*" if s is None else str(s) for s in shape),
                                                               list(t.shape)))
+    if strided and (t.shape[1] <= 1 or t.stride(1) == 1):
+        return
     if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+        raise ValueError("%s must %s" % (name, "have contiguous rows" if strided else "be contiguous"))
 
 
 def _refuse(fn, status, *arguments):
-    """Raise for a call that did not succeed: the first argument (tensor, name, types, shape) that is not
-    as the call takes it, or the C call's status.  None stands for any size, and for a tensor left out."""
+    """Raise for a call that did not succeed: the first argument (tensor, name, types, shape, and True for a
+    matrix with rows apart) that is not as the call takes it, or the C call's status.  None stands for any
+    size, and for a tensor left out."""
     if status > 0:
         raise Fp8GemmError(status, fn)
     device = None
-    for t, name, dtypes, shape in arguments:
+    for t, name, dtypes, shape, *strided in arguments:
         if t is None:
             continue
         if device is None:
             device = getattr(t, "device", None)
-        _require(t, name, dtypes, shape, device)
+        _require(t, name, dtypes, shape, device, *strided)
     raise ValueError("%s: arguments out of range" % fn)
 
 
@@ -784,7 +789,7 @@ def w4_gemv_experts(X, W, scales, ids, zeros=None, first_expert: int = 0, swiglu
     return out
 
 
-# ---- gated feed-forward block -------------------------------------------------------------------
+# ---- gated feed-forward block, low-rank adapters -------------------------------------------------------------------
 
 _ACTS = {"silu": 0, "gelu_tanh": 1}
 
@@ -844,3 +849,25 @@ def gated_ffn_backward(dH, X, W, pre=None, act="silu", dX=None, dW=None, dpre=No
                 (W, "W", (bf16,), (2 * I, K)), (pre, "pre", (bf16,), (M, 2 * I)), (dpre, "dpre", (bf16,), (M, 2 * I)),
                 (dX, "dX", (bf16,), (M, K)), (dW, "dW", (bf16,), (2 * I, K)))
     return dX, dW
+
+
+def lora_add(Y, X, A, B, ids, scales=None, order=None, out=None, stream=None):
+    """out[t] = Y[t] + scales[a] * B[a] (A[a] x[t]) with the adapter a = ids[t] of each row, Y[t] where
+    ids[t] < 0: Y bf16 [T,N], X bf16 [T,K] (rows may stand apart), A bf16 [L,R,K], B bf16 [L,N,R], ids
+    int32 [T], scales fp32 [L] (None: ones) -> bf16 [T,N].  ``out`` may be Y.  ``order`` int32 [T]: a
+    permutation of the rows that brings those of an adapter together (``ids.argsort(stable=True).int()``,
+    once for a batch and all its projections); it changes no result, and saves time where neighbouring
+    rows have different adapters.  R: a multiple of 8 up to 128."""
+    if out is None:
+        out = _new(_dims(Y, 2, "Y"), _torch().bfloat16, Y, stream)
+    st = _calls().lora_add(Y, X, A, B, ids, order, scales, out, _handle(stream))
+    if st != 0:
+        torch = _torch()
+        T, K = _dims(X, 2, "X")
+        L, R, _ = _dims(A, 3, "A")
+        N = _dims(B, 3, "B")[1]
+        bf16, i32 = (torch.bfloat16,), (torch.int32,)
+        _refuse("fp8gemm_lora_add", st, (Y, "Y", bf16, (T, N), True), (X, "X", bf16, (T, K), True), (A, "A", bf16, (L, R, K)),
+                (B, "B", bf16, (L, N, R)), (ids, "ids", i32, (T,)), (order, "order", i32, (T,)),
+                (scales, "scales", (torch.float32,), (L,)), (out, "out", bf16, (T, N), True))
+    return out

@@ -27,6 +27,7 @@ SOURCES = [os.path.join(CSRC, "fp8gemm_kernels.hip"), os.path.join(CSRC, "stream
            os.path.join(CSRC, "quantize_kernels.hip"), os.path.join(CSRC, "scratch.hip"),
            os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "permute_kernels.hip"),
            os.path.join(CSRC, "w4_kernels.hip"), os.path.join(CSRC, "gated_kernels.hip"),
+           os.path.join(CSRC, "lora_kernels.hip"),
            os.path.join(CSRC, "fp8gemm_api.cpp"), os.path.join(CSRC, "moe_api.cpp"),
            os.path.join(CSRC, "ffn_api.cpp"),
            os.path.join(CSRC, "fp8gemm_jit.cpp")]

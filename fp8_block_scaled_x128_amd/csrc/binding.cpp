@@ -1,5 +1,6 @@
 // binding.cpp -- Python module `_native`: the short path from torch tensors to the C ABI for the
-// operators whose kernels take a few microseconds (routing, token permutation, 4-bit products).
+// operators whose kernels take a few microseconds (routing, token permutation, 4-bit products, the gated
+// block, low-rank adapters).
 // Each function reads its tensors' types, shapes and addresses directly, launches on the current
 // stream of their device (or the given one) and returns the C call's status, or -1 where an
 // argument is not what the call takes; the Python layer then finds out which one and raises.
@@ -30,12 +31,12 @@ struct Call {
     Call(PyObject* const* a, Py_ssize_t count, Py_ssize_t expected) : args(a), n(count), ok(count == expected) {}
 
     // Argument i as a tensor, or null: the call is refused (now or before), or it is `optional` and None.
-    const at::Tensor* tensor(int i, bool optional = false) {
+    const at::Tensor* tensor(int i, bool optional = false, bool strided = false) {
         if (!ok) return nullptr;
         if (optional && args[i] == Py_None) return nullptr;
         if (!THPVariable_Check(args[i])) return refuse();
         const at::Tensor& t = THPVariable_Unpack(args[i]);
-        if (!t.is_cuda() || !t.is_contiguous()) return refuse();
+        if (!t.is_cuda() || (!strided && !t.is_contiguous())) return refuse();
         if (device < 0) device = t.get_device();
         if (t.get_device() != device) return refuse();
         return &t;
@@ -45,6 +46,16 @@ struct Call {
         const at::Tensor* t = tensor(i, optional);
         if (!t) return nullptr;
         if (t->scalar_type() != type || t->sizes() != at::IntArrayRef(shape)) return refuse();
+        return t->data_ptr();
+    }
+    // Argument i, a bf16 matrix [rows][cols] whose rows are contiguous, `stride` values apart.
+    void* matrix(int i, int64_t rows, int64_t cols, int64_t* stride) {
+        const at::Tensor* t = tensor(i, false, true);
+        if (!t) return nullptr;
+        if (t->scalar_type() != at::kBFloat16 || t->dim() != 2 || t->size(0) != rows || t->size(1) != cols ||
+            (cols > 1 && t->stride(1) != 1))
+            return refuse();
+        *stride = rows > 1 ? t->stride(0) : cols;
         return t->data_ptr();
     }
     int64_t integer(int i) {
@@ -324,10 +335,35 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// (Y, X, A, B, ids, order, scales, out, stream)
+PyObject* lora_add(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Call c(args, n, 9);
+        const at::Tensor *x = c.tensor(1, false, true), *ta = c.tensor(2), *tb = c.tensor(3);
+        if (!x || !ta || !tb || x->dim() != 2 || ta->dim() != 3 || tb->dim() != 3) return PyLong_FromLong(kRefused);
+        const int64_t T = x->size(0), K = x->size(1), L = ta->size(0), R = ta->size(1), N = tb->size(1);
+        int64_t ldx = 0, ldy = 0, ldo = 0;
+        void* Y = c.matrix(0, T, N, &ldy);
+        void* X = c.matrix(1, T, K, &ldx);
+        void* A = c.data(2, kBFloat16, {L, R, K});
+        void* B = c.data(3, kBFloat16, {L, N, R});
+        void* ids = c.data(4, kInt, {T});
+        void* order = c.data(5, kInt, {T}, true);
+        void* scales = c.data(6, kFloat, {L}, true);
+        void* out = c.matrix(7, T, N, &ldo);
+        if (L != (int32_t)L || R != (int32_t)R) c.refuse();
+        return c.run(8, [&](void* s) {
+            return fp8gemm_lora_add(Y, X, A, B, (const int32_t*)ids, (const int32_t*)order, (const float*)scales, out, T, (int32_t)L,
+                                    (int32_t)R, K, N, ldx, ldy, ldo, s);
+        });
+    });
+}
+
 #define FP8GEMM_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP8GEMM_METHOD(route_topk), FP8GEMM_METHOD(route_topk_backward), FP8GEMM_METHOD(moe_dispatch),
                          FP8GEMM_METHOD(moe_combine), FP8GEMM_METHOD(moe_combine_backward), FP8GEMM_METHOD(w4_gemv),
                          FP8GEMM_METHOD(w4_gemv_experts), FP8GEMM_METHOD(gated_ffn), FP8GEMM_METHOD(gated_ffn_backward),
+                         FP8GEMM_METHOD(lora_add),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,4 +1,4 @@
-// ffn_api.cpp -- C ABI of the gated feed-forward block in bf16 and its gradients.  Argument validation,
+// ffn_api.cpp -- C ABI of the gated feed-forward block in bf16, its gradients, and low-rank adapters.  Argument validation,
 // launch-shape choice and launch (host code); meaning and layouts: include/fp8gemm.h.
 
 #include <hip/hip_runtime.h>
@@ -225,6 +225,70 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         st = launched();
     }
     return st;
+}
+
+int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B, const int32_t* ids, const int32_t* order,
+                     const float* scales, void* out, int64_t T, int32_t L, int32_t R, int64_t K, int64_t N, int64_t ldx,
+                     int64_t ldy, int64_t ldo, void* stream) {
+    if (T < 0 || L <= 0 || R <= 0 || R % 8 != 0 || K <= 0 || K % 8 != 0 || N < 0 || N % 8 != 0) return FP8GEMM_ERR_BAD_SHAPE;
+    if (T > 1 && (ldx < K || ldy < N || ldo < N || ldx % 8 != 0 || ldy % 8 != 0 || ldo % 8 != 0)) return FP8GEMM_ERR_BAD_SHAPE;
+    if (R > kLoraMaxRank || K > kMaxWidth || N > kMaxWidth || T >= (int64_t(1) << 31) - 64) return FP8GEMM_ERR_UNSUPPORTED;
+    if (T > 1 && std::max(ldx, std::max(ldy, ldo)) > kMaxBytes / 2 / T) return FP8GEMM_ERR_UNSUPPORTED;
+    if ((int64_t)L * R > kMaxBytes / 2 / std::max<int64_t>(std::max(K, N), 1)) return FP8GEMM_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0) return FP8GEMM_OK;
+    if (!Y || !X || !A || !B || !ids || !out) return FP8GEMM_ERR_NULL_PTR;
+    if (!aligned(Y, 16) || !aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16) || !aligned(ids, 4) ||
+        !aligned(order, 4) || !aligned(scales, 4))
+        return FP8GEMM_ERR_MISALIGNED;
+    HostDevice d;
+    int st = host_device(&d);
+    if (st != FP8GEMM_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    LoraArgs a{};
+    a.X = static_cast<const uint16_t*>(X);
+    a.A = static_cast<const uint16_t*>(A);
+    a.B = static_cast<const uint16_t*>(B);
+    a.Y = static_cast<const uint16_t*>(Y);
+    a.out = static_cast<uint16_t*>(out);
+    a.ids = ids;
+    a.order = order;
+    a.scales = scales;
+    a.err = d.err;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.ldo = ldo;
+    a.T = T;
+    a.L = L;
+    a.R = R;
+    a.K = (int32_t)K;
+    a.N = (int32_t)N;
+    a.rank = (R + 15) / 16 * 16;
+    a.steps = (int32_t)((K + 63) / 64);
+    const int tiles = T <= 512 ? 1 : a.rank > 64 ? 2 : 4;
+    const int64_t row_tiles = (T + 16 * tiles - 1) / (16 * tiles);
+    // splits of K that give the CUs two workgroups each, of at least a step for each of the four waves
+    const int64_t want = std::max<int64_t>(1, 2 * d.cus / row_tiles);
+    const int64_t splits = std::min<int64_t>(want, (a.steps + 3) / 4);
+    a.per_split = (int32_t)((a.steps + splits - 1) / splits);
+    a.splits = (a.steps + a.per_split - 1) / a.per_split;
+    // rows of a pass: the parts of A x fit the workspace, and the grid's second dimension
+    const int64_t room = (int64_t)d.cus * 512 * 1024 / ((int64_t)a.splits * a.rank * 4) / 64 * 64;
+    const int64_t pass = std::min<int64_t>(room, 32768 * 16);
+    const int64_t most = std::min(T, pass);
+    std::unique_lock<std::mutex> hold;
+    void* low = nullptr;
+    st = host_stream_scratch(s, (size_t)(most * a.splits * a.rank) * sizeof(float), &low, &hold);
+    if (st != FP8GEMM_OK) return st;
+    a.low = static_cast<float*>(low);
+    host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld rows=%lld split=%lld", {T, R, K, N, 16 * tiles, a.splits});
+    for (a.first = 0; a.first < T; a.first += pass) {
+        a.places = (int32_t)std::min(pass, T - a.first);
+        launch_lora_down(a, tiles, s);
+        launch_lora_up(a, tiles, s);
+        st = launched();
+        if (st != FP8GEMM_OK) return st;
+    }
+    return FP8GEMM_OK;
 }
 
 }  // extern "C"

@@ -74,6 +74,35 @@ struct GatedGradArgs {
 };
 void launch_gated_grad(const GatedGradArgs& a, hipStream_t s);
 
+// ---- low-rank adapters ----
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraSpan = 256;      // columns of the result that a workgroup takes
+
+struct LoraArgs {
+    const uint16_t* X;          // [T][ldx]
+    const uint16_t* A;          // [L][R][K]
+    const uint16_t* B;          // [L][N][R]
+    const uint16_t* Y;          // [T][ldy]
+    uint16_t* out;              // [T][ldo]
+    const int32_t* ids;         // [T]
+    const int32_t* order;       // [T] or null
+    const float* scales;        // [L] or null
+    float* low;                 // A x, partial sums: [splits][places][rank], rank padded to 16
+    int32_t* err;
+    int64_t ldx, ldy, ldo;
+    int64_t T;
+    int64_t first;              // first place (row, or position in order) of this pass
+    int32_t places;             // of this pass
+    int32_t L, R, K, N;
+    int32_t rank;               // R rounded up to 16
+    int32_t steps;              // ceil(K / 64)
+    int32_t splits, per_split;  // steps of a split, over the waves of a workgroup
+};
+
+// tiles: 16-row tiles of a workgroup, 1, 2 or 4
+void launch_lora_down(const LoraArgs& a, int tiles, hipStream_t s);
+void launch_lora_up(const LoraArgs& a, int tiles, hipStream_t s);
+
 // 16-byte units set to zero (a gradient over no rows).
 void launch_fill_zero(void* p, int64_t bytes, hipStream_t s);
 

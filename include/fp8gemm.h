@@ -365,6 +365,25 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
 int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, const void* pre, void* dpre, void* dX, void* dW,
                                int64_t M, int64_t I, int64_t K, int32_t act, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection (fp8gemm_nt, fp8gemm_w4_gemv, ...),
+ * whose bf16 results Y they are added to:
+ *   out[t] = bf16(Y[t] + scales[a] * B[a] (A[a] x[t])),  a = ids[t];  out[t] = Y[t] where ids[t] < 0
+ *   X [T][ldx], Y [T][ldy], out [T][ldo] bf16, rows of K, N and N values (strides in values, multiples
+ *   of 8); A [L][R][K], B [L][N][R] bf16; ids [T] int32; scales [L] fp32 or NULL (ones).
+ * Sums in fp32; A x enters the second product with 16 bits.  An adapter of smaller rank is padded with
+ * zeros.  out may be Y itself (rows without an adapter are then not written).  An id of L or more
+ * counts as none and flags FP8GEMM_DEVERR_BAD_INDEX.
+ *   order [T] int32 or NULL: a permutation of the rows that brings those of an adapter together.  It
+ *   changes no result, only the time of a batch in which neighbours have different adapters: rows are
+ *   taken 16 at a time (32 or 64 in batches of more than 512), each adapter among them in turn.  An
+ *   entry outside [0, T) is left out and flags FP8GEMM_DEVERR_BAD_INDEX; rows that it does not name are
+ *   not written, with repeated entries rows are unspecified.
+ * R: a positive multiple of 8, at most 128; K, N: multiples of 8, at most 2^20; X, Y, A, B, out 16-byte
+ * aligned.  Uses the stream's workspace (see fp8gemm_prepare_stream). */
+int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B, const int32_t* ids, const int32_t* order,
+                     const float* scales, void* out, int64_t T, int32_t L, int32_t R, int64_t K, int64_t N, int64_t ldx,
+                     int64_t ldy, int64_t ldo, void* stream);
+
 /* Device-side precondition flags (bits of the device error word). */
 #define FP8GEMM_DEVERR_BAD_INDEX 1 /* contiguous: an m_indices entry outside [-1, G) or off its block's group;
                                       combine: a row_map entry of R or more */
