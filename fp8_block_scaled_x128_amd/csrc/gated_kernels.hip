@@ -4,6 +4,7 @@
 // The mathematics and the limits are stated in include/fp8gemm.h.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn_internal.h"
 #include "fp8gemm_device.h"
@@ -97,11 +98,12 @@ struct Tile {
     static constexpr int PITCH = 2 * W_COLS + (CPR % 2 == 0 ? 16 : 0);
     static constexpr int STG = WM * PITCH;
     static constexpr int SMEM = STAGES * STAGE_BYTES > NW * STG ? STAGES * STAGE_BYTES : NW * STG;
-    static_assert(SMEM <= 160 * 1024, "LDS budget");
+    static_assert(SMEM < 160 * 1024, "LDS budget");
+    static constexpr int WAVES_PER_SIMD = NW / 4 * (SMEM < 80 * 1024 ? 2 : 1);   // as LDS allows
 };
 
 template <int BM, int BN, int WMW, int WNW, int STAGES, int KIND>
-__global__ __launch_bounds__(WMW * WNW * 64, 2) void product_kernel(const ProductArgs a) {
+__global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIND>::WAVES_PER_SIMD)) void product_kernel(const ProductArgs a) {
     using T = Tile<BM, BN, WMW, WNW, STAGES, KIND>;
     using OpP = typename T::OpP;
     using OpQ = typename T::OpQ;
@@ -152,22 +154,28 @@ __global__ __launch_bounds__(WMW * WNW * 64, 2) void product_kernel(const Produc
     const uint16_t* pbase = a.P + (T::PT ? (int64_t)s0 * 64 * a.ldp : (int64_t)m0 * a.ldp + (int64_t)s0 * 64);
     const uint16_t* qbase = a.Q + (T::QT ? (int64_t)s0 * 64 * a.ldq : (int64_t)n0 * a.ldq + (int64_t)s0 * 64);
     const int64_t pstep = T::PT ? (int64_t)64 * a.ldp : 64, qstep = T::QT ? (int64_t)64 * a.ldq : 64;
+    const int64_t up = (int64_t)a.cols * a.ldq;              // gated: from a gate row to its up row
     const int tail = a.K - (a.slices - 1) * 64;              // values of the last slice
     const int tail_at = tail < 64 ? a.slices - 1 - s0 : -1;  // this unit's slice that is not whole
 
-    auto issue = [&](int i) {
+    // load x of slice i (of a wave's NDMA: Q's, then P's)
+    auto issue = [&](int i, int x) {
         const uint32_t st = smem_base + (uint32_t)((i % STAGES) * T::STAGE_BYTES);
-        const uint16_t* qs[2];                               // with turned rows, and of gate rows; of up rows
-        qs[0] = uniform_ptr(qbase + i * qstep);
-        qs[1] = T::GATED ? uniform_ptr(qbase + i * qstep + (int64_t)a.cols * a.ldq) : qs[0];
-        const uint16_t* ps = uniform_ptr(pbase + i * pstep);
-        const bool part = i == tail_at;
+        if (x < OpQ::LOADS) {
+            const int l = wave * OpQ::LOADS + x;
+            dma_x4(st + l * 1024, uniform_ptr(qbase + i * qstep + (T::GATED && (l >> 1 & 1) ? up : 0)), qoff[x]);
+        } else {
+            const int l = wave * OpP::LOADS + x - OpQ::LOADS;
+            dma_x4(st + T::P_OFF + l * 1024, uniform_ptr(pbase + i * pstep), poff[x - OpQ::LOADS]);
+        }
+    };
+    // before the loads of slice i, in order: the last one may not be whole
+    auto aim = [&](int i) {
+        if (i != tail_at) return;
 #pragma unroll
-        for (int q = 0; q < OpQ::LOADS; ++q)
-            dma_x4(st + (wave * OpQ::LOADS + q) * 1024, T::GATED && ((wave * OpQ::LOADS + q) >> 1 & 1) ? qs[1] : qs[0], part ? q_off(q, tail) : qoff[q]);
+        for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, tail);
 #pragma unroll
-        for (int q = 0; q < OpP::LOADS; ++q)
-            dma_x4(st + T::P_OFF + (wave * OpP::LOADS + q) * 1024, ps, part ? p_off(q, tail) : poff[q]);
+        for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, tail);
     };
     // zeros in both operands for the values of k that the last slice does not have
     auto clear_tail = [&](int i) {
@@ -194,40 +202,74 @@ __global__ __launch_bounds__(WMW * WNW * 64, 2) void product_kernel(const Produc
 
     const int straight[2] = {((2 * grp) ^ swz(row16)) << 4, ((2 * grp + 1) ^ swz(row16)) << 4};
     const int tk = 16 * grp + (row16 >> 2);                   // a turned read's row of LDS
-    const int tp = turn<BM>(tk), tqr = turn<BN>(tk);         // and its permutations
+    const int turned_lane = (lane & 3) * 8, tp = turn<BM>(tk) << 5, tqr = turn<BN>(tk) << 5;   // and its permutations
     auto fragment = [&](const uint8_t* part, int row0, int s, bool turned, int row_bytes, int tx) -> v4u {
         if (!turned) return *reinterpret_cast<const v4u*>(part + (row0 + row16) * 128 + straight[s]);
-        const uint8_t* p = part + (tk + 8 * s) * row_bytes + (((row0 >> 4) ^ tx) << 5) + (lane & 3) * 8;
+        const uint8_t* p = part + ((row0 << 1) ^ tx) + (tk + 8 * s) * row_bytes + turned_lane;
         typedef __attribute__((address_space(3))) v4s* lds_v4s;
         const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p)));
         const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * row_bytes)));
         return (v4u){lo.x, lo.y, hi.x, hi.y};
     };
-    auto compute = [&](int i) {
+    // Fragments of a matrix-core step, P's first
+    struct Step {
+        v4u f[T::JM + T::IN];
+    };
+    // The products of the fragments in `from` and, in groups between them, reads of the fragments of step s of slice
+    // i and the loads of slice i2 (if LOAD): the matrix core, LDS and the loads' issue work side by side.
+    auto products = [&](const Step& from, Step& to, int i, int s, auto load, int i2) {
+        constexpr bool LOAD = decltype(load)::value;
+        constexpr int READS = T::JM + T::IN, MFMAS = T::JM * T::IN, GROUPS = LOAD && T::NDMA > 4 ? T::NDMA : 4;
         const uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
+        // (opaque: an address for each fragment, formed ahead of the loop, costs registers that spill)
+        int xp = tp, xq = tqr;
+        if constexpr (T::PT) asm volatile("" : "+v"(xp));
+        if constexpr (T::QT) asm volatile("" : "+v"(xq));
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            v4u pf[T::JM], qf[T::IN];
+        for (int g = 0; g < GROUPS; ++g) {
 #pragma unroll
-            for (int j = 0; j < T::JM; ++j) pf[j] = fragment(st + T::P_OFF, wm * T::WM + 16 * j, s, T::PT, OpP::ROW_BYTES, tp);
+            for (int x = READS * g / GROUPS; x < READS * (g + 1) / GROUPS; ++x)
+                to.f[x] = x < T::JM ? fragment(st + T::P_OFF, wm * T::WM + 16 * x, s, T::PT, OpP::ROW_BYTES, xp)
+                                    : fragment(st, wn * T::WN + 16 * (x - T::JM), s, T::QT, OpQ::ROW_BYTES, xq);
+            if constexpr (LOAD) {
 #pragma unroll
-            for (int i2 = 0; i2 < T::IN; ++i2) qf[i2] = fragment(st, wn * T::WN + 16 * i2, s, T::QT, OpQ::ROW_BYTES, tqr);
+                for (int x = T::NDMA * g / GROUPS; x < T::NDMA * (g + 1) / GROUPS; ++x)
+                    if (i2 < nks) issue(i2, x);
+            }
 #pragma unroll
-            for (int i2 = 0; i2 < T::IN; ++i2)
-#pragma unroll
-                for (int j = 0; j < T::JM; ++j) acc[i2][j] = mfma_bf16(qf[i2], pf[j], acc[i2][j]);
+            for (int x = MFMAS * g / GROUPS; x < MFMAS * (g + 1) / GROUPS; ++x)
+                acc[x / T::JM][x % T::JM] = mfma_bf16(from.f[T::JM + x / T::JM], from.f[x % T::JM], acc[x / T::JM][x % T::JM]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
+    // Slices stand in a ring of STAGES.  The second step's fragments of a slice are read during the products of
+    // its first, then the slice's place is free for slice i + STAGES, and the next slice's first step is read
+    // during the products of the second: a wave's matrix core works across the barrier.
+    Step f0, f1;
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        if (i < nks) issue(i);
+    for (int i = 0; i < STAGES; ++i) {
+        if (i >= nks) continue;
+        aim(i);
+#pragma unroll
+        for (int x = 0; x < T::NDMA; ++x) issue(i, x);
+    }
+    wait_slices<T::NDMA, STAGES - 1, 0>(min(STAGES - 1, nks - 1));
+    __syncthreads();
+    if (tail_at == 0) clear_tail(0);
+#pragma unroll
+    for (int x = 0; x < T::JM + T::IN; ++x)
+        f0.f[x] = x < T::JM ? fragment(smem + T::P_OFF, wm * T::WM + 16 * x, 0, T::PT, OpP::ROW_BYTES, tp)
+                            : fragment(smem, wn * T::WN + 16 * (x - T::JM), 0, T::QT, OpQ::ROW_BYTES, tqr);
     for (int i = 0; i < nks; ++i) {
-        wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2, nks - 1 - i));
-        __syncthreads();
-        if (i + STAGES - 1 < nks) issue(i + STAGES - 1);
-        if (i == tail_at) clear_tail(i);
-        compute(i);
+        products(f0, f1, i, 1, std::false_type{}, 0);
+        if (i + 1 < nks) {
+            wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2, nks - 2 - i));
+            __syncthreads();
+            aim(i + STAGES);
+            if (i + 1 == tail_at) clear_tail(i + 1);
+        }
+        products(f1, f0, min(i + 1, nks - 1), 0, std::true_type{}, i + STAGES);
     }
 
     // ---- K splits: the last workgroup of a tile to arrive sums the partials in split order -------------------
@@ -344,77 +386,62 @@ __global__ __launch_bounds__(WMW * WNW * 64, 2) void product_kernel(const Produc
 
 // ---- the block for few rows -----------------------------------------------------------------------------
 // A workgroup has 8 output columns, whose 8 gate rows and 8 up rows of W are the 16 rows of one matrix-core
-// operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in
-// turn; their sums meet in LDS and are added in wave order.
-constexpr int kRowsWaves = 8;
+// operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in turn, two on
+// their way each; their sums meet in LDS and are added in wave order.
+constexpr int kRowsWaves = 8, kRowsAhead = 2;
 
-// 64 values of k of step `step` as this lane's 8 for matrix-core steps 0 and 1: 16 (lane / 16) + 8 s
-__device__ __forceinline__ v4u load16(const __amdgpu_buffer_rsrc_t& b, int offset) {
-    return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(b, offset, 0, 0));
-}
-
-template <int MT, int PF>
 __global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const GatedRowsArgs a) {
-    __shared__ v4f red[kRowsWaves][MT][64];
+    __shared__ v4f red[kRowsWaves][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row16 = lane & 15, grp = lane >> 4;
-    const int n0 = blockIdx.x * 8;
+    const int n0 = blockIdx.x * 8, here = min(8, a.I - n0);
     const int K2 = a.K * 2, steps = (a.K + 63) / 64;
 
-    // gate rows n0.. and up rows I + n0..: one buffer from the first gate row to the last up row of the tile
-    const int64_t span = ((int64_t)a.I + min(8, a.I - n0)) * K2;
+    // gate rows n0.. and up rows I + n0..: one buffer from the first gate row to the last up row
     const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(uniform_ptr(a.W + (int64_t)n0 * a.K)), 0, (int)span, kBufferFlags);
+        const_cast<uint16_t*>(uniform_ptr(a.W + (int64_t)n0 * a.K)), 0, (a.I + here) * K2, kBufferFlags);
     const __amdgpu_buffer_rsrc_t xb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.X), 0, a.M * K2, kBufferFlags);
-    const int wrow = (min(row16 & 7, a.I - 1 - n0) + (row16 >> 3) * a.I) * K2 + grp * 32;
-    int xrow[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xrow[t] = min(t * 16 + row16, a.M - 1) * K2 + grp * 32;
+    const int wrow = (min(row16 & 7, here - 1) + (row16 >> 3) * a.I) * K2 + grp * 32;
+    const int xrow = min(row16, a.M - 1) * K2 + grp * 32;
 
-    v4f acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    // a step's 64 values of k: lane group grp has 16 of them, in halves for two matrix-core steps
     struct Slot {
-        v4u w[2], x[2][MT];
+        v4u w[2], x[2];
     };
-    Slot ring[PF];
+    Slot ring[kRowsAhead];
     auto load = [&](Slot& s, int step) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            // past the end of K: past the buffer, which reads as zeros
             const int k = step * 128 + h * 16;
-            const bool in = k + grp * 32 < K2;
-            s.w[h] = load16(wb, in ? wrow + k : -16);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) s.x[h][t] = load16(xb, in ? xrow[t] + k : -16);
+            const bool in = k + grp * 32 < K2;               // else past the buffer, which reads as zeros
+            s.w[h] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(wb, in ? wrow + k : -16, 0, 0));
+            s.x[h] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(xb, in ? xrow + k : -16, 0, 0));
         }
     };
 #pragma unroll
-    for (int p = 0; p < PF; ++p) load(ring[p], wave + p * kRowsWaves);
-    for (int s0 = wave; s0 < steps; s0 += kRowsWaves * PF) {
+    for (int p = 0; p < kRowsAhead; ++p) load(ring[p], wave + p * kRowsWaves);
+    for (int s0 = wave; s0 < steps; s0 += kRowsWaves * kRowsAhead) {
 #pragma unroll
-        for (int p = 0; p < PF; ++p) {
+        for (int p = 0; p < kRowsAhead; ++p) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) acc[t] = mfma_bf16(ring[p].w[h], ring[p].x[h][t], acc[t]);
-            load(ring[p], s0 + (p + PF) * kRowsWaves);
+            for (int h = 0; h < 2; ++h) acc = mfma_bf16(ring[p].w[h], ring[p].x[h], acc);
+            load(ring[p], s0 + (p + kRowsAhead) * kRowsWaves);
         }
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+    red[wave][lane] = acc;
     __syncthreads();
-    // output (row m, column n0 + c): gate sum in lane 16 (c / 4) + m % 16, element c % 4; up sum 32 lanes on
-    for (int x = tid; x < 8 * 16 * MT; x += kRowsWaves * 64) {
-        const int c = x & 7, m = x >> 3, t = m >> 4;
-        if (m >= a.M || n0 + c >= a.I) continue;
-        const int from = 16 * (c >> 2) + (m & 15);
+    // output (row m, column n0 + c): gate sum in lane 16 (c / 4) + m, element c % 4; up sum 32 lanes on
+    for (int x = tid; x < 8 * a.M; x += kRowsWaves * 64) {
+        const int c = x & 7, m = x >> 3;
+        if (c >= here) continue;
+        const int from = 16 * (c >> 2) + m;
         float g = 0.f, u = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowsWaves; ++w) {
-            g += red[w][t][from][c & 3];
-            u += red[w][t][from + 32][c & 3];
+            g += red[w][from][c & 3];
+            u += red[w][from + 32][c & 3];
         }
         a.out[(int64_t)m * a.I + n0 + c] = f32_to_bf16(activation(g, a.gelu) * u);
         if (a.pre) {
@@ -455,9 +482,10 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(v4u* p, int64_t units) {
 template <int KIND>
 void launch_kind(const ProductArgs& a, int shape, hipStream_t s) {
     const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n * a.splits));
-    if (shape == 0) product_kernel<256, 256, 4, 2, 2, KIND><<<grid, 512, 0, s>>>(a);
-    else if (shape == 1) product_kernel<128, 128, 2, 2, 2, KIND><<<grid, 256, 0, s>>>(a);
-    else product_kernel<64, 128, 2, 2, 3, KIND><<<grid, 256, 0, s>>>(a);
+    if (shape == 0) product_kernel<256, 256, 2, 4, 2, KIND><<<grid, 512, 0, s>>>(a);
+    else if (shape == 1) product_kernel<128, 256, 2, 4, 3, KIND><<<grid, 512, 0, s>>>(a);
+    else if (shape == 2) product_kernel<128, 128, 2, 4, 4, KIND><<<grid, 512, 0, s>>>(a);
+    else product_kernel<64, 64, 2, 2, 4, KIND><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -472,10 +500,7 @@ void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s
 }
 
 void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)((a.I + 7) / 8));
-    if (a.M <= 16) gated_rows_kernel<1, 4><<<grid, kRowsWaves * 64, 0, s>>>(a);
-    else if (a.M <= 32) gated_rows_kernel<2, 2><<<grid, kRowsWaves * 64, 0, s>>>(a);
-    else gated_rows_kernel<4, 2><<<grid, kRowsWaves * 64, 0, s>>>(a);
+    gated_rows_kernel<<<dim3((uint32_t)((a.I + 7) / 8)), kRowsWaves * 64, 0, s>>>(a);
 }
 
 void launch_gated_grad(const GatedGradArgs& a, hipStream_t s) {
