@@ -28,6 +28,7 @@ int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_E
 
 struct Choice {
     int shape, splits;
+    double us;                  // of its slices and exchange
 };
 
 // FP8GEMM_FORCE_CONFIG=product:BMxBN:SPLIT
@@ -37,35 +38,44 @@ bool forced(Choice* c) {
     if (!s || std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3) return false;
     for (int i = 0; i < kTileShapes; ++i)
         if (kTiles[i].bm == bm && kTiles[i].bn == bn) {
-            *c = {i, std::max(1, split)};
+            *c = {i, std::max(1, split), 0.0};
             return true;
         }
     return false;
 }
 
-// Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K.
+// Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K:
+// the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes.
 Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
-    Choice best{0, 1};
+    Choice best{0, 1, 1e30};
     if (forced(&best)) return best;
-    // us of a slice on a CU full of such workgroups
-    constexpr double kSlice[kTileShapes] = {1.45, 0.95, 0.62};
-    double least = 1e30;
     for (int i = 0; i < kTileShapes; ++i) {
         const TileShape& t = kTiles[i];
         const int64_t width = gated ? t.bn / 2 : t.bn;
         const int64_t tiles = ((rows + t.bm - 1) / t.bm) * ((cols + width - 1) / width);
-        for (int64_t s = 1; s <= 16 && s * 4 <= std::max<int64_t>(slices, 4); ++s) {
-            const int64_t units = tiles * s, slots = (int64_t)cus * t.per_cu;
-            if (s > 1 && units > slots) break;
-            const double per = (double)((slices + s - 1) / s);
-            const double cost = (double)((units + slots - 1) / slots) * (per * kSlice[i] + 3.0) + (s > 1 ? 3.0 + 0.3 * s : 0.0);
-            if (cost < least) {
-                least = cost;
-                best = {i, (int)s};
-            }
+        const int64_t slots = (int64_t)cus * t.per_cu;
+        for (int64_t s = 1; s <= 16 && (s == 1 || (s * 2 <= slices && tiles * s <= slots)); ++s) {
+            const int64_t per = (slices + s - 1) / s;
+            if (s > 1 && (slices + per - 1) / per != s) continue;
+            const int64_t units = tiles * s, last = units % slots;
+            const double cost = (double)per * ((double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared)) +
+                                (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
+            if (cost < best.us) best = {i, (int)s, cost};
         }
     }
     return best;
+}
+
+// Whether the kernel for few rows takes the block.  It brings X to every 8 columns' workgroup, so its time is
+// that of the weights and of X's copies, or of a wave's steps one after the other; tiles start and end slower.
+// Measured, rows and tiles, us: I = 2048, K = 7168: 1 row 11.3 and 14.2, 8 rows 12.8 and 14.4, 16 rows 15.0 and
+// 14.3; 4096 and 4096: 4 rows 14.2 and 14.5, 16 rows 18.0 and 14.5; 256 and 7168: 16 rows 14.9 and 10.4;
+// 1416 and 2056: 16 rows 5.7 and 8.3; 9216 and 7168: 1 row 54 and 58, 16 rows 79 and 58.
+bool few_rows(int64_t M, int64_t I, int64_t K, int cus) {
+    if (M > kGatedRowsMax || (I + 8) * K * 2 >= (int64_t(1) << 31)) return false;
+    const double rounds = (double)((K + 511) / 512);                             // steps of a wave
+    const double bytes = 4e-6 * (double)I * (double)K / 6.7 + 2e-6 * (double)M * (double)K * (double)((I + 7) / 8) / 12.0;
+    return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 4.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, true, cus).us;
 }
 
 // Sizes, order of the tiles and workspace of a product; `hold` keeps the workspace until the launch is enqueued.
@@ -115,7 +125,7 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     if (st != FP8GEMM_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     Choice c;
-    if (M <= kGatedRowsMax && (I + 8) * K * 2 < (int64_t(1) << 31) && !forced(&c)) {
+    if (!forced(&c) && few_rows(M, I, K, d.cus)) {
         GatedRowsArgs a{};
         a.X = static_cast<const uint16_t*>(X);
         a.W = static_cast<const uint16_t*>(W);
@@ -166,7 +176,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     if (st != FP8GEMM_OK) return st;
     // every choice and the workspace before the first launch
     std::unique_lock<std::mutex> hold;
-    Choice cp{0, 1}, cx{0, 1}, cw{0, 1};
+    Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0};
     ProductArgs ap{}, ax{}, aw{};
     if (!pre) {
         ap.P = static_cast<const uint16_t*>(X);
@@ -264,27 +274,38 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     a.N = (int32_t)N;
     a.rank = (R + 15) / 16 * 16;
     a.steps = (int32_t)((K + 63) / 64);
-    const int tiles = T <= 512 ? 1 : a.rank > 64 ? 2 : 4;
-    const int64_t row_tiles = (T + 16 * tiles - 1) / (16 * tiles);
-    // splits of K that give the CUs two workgroups each, of at least a step for each of the four waves
+    // Rows of a workgroup.  64, where there are many and an adapter has 16 of them or more on average: measured, 64
+    // and 16 rows, us: 8192 rows of 8 adapters, R = 32, 7168 to 4096, 64 and 117; 1000 of 4, R = 64, 22.5 and 26.0,
+    // but R = 16 15.2 and 14.0; 4096 of 64, R = 16, 38 and 42; 2048 of 128, R = 8, 32 and 25.  Else so few that the
+    // workgroups go through few adapters each, and 32 of them have rows: 1, 4 and 16 rows, us, 64 adapters, R = 16,
+    // 7168 to 4096: 16 rows 7.3, 10.8 and 19.3; 128 rows 15.6, 14.9 and 20.7; 512 rows 37, 26 and 16.5.
+    if (T >= 16 * (int64_t)L && T > (R > 32 ? 512 : 1024)) a.tile = 64;
+    else for (a.tile = 1; a.tile < 16 && a.tile * 32 < T;) a.tile *= 2;
+    const int64_t row_tiles = (T + a.tile - 1) / a.tile;
+    // splits of K that give the CUs two workgroups each, of 8 steps at least: 4, 8 and 16 steps, us: 1 row 7.5, 6.9
+    // and 7.4, 256 rows of 64 adapters 19.8, 16.3 and 20.1
     const int64_t want = std::max<int64_t>(1, 2 * d.cus / row_tiles);
-    const int64_t splits = std::min<int64_t>(want, (a.steps + 3) / 4);
+    const int64_t splits = std::min<int64_t>(want, (a.steps + 7) / 8);
     a.per_split = (int32_t)((a.steps + splits - 1) / splits);
     a.splits = (a.steps + a.per_split - 1) / a.per_split;
-    // rows of a pass: the parts of A x fit the workspace, and the grid's second dimension
-    const int64_t room = (int64_t)d.cus * 512 * 1024 / ((int64_t)a.splits * a.rank * 4) / 64 * 64;
-    const int64_t pass = std::min<int64_t>(room, 32768 * 16);
-    const int64_t most = std::min(T, pass);
+    // runs of columns that a workgroup takes one after the other, so that there are six for each CU where the rows
+    // allow it: 1, 6 and 16 for each CU, us: 8192 rows, R = 32 85, 64 and 65; 2000 rows, R = 128 50, 38 and 43
+    const int64_t spans = a.tile <= 16 ? (N + kLoraSpan - 1) / kLoraSpan : (N + 63) / 64;
+    a.chunks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(spans, spans * row_tiles / (6 * d.cus)));
+    // rows of a pass: the splits' sums of A x and its halves fit the workspace, the tiles the grid's second
+    // dimension and the counters
+    const int64_t row_bytes = (int64_t)a.rank * 4 * (a.splits + 1);
+    const int64_t room = (int64_t)d.cus * 512 * 1024 / row_bytes / 64 * 64;
+    const int64_t pass = std::min(T, std::min<int64_t>(room, (int64_t)4096 * a.tile));
     std::unique_lock<std::mutex> hold;
-    void* low = nullptr;
-    st = host_stream_scratch(s, (size_t)(most * a.splits * a.rank) * sizeof(float), &low, &hold);
+    st = host_stream_workspace(s, (size_t)(pass * row_bytes), a.tile == 64 ? (size_t)((pass + 63) / 64) : 0, &a.low, &a.counters, &hold);
     if (st != FP8GEMM_OK) return st;
-    a.low = static_cast<float*>(low);
-    host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld rows=%lld split=%lld", {T, R, K, N, 16 * tiles, a.splits});
+    a.halves = reinterpret_cast<uint16_t*>(a.low + pass * a.splits * a.rank);
+    host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld rows=%lld split=%lld", {T, R, K, N, a.tile, a.splits});
     for (a.first = 0; a.first < T; a.first += pass) {
         a.places = (int32_t)std::min(pass, T - a.first);
-        launch_lora_down(a, tiles, s);
-        launch_lora_up(a, tiles, s);
+        launch_lora_down(a, s);
+        launch_lora_up(a, s);
         st = launched();
         if (st != FP8GEMM_OK) return st;
     }

@@ -39,12 +39,17 @@ struct ProductArgs {
     FastDiv div_splits, div_band_units, div_band_h, div_band_h_last;
 };
 
+// Tiles of a workgroup: bm rows of P, bn rows of Q.  Times in us, measured: a slice where the workgroup has a
+// CU to itself, where `per_cu` share it (for all of them), and a K split's exchange (constant, and by split).
 struct TileShape {
-    int bm, bn;                 // rows of P and of Q
-    int per_cu;                 // workgroups a CU holds
+    int bm, bn, per_cu;
+    double alone, shared, exchange, exchange_split;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1}, {128, 128, 2}, {64, 128, 2}};
-constexpr int kTileShapes = 3;
+constexpr TileShape kTiles[] = {{256, 256, 1, 1.50, 1.50, 20.0, 2.7},
+                                {128, 256, 1, 0.88, 0.88, 8.0, 1.5},
+                                {128, 128, 1, 0.56, 0.56, 6.0, 0.7},
+                                {64, 64, 2, 0.27, 0.44, 1.0, 0.3}};
+constexpr int kTileShapes = 4;
 constexpr int kSliceK = 64;
 
 void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s);
@@ -58,7 +63,7 @@ struct GatedRowsArgs {
     int32_t M, I, K;
     int32_t gelu;
 };
-constexpr int kGatedRowsMax = 64;   // rows of X that the kernel takes
+constexpr int kGatedRowsMax = 16;   // rows of X that the kernel takes
 
 void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s);
 
@@ -76,7 +81,7 @@ void launch_gated_grad(const GatedGradArgs& a, hipStream_t s);
 
 // ---- low-rank adapters ----
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraSpan = 256;      // columns of the result that a workgroup takes
+constexpr int kLoraSpan = 256;      // columns of the result that a workgroup takes at a time
 
 struct LoraArgs {
     const uint16_t* X;          // [T][ldx]
@@ -88,20 +93,23 @@ struct LoraArgs {
     const int32_t* order;       // [T] or null
     const float* scales;        // [L] or null
     float* low;                 // A x, partial sums: [splits][places][rank], rank padded to 16
+    uint16_t* halves;           // tiles of 64 places: A x as two bf16 halves, [places][2][rank]
+    int32_t* counters;          // tiles of 64 places: arrivals, zero between launches
     int32_t* err;
     int64_t ldx, ldy, ldo;
     int64_t T;
     int64_t first;              // first place (row, or position in order) of this pass
     int32_t places;             // of this pass
+    int32_t tile;               // places of a workgroup: 64, or at most 16
     int32_t L, R, K, N;
     int32_t rank;               // R rounded up to 16
     int32_t steps;              // ceil(K / 64)
-    int32_t splits, per_split;  // steps of a split, over the waves of a workgroup
+    int32_t splits, per_split;  // steps of a split
+    int32_t chunks;             // runs of kLoraSpan columns that a workgroup takes
 };
 
-// tiles: 16-row tiles of a workgroup, 1, 2 or 4
-void launch_lora_down(const LoraArgs& a, int tiles, hipStream_t s);
-void launch_lora_up(const LoraArgs& a, int tiles, hipStream_t s);
+void launch_lora_down(const LoraArgs& a, hipStream_t s);
+void launch_lora_up(const LoraArgs& a, hipStream_t s);
 
 // 16-byte units set to zero (a gradient over no rows).
 void launch_fill_zero(void* p, int64_t bytes, hipStream_t s);
