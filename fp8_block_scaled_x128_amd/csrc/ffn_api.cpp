@@ -45,10 +45,14 @@ bool forced(Choice* c) {
 }
 
 // Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K:
-// the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes.
+// the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes, where
+// those take longer than reading both operands once.  Over 26 sizes of each product (17 to 4096 rows, I 64 to 2048, K
+// 128 to 7168) the choice is within 7% of the best of all tiles with 1 to 16 splits, but for three that are 13 to 17%
+// off (exchanges of many partials: 256 rows, 2048, 7168; dX of 3565 and 3808 rows, K about 400).
 Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
     Choice best{0, 1, 1e30};
     if (forced(&best)) return best;
+    const double bytes = 128e-6 * (double)slices * (double)(rows + (gated ? 2 : 1) * cols) / 5.2;
     for (int i = 0; i < kTileShapes; ++i) {
         const TileShape& t = kTiles[i];
         const int64_t width = gated ? t.bn / 2 : t.bn;
@@ -58,8 +62,8 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
             const int64_t per = (slices + s - 1) / s;
             if (s > 1 && (slices + per - 1) / per != s) continue;
             const int64_t units = tiles * s, last = units % slots;
-            const double cost = (double)per * ((double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared)) +
-                                (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
+            const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared);
+            const double cost = std::max((double)per * rounds, bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
             if (cost < best.us) best = {i, (int)s, cost};
         }
     }
@@ -68,13 +72,13 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
 
 // Whether the kernel for few rows takes the block.  It brings X to every 8 columns' workgroup, so its time is
 // that of the weights and of X's copies, or of a wave's steps one after the other; tiles start and end slower.
-// Measured, rows and tiles, us: I = 2048, K = 7168: 1 row 11.3 and 14.2, 8 rows 12.8 and 14.4, 16 rows 15.0 and
-// 14.3; 4096 and 4096: 4 rows 14.2 and 14.5, 16 rows 18.0 and 14.5; 256 and 7168: 16 rows 14.9 and 10.4;
-// 1416 and 2056: 16 rows 5.7 and 8.3; 9216 and 7168: 1 row 54 and 58, 16 rows 79 and 58.
+// Measured, rows and tiles, us: I = 2048, K = 7168: 1 row 11.2 and 14.2, 8 rows 13.0 and 14.2, 16 rows 15.3 and
+// 14.2; 4096 and 4096: 4 rows 14.3 and 15.1, 16 rows 18.1 and 15.1; 256 and 7168: 16 rows 14.9 and 10.1;
+// 1416 and 2056: 16 rows 5.8 and 8.7.
 bool few_rows(int64_t M, int64_t I, int64_t K, int cus) {
     if (M > kGatedRowsMax || (I + 8) * K * 2 >= (int64_t(1) << 31)) return false;
     const double rounds = (double)((K + 511) / 512);                             // steps of a wave
-    const double bytes = 4e-6 * (double)I * (double)K / 6.7 + 2e-6 * (double)M * (double)K * (double)((I + 7) / 8) / 12.0;
+    const double bytes = 4e-6 * (double)I * (double)K / 5.2 + 2e-6 * (double)M * (double)K * (double)((I + 7) / 8) / 12.0;
     return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 4.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, true, cus).us;
 }
 

@@ -45,10 +45,10 @@ struct TileShape {
     int bm, bn, per_cu;
     double alone, shared, exchange, exchange_split;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1, 1.50, 1.50, 20.0, 2.7},
-                                {128, 256, 1, 0.88, 0.88, 8.0, 1.5},
-                                {128, 128, 1, 0.56, 0.56, 6.0, 0.7},
-                                {64, 64, 2, 0.27, 0.44, 1.0, 0.3}};
+constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 20.0, 2.7},
+                                {128, 256, 1, 0.86, 0.86, 8.0, 1.5},
+                                {128, 128, 1, 0.50, 0.50, 6.0, 0.7},
+                                {64, 64, 2, 0.25, 0.40, 1.0, 0.3}};
 constexpr int kTileShapes = 4;
 constexpr int kSliceK = 64;
 

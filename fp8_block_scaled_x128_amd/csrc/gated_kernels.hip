@@ -216,9 +216,9 @@ __global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIN
         v4u f[T::JM + T::IN];
     };
     // The products of the fragments in `from` and, in groups between them, reads of the fragments of step s of slice
-    // i and the loads of slice i2 (if LOAD): the matrix core, LDS and the loads' issue work side by side.
+    // i and the loads of slice i2 (load 1: if there is one, 2: there is): the matrix core, LDS and the loads' issue work side by side.
     auto products = [&](const Step& from, Step& to, int i, int s, auto load, int i2) {
-        constexpr bool LOAD = decltype(load)::value;
+        constexpr bool LOAD = decltype(load)::value != 0, CERTAIN = decltype(load)::value == 2;
         constexpr int READS = T::JM + T::IN, MFMAS = T::JM * T::IN, GROUPS = LOAD && T::NDMA > 4 ? T::NDMA : 4;
         const uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
         // (opaque: an address for each fragment, formed ahead of the loop, costs registers that spill)
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIN
             if constexpr (LOAD) {
 #pragma unroll
                 for (int x = T::NDMA * g / GROUPS; x < T::NDMA * (g + 1) / GROUPS; ++x)
-                    if (i2 < nks) issue(i2, x);
+                    if (CERTAIN || i2 < nks) issue(i2, x);
             }
 #pragma unroll
             for (int x = MFMAS * g / GROUPS; x < MFMAS * (g + 1) / GROUPS; ++x)
@@ -261,15 +261,27 @@ __global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIN
     for (int x = 0; x < T::JM + T::IN; ++x)
         f0.f[x] = x < T::JM ? fragment(smem + T::P_OFF, wm * T::WM + 16 * x, 0, T::PT, OpP::ROW_BYTES, tp)
                             : fragment(smem, wn * T::WN + 16 * (x - T::JM), 0, T::QT, OpQ::ROW_BYTES, tqr);
-    for (int i = 0; i < nks; ++i) {
-        products(f0, f1, i, 1, std::false_type{}, 0);
+    using load = std::integral_constant<int, 1>;
+    using load_surely = std::integral_constant<int, 2>;
+    using none = std::integral_constant<int, 0>;
+    int i = 0;
+    // slices with a whole one to load, without a branch
+    const int steady = nks - STAGES - (tail_at >= 0 ? 1 : 0);
+    for (; i < steady; ++i) {
+        products(f0, f1, i, 1, none{}, 0);
+        wait_vmcnt<T::NDMA * (STAGES - 2)>();
+        __syncthreads();
+        products(f1, f0, i + 1, 0, load_surely{}, i + STAGES);
+    }
+    for (; i < nks; ++i) {
+        products(f0, f1, i, 1, none{}, 0);
         if (i + 1 < nks) {
             wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2, nks - 2 - i));
             __syncthreads();
             aim(i + STAGES);
             if (i + 1 == tail_at) clear_tail(i + 1);
         }
-        products(f1, f0, min(i + 1, nks - 1), 0, std::true_type{}, i + STAGES);
+        products(f1, f0, min(i + 1, nks - 1), 0, load{}, i + STAGES);
     }
 
     // ---- K splits: the last workgroup of a tile to arrive sums the partials in split order -------------------
