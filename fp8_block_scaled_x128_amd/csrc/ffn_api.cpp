@@ -7,7 +7,9 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "ffn_internal.h"
 #include "fp8gemm.h"
@@ -44,15 +46,18 @@ bool forced(Choice* c) {
     return false;
 }
 
+double slower(const TileShape& t, Product kind) { return kind == kTimesW ? t.turned : kind == kTurned ? t.both_turned : 1.0; }
+
 // Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K:
 // the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes, where
-// those take longer than reading both operands once.  Over 26 sizes of each product (17 to 4096 rows, I 64 to 2048, K
+// those take longer than reading both operands and writing the result.  Over 26 sizes of each product (17 to 4096 rows, I 64 to 2048, K
 // 128 to 7168) the choice is within 7% of the best of all tiles with 1 to 16 splits, but for three that are 13 to 17%
 // off (exchanges of many partials: 256 rows, 2048, 7168; dX of 3565 and 3808 rows, K about 400).
-Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
+Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus) {
+    const bool gated = kind == kGated || kind == kGatedBack;
     Choice best{0, 1, 1e30};
     if (forced(&best)) return best;
-    const double bytes = 128e-6 * (double)slices * (double)(rows + (gated ? 2 : 1) * cols) / 5.2;
+    const double bytes = (128e-6 * (double)slices * (double)(rows + (gated ? 2 : 1) * cols) + 2e-6 * (double)rows * (double)cols) / 5.2;
     for (int i = 0; i < kTileShapes; ++i) {
         const TileShape& t = kTiles[i];
         const int64_t width = gated ? t.bn / 2 : t.bn;
@@ -63,7 +68,7 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, bool gated, int cus) {
             if (s > 1 && (slices + per - 1) / per != s) continue;
             const int64_t units = tiles * s, last = units % slots;
             const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared);
-            const double cost = std::max((double)per * rounds, bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
+            const double cost = std::max(((double)per + t.ends) * rounds * slower(t, kind), bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
             if (cost < best.us) best = {i, (int)s, cost};
         }
     }
@@ -79,13 +84,62 @@ bool few_rows(int64_t M, int64_t I, int64_t K, int cus) {
     if (M > kGatedRowsMax || (I + 8) * K * 2 >= (int64_t(1) << 31)) return false;
     const double rounds = (double)((K + 511) / 512);                             // steps of a wave
     const double bytes = 4e-6 * (double)I * (double)K / 5.2 + 2e-6 * (double)M * (double)K * (double)((I + 7) / 8) / 12.0;
-    return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 4.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, true, cus).us;
+    return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 3.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, cus).us;
 }
 
-// Sizes, order of the tiles and workspace of a product; `hold` keeps the workspace until the launch is enqueued.
-int plan(ProductArgs* a, Choice* c, bool gated, int cus, hipStream_t stream, std::unique_lock<std::mutex>* hold) {
+// Time, in slices, until n units of L slices and then n2 of L2 are done on `slots` places that take the next unit as
+// they get free: half way between the mean load and what units that all take the same time would need.
+double rounds_of(int64_t n, double L, int64_t n2, double L2, int64_t slots) {
+    const int64_t late = n % slots;
+    const double a = (double)(n / slots) * L, b = late ? a + L : a;
+    // every place has time for at least (mean - a) / L2 of the second, rounded down
+    const double mean = ((double)n * L + (double)n2 * L2) / (double)slots;
+    for (int64_t k = std::max<int64_t>(1, (int64_t)((mean - a) / L2));; ++k) {
+        const double t = a + (double)k * L2;
+        if ((slots - late) * k + (t > b ? late * (int64_t)((t - b) / L2) : 0) >= n2) return std::max(L, 0.5 * (mean + std::max(t, b)));
+    }
+}
+
+// dX and dW as one launch, if that is quicker than one after the other (the second's units fill the CUs that the
+// first's last ones leave, but L2 serves both): a shape for both, and the splits of each.  Measured, one after the
+// other and together, us: M = 1023, I = 1416, K = 2056 55 and 47; 1024, 2048, 7168 138 and 120; 905, 336, 456 17.8 and
+// 13.1; 77, 512, 1536 12.7 and 11.4; but 256, 2048, 7168 62 and 73, 4096, 2048, 7168 417 and 420.
+bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx, Choice* cw) {
+    if (forced(cx)) {
+        *cw = *cx;
+        return true;
+    }
+    const int64_t sx = (x.K + kSliceK - 1) / kSliceK, sw = (w.K + kSliceK - 1) / kSliceK;
+    const double bytes = (128e-6 * ((double)sx * (double)(x.rows + x.cols) + (double)sw * (double)(w.rows + w.cols)) +
+                          2e-6 * ((double)x.rows * (double)x.cols + (double)w.rows * (double)w.cols)) / 5.2;
+    double least = cx->us + cw->us + 3.5;
+    bool pair = false;
+    for (int i = 0; i < kTileShapes; ++i) {
+        const TileShape& t = kTiles[i];
+        auto tiles = [&](const ProductArgs& a) { return (((int64_t)a.rows + t.bm - 1) / t.bm) * (((int64_t)a.cols + t.bn - 1) / t.bn); };
+        const int64_t tx = tiles(x), tw = tiles(w), slots = (int64_t)cus * t.per_cu;
+        for (int64_t px = 1; px <= 8 && (px == 1 || (px * 2 <= sx && px * tx <= slots)); px *= 2)
+            for (int64_t pw = 1; pw <= 8 && (pw == 1 || (pw * 2 <= sw && pw * tw <= slots)); pw *= 2) {
+                const double lx = ((double)((sx + px - 1) / px) + t.ends) * t.turned;
+                const double lw = ((double)((sw + pw - 1) / pw) + t.ends) * t.both_turned;
+                const int64_t nx = tx * px, nw = tw * pw;
+                const double rounds = lx >= lw ? rounds_of(nx, lx, nw, lw, slots) : rounds_of(nw, lw, nx, lx, slots);
+                const int64_t most = std::max(px > 1 ? px : 0, pw > 1 ? pw : 0);
+                const double us = 1.03 * std::max(rounds * (nx + nw <= cus ? t.alone : t.shared), bytes) +
+                                  (most ? t.exchange + t.exchange_split * (double)most : 0.0);
+                if (us >= least) continue;
+                least = us;
+                pair = true;
+                *cx = {i, (int)px, us};
+                *cw = {i, (int)pw, us};
+            }
+    }
+    return pair;
+}
+
+// Sizes and order of the tiles of a product.
+int arrange(ProductArgs* a, Choice* c, bool gated) {
     a->slices = (a->K + kSliceK - 1) / kSliceK;
-    *c = choose(a->rows, a->cols, a->slices, gated, cus);
     const TileShape& t = kTiles[c->shape];
     const int width = gated ? t.bn / 2 : t.bn;
     const int64_t tm = ((int64_t)a->rows + t.bm - 1) / t.bm, tn = ((int64_t)a->cols + width - 1) / width;
@@ -99,10 +153,34 @@ int plan(ProductArgs* a, Choice* c, bool gated, int cus, hipStream_t stream, std
     a->div_band_units = make_fastdiv((uint32_t)(a->group_m * tn));
     a->div_band_h = make_fastdiv((uint32_t)a->group_m);
     a->div_band_h_last = make_fastdiv((uint32_t)(tm - (tm - 1) / a->group_m * a->group_m));
-    if (a->splits == 1) return FP8GEMM_OK;
-    // (a call of several products takes the same workspace for each: the stream orders them)
-    return host_stream_workspace(stream, (size_t)(tm * tn) * a->splits * t.bm * t.bn * sizeof(float), (size_t)(tm * tn), &a->ws,
-                                 &a->counters, hold->owns_lock() ? nullptr : hold);
+    return FP8GEMM_OK;
+}
+
+// The stream's workspace for the K splits of products that may run at the same time, one part after the other; `hold`
+// keeps it until the launches are enqueued.
+int share_workspace(std::initializer_list<std::pair<ProductArgs*, Choice>> products, hipStream_t stream, std::unique_lock<std::mutex>* hold) {
+    size_t floats = 0, tiles = 0;
+    for (const auto& p : products) {
+        if (p.first->splits <= 1) continue;
+        const size_t n = (size_t)p.first->tiles_m * p.first->tiles_n;
+        tiles += n;
+        floats += n * p.first->splits * kTiles[p.second.shape].bm * kTiles[p.second.shape].bn;
+    }
+    if (tiles == 0) return FP8GEMM_OK;
+    float* ws = nullptr;
+    int32_t* counters = nullptr;
+    const int st = host_stream_workspace(stream, floats * sizeof(float), tiles, &ws, &counters,
+                                         hold->owns_lock() ? nullptr : hold);
+    if (st != FP8GEMM_OK) return st;
+    for (const auto& p : products) {
+        if (p.first->splits <= 1) continue;
+        const size_t n = (size_t)p.first->tiles_m * p.first->tiles_n;
+        p.first->ws = ws;
+        p.first->counters = counters;
+        counters += n;
+        ws += n * p.first->splits * kTiles[p.second.shape].bm * kTiles[p.second.shape].bn;
+    }
+    return FP8GEMM_OK;
 }
 
 int check_gated(int64_t M, int64_t I, int64_t K, int32_t act) {
@@ -152,8 +230,11 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     a.cols = (int32_t)I;
     a.K = a.ldp = a.ldq = (int32_t)K;
     a.gelu = act == FP8GEMM_ACT_GELU_TANH;
+    c = choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, d.cus);
+    st = arrange(&a, &c, true);
+    if (st != FP8GEMM_OK) return st;
     std::unique_lock<std::mutex> hold;
-    st = plan(&a, &c, true, d.cus, s, &hold);
+    st = share_workspace({{&a, c}}, s, &hold);
     if (st != FP8GEMM_OK) return st;
     host_set_config("gated_ffn M=%lld I=%lld K=%lld tile=%lldx%lld split=%lld",
                     {M, I, K, kTiles[c.shape].bm, kTiles[c.shape].bn, c.splits});
@@ -179,9 +260,9 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     st = host_device(&d);
     if (st != FP8GEMM_OK) return st;
     // every choice and the workspace before the first launch
-    std::unique_lock<std::mutex> hold;
     Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0};
     ProductArgs ap{}, ax{}, aw{};
+    auto slices = [](int64_t k) { return (k + kSliceK - 1) / kSliceK; };
     if (!pre) {
         ap.P = static_cast<const uint16_t*>(X);
         ap.Q = static_cast<const uint16_t*>(W);
@@ -191,7 +272,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ap.cols = (int32_t)I;
         ap.K = ap.ldp = ap.ldq = (int32_t)K;
         ap.gelu = act == FP8GEMM_ACT_GELU_TANH;
-        st = plan(&ap, &cp, true, d.cus, s, &hold);
+        cp = choose(M, I, slices(K), kGatedBack, d.cus);
+        st = arrange(&ap, &cp, true);
         if (st != FP8GEMM_OK) return st;
     }
     if (dX) {
@@ -201,8 +283,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ax.rows = (int32_t)M;
         ax.cols = ax.ldq = (int32_t)K;
         ax.K = ax.ldp = (int32_t)(2 * I);
-        st = plan(&ax, &cx, false, d.cus, s, &hold);
-        if (st != FP8GEMM_OK) return st;
+        cx = choose(M, K, slices(2 * I), kTimesW, d.cus);
     }
     if (dW) {
         aw.P = static_cast<const uint16_t*>(dpre);
@@ -211,11 +292,20 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         aw.rows = aw.ldp = (int32_t)(2 * I);
         aw.cols = aw.ldq = (int32_t)K;
         aw.K = (int32_t)M;
-        st = plan(&aw, &cw, false, d.cus, s, &hold);
-        if (st != FP8GEMM_OK) return st;
+        cw = choose(2 * I, K, slices(M), kTurned, d.cus);
     }
-    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld again=%lld dX tile=%lld split=%lld dW tile=%lld split=%lld",
-                    {M, I, K, pre ? 0 : cp.splits, dX ? kTiles[cx.shape].bm : 0, cx.splits, dW ? kTiles[cw.shape].bm : 0, cw.splits});
+    const bool pair = dX && dW && choose_pair(ax, aw, d.cus, &cx, &cw);
+    if (dX && (st = arrange(&ax, &cx, false)) != FP8GEMM_OK) return st;
+    if (dW && (st = arrange(&aw, &cw, false)) != FP8GEMM_OK) return st;
+    if (pair && (int64_t)ax.tiles_m * ax.tiles_n * ax.splits + (int64_t)aw.tiles_m * aw.tiles_n * aw.splits > kMaxUnits)
+        return FP8GEMM_ERR_UNSUPPORTED;
+    // (dX and dW, which follow, take the first product's part again)
+    std::unique_lock<std::mutex> hold;
+    st = share_workspace({{&ap, cp}}, s, &hold);
+    if (st == FP8GEMM_OK) st = share_workspace({{&ax, cx}, {&aw, cw}}, s, &hold);
+    if (st != FP8GEMM_OK) return st;
+    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lld split=%lld dW tile=%lld split=%lld",
+                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, cx.splits, dW ? kTiles[cw.shape].bm : 0, cw.splits});
     if (pre) {
         GatedGradArgs g{};
         g.pre = static_cast<const uint16_t*>(pre);
@@ -230,6 +320,10 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         launch_product(ap, kGatedBack, cp.shape, s);
     }
     st = launched();
+    if (st == FP8GEMM_OK && pair) {
+        launch_gradients(ax, aw, cx.shape, s);
+        return launched();
+    }
     if (st == FP8GEMM_OK && dX) {
         launch_product(ax, kTimesW, cx.shape, s);
         st = launched();

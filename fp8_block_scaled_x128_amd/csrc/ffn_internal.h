@@ -40,19 +40,23 @@ struct ProductArgs {
 };
 
 // Tiles of a workgroup: bm rows of P, bn rows of Q.  Times in us, measured: a slice where the workgroup has a
-// CU to itself, where `per_cu` share it (for all of them), and a K split's exchange (constant, and by split).
+// CU to itself, and where `per_cu` share it (for all of them); how much longer it takes with Q turned, and with both
+// operands; its start and end, in slices; a K split's exchange (constant, and by split).
 struct TileShape {
     int bm, bn, per_cu;
-    double alone, shared, exchange, exchange_split;
+    double alone, shared, turned, both_turned, ends, exchange, exchange_split;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 20.0, 2.7},
-                                {128, 256, 1, 0.86, 0.86, 8.0, 1.5},
-                                {128, 128, 1, 0.50, 0.50, 6.0, 0.7},
-                                {64, 64, 2, 0.25, 0.40, 1.0, 0.3}};
+constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 1.00, 1.05, 5.3, 20.0, 2.7},
+                                {128, 256, 1, 0.83, 0.83, 1.05, 1.15, 6.0, 8.0, 1.5},
+                                {128, 128, 1, 0.47, 0.47, 1.15, 1.30, 8.0, 6.0, 0.7},
+                                {64, 64, 2, 0.25, 0.46, 1.05, 1.10, 5.3, 1.0, 0.3}};
 constexpr int kTileShapes = 4;
 constexpr int kSliceK = 64;
 
 void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s);
+
+// kTimesW and kTurned with tiles of one shape, as one launch
+void launch_gradients(const ProductArgs& x, const ProductArgs& w, int shape, hipStream_t s);
 
 // ---- the block for few rows ----
 struct GatedRowsArgs {

@@ -78,8 +78,9 @@ struct Operand {
     }
 };
 
-template <int BM, int BN, int WMW, int WNW, int STAGES, int KIND>
+template <int BM_, int BN_, int WMW_, int WNW_, int STAGES_, int KIND_>
 struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WMW = WMW_, WNW = WNW_, STAGES = STAGES_, KIND = KIND_;
     static constexpr bool PT = KIND == kTurned, QT = KIND == kTimesW || KIND == kTurned;
     static constexpr bool GATED = KIND == kGated || KIND == kGatedBack;
     static constexpr int NW = WMW * WNW, NT = 64 * NW;
@@ -102,13 +103,12 @@ struct Tile {
     static constexpr int WAVES_PER_SIMD = NW / 4 * (SMEM < 80 * 1024 ? 2 : 1);   // as LDS allows
 };
 
-template <int BM, int BN, int WMW, int WNW, int STAGES, int KIND>
-__global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIND>::WAVES_PER_SIMD)) void product_kernel(const ProductArgs a) {
-    using T = Tile<BM, BN, WMW, WNW, STAGES, KIND>;
+// Unit `block` of the `blocks` of a product; smem: T::SMEM bytes.
+template <class T>
+__device__ __forceinline__ void product(const ProductArgs& a, int block, int blocks, uint8_t* smem, int& s_flag) {
+    constexpr int BM = T::BM, BN = T::BN, WMW = T::WMW, STAGES = T::STAGES, KIND = T::KIND;
     using OpP = typename T::OpP;
     using OpQ = typename T::OpQ;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
-    __shared__ int s_flag;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIN
 
     // Workgroups are dealt to the 8 XCDs in turn: those of one XCD take consecutive units, which share operands
     // in its L2.
-    const int U = gridDim.x, xcd = blockIdx.x & 7;
-    const int unit = xcd * (U >> 3) + min(xcd, U & 7) + (blockIdx.x >> 3);
+    const int xcd = block & 7;
+    const int unit = xcd * (blocks >> 3) + min(xcd, blocks & 7) + (block >> 3);
     // split fastest, then the M tile within a band of group_m of them, then the N tile
     const uint32_t tile = fast_div((uint32_t)unit, a.div_splits);
     const int split = unit - (int)tile * a.splits;
@@ -396,6 +396,25 @@ __global__ __launch_bounds__(WMW * WNW * 64, (Tile<BM, BN, WMW, WNW, STAGES, KIN
     }
 }
 
+template <class T>
+__global__ __launch_bounds__(T::NT, T::WAVES_PER_SIMD) void product_kernel(const ProductArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
+    __shared__ int s_flag;
+    product<T>(a, blockIdx.x, gridDim.x, smem, s_flag);
+}
+
+// Two products that need nothing of each other, as one launch: the second's workgroups fill the CUs that the first's
+// last ones leave.
+template <class T, class T2>
+__global__ __launch_bounds__(T::NT, T::WAVES_PER_SIMD) void product_pair_kernel(const ProductArgs a, const ProductArgs b) {
+    static_assert(T::NT == T2::NT && T::SMEM == T2::SMEM, "one shape");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
+    __shared__ int s_flag;
+    const int first = a.tiles_m * a.tiles_n * a.splits;
+    if ((int)blockIdx.x < first) product<T>(a, blockIdx.x, first, smem, s_flag);
+    else product<T2>(b, blockIdx.x - first, gridDim.x - first, smem, s_flag);
+}
+
 // ---- the block for few rows -----------------------------------------------------------------------------
 // A workgroup has 8 output columns, whose 8 gate rows and 8 up rows of W are the 16 rows of one matrix-core
 // operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in turn, two on
@@ -492,12 +511,35 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(v4u* p, int64_t units) {
 }
 
 template <int KIND>
+using Tile256 = Tile<256, 256, 2, 4, 2, KIND>;
+template <int KIND>
+using Tile128x256 = Tile<128, 256, 2, 4, 3, KIND>;
+template <int KIND>
+using Tile128 = Tile<128, 128, 2, 4, 4, KIND>;
+template <int KIND>
+using Tile64 = Tile<64, 64, 2, 2, 4, KIND>;
+
+uint32_t units(const ProductArgs& a) { return (uint32_t)(a.tiles_m * a.tiles_n * a.splits); }
+
+template <template <int> class T, int KIND>
+void launch_one(const ProductArgs& a, hipStream_t s) {
+    product_kernel<T<KIND>><<<dim3(units(a)), T<KIND>::NT, 0, s>>>(a);
+}
+
+template <int KIND>
 void launch_kind(const ProductArgs& a, int shape, hipStream_t s) {
-    const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n * a.splits));
-    if (shape == 0) product_kernel<256, 256, 2, 4, 2, KIND><<<grid, 512, 0, s>>>(a);
-    else if (shape == 1) product_kernel<128, 256, 2, 4, 3, KIND><<<grid, 512, 0, s>>>(a);
-    else if (shape == 2) product_kernel<128, 128, 2, 4, 4, KIND><<<grid, 512, 0, s>>>(a);
-    else product_kernel<64, 64, 2, 2, 4, KIND><<<grid, 256, 0, s>>>(a);
+    if (shape == 0) launch_one<Tile256, KIND>(a, s);
+    else if (shape == 1) launch_one<Tile128x256, KIND>(a, s);
+    else if (shape == 2) launch_one<Tile128, KIND>(a, s);
+    else launch_one<Tile64, KIND>(a, s);
+}
+
+// the longer units first
+template <template <int> class T>
+void launch_two(const ProductArgs& x, const ProductArgs& w, hipStream_t s) {
+    const dim3 grid(units(x) + units(w));
+    if (x.per_split >= w.per_split) product_pair_kernel<T<kTimesW>, T<kTurned>><<<grid, T<kTurned>::NT, 0, s>>>(x, w);
+    else product_pair_kernel<T<kTurned>, T<kTimesW>><<<grid, T<kTurned>::NT, 0, s>>>(w, x);
 }
 
 }  // namespace
@@ -509,6 +551,13 @@ void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s
         case kTimesW: return launch_kind<kTimesW>(a, shape, s);
         case kTurned: return launch_kind<kTurned>(a, shape, s);
     }
+}
+
+void launch_gradients(const ProductArgs& x, const ProductArgs& w, int shape, hipStream_t s) {
+    if (shape == 0) launch_two<Tile256>(x, w, s);
+    else if (shape == 1) launch_two<Tile128x256>(x, w, s);
+    else if (shape == 2) launch_two<Tile128>(x, w, s);
+    else launch_two<Tile64>(x, w, s);
 }
 
 void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s) {
