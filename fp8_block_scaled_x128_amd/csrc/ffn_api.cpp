@@ -372,6 +372,14 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     a.N = (int32_t)N;
     a.rank = (R + 15) / 16 * 16;
     a.steps = (int32_t)((K + 63) / 64);
+    // A workgroup a row, one launch and no workspace, while each of an adapter's matrices is small: the kernel's comment
+    // has both sides.  Of many rows (1000, R = 8, 256 to 256: 8.2 us either way) the matrices are read too often.
+    if (R <= 32 && K <= 2048 && R * K <= 32768 && R * N <= 32768 && T <= 512) {
+        a.places = (int32_t)T;
+        host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld by row", {T, R, K, N});
+        launch_lora_rows(a, s);
+        return launched();
+    }
     // Rows of a workgroup.  64, where there are many and an adapter has 16 of them or more on average: measured, 64
     // and 16 rows, us: 8192 rows of 8 adapters, R = 32, 7168 to 4096, 64 and 117; 1000 of 4, R = 64, 22.5 and 26.0,
     // but R = 16 15.2 and 14.0; 4096 of 64, R = 16, 38 and 42; 2048 of 128, R = 8, 32 and 25.  Else so few that the

@@ -43,6 +43,8 @@ __device__ __forceinline__ Place place_of(const LoraArgs& a, int p, bool report)
     return o;
 }
 
+__device__ __forceinline__ float scale_of(const LoraArgs& a, int id) { return a.scales && id >= 0 ? a.scales[id] : 1.0f; }
+
 // Workgroup barrier for LDS alone: global loads stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -180,6 +182,111 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_down_kernel(const Lor
     }
 }
 
+// Both products of a row by one workgroup, for small adapters of a rank up to 16 RT: its waves take the steps of K in
+// turn, their sums meet in LDS, and a thread forms a column of the result from A x in fp32.  The adapter's two matrices
+// come to one CU, so this pays while they are small: measured, this and two launches, us, 64 rows, R = 8, 2048 to 1024,
+// 4.7 and 8.0; 45 rows, R = 8, 1544 to 2112, 5.4 and 7.9; 32 rows, R = 16, 2048 to 2048, 5.6 and 7.0, R = 32, 1024 to
+// 1024, 6.3 and 7.5; but 8 rows, R = 8, 4096 to 4096, 7.5 and 6.8, 1 row, R = 16, 7168 to 4096, 13 and 6.7.
+template <int RT>
+__global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const LoraArgs a) {
+    constexpr int kRowThreads = kDownWaves * 64;
+    __shared__ v4f red[kDownWaves][RT][4];
+    __shared__ v4f low[4 * RT];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row16 = lane & 15, grp = lane >> 4;
+    const Place mine = place_of(a, blockIdx.x, tid == 0);
+    if (mine.row < 0) return;
+    const uint16_t* y = a.Y + mine.row * a.ldy;
+    uint16_t* out = a.out + mine.row * a.ldo;
+    if (mine.id < 0) {
+        if (a.Y != a.out)
+            for (int n = tid * 8; n < a.N; n += kRowThreads * 8) *reinterpret_cast<v4u*>(out + n) = *reinterpret_cast<const v4u*>(y + n);
+        return;
+    }
+    const uint16_t* xp = a.X + mine.row * a.ldx;
+    const uint16_t* ap[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) ap[r] = a.A + ((int64_t)mine.id * a.R + min(16 * r + row16, a.R - 1)) * a.K;
+    v4f acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+    constexpr int AHEAD = 4 / RT;                            // steps whose loads go out together
+    for (int s0 = wave; s0 < a.steps; s0 += AHEAD * kDownWaves) {
+        v4u w[AHEAD][2][RT], x[AHEAD][2];
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (s0 + p * kDownWaves) * 64 + grp * 16 + h * 8;
+                const bool in = k < a.K;                     // else zeros, in both operands
+                const int ko = in ? k : 0;
+                x[p][h] = *reinterpret_cast<const v4u*>(xp + ko);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) w[p][h][r] = *reinterpret_cast<const v4u*>(ap[r] + ko);
+                if (!in) {
+                    x[p][h] = (v4u){0, 0, 0, 0};
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) w[p][h][r] = (v4u){0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r] = mfma_bf16(w[p][h][r], x[p][h], acc[r]);
+    }
+    // every matrix-core column is the row; lane group grp has values 16 r + 4 grp .. + 3
+    if (row16 == 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) red[wave][r][grp] = acc[r];
+    }
+    __syncthreads();
+    if (tid < 4 * RT) {
+        v4f v = red[0][tid >> 2][tid & 3];
+#pragma unroll
+        for (int w = 1; w < kDownWaves; ++w) v += red[w][tid >> 2][tid & 3];
+        low[tid] = v;
+    }
+    const float scale = scale_of(a, mine.id);
+    const uint16_t* bp = a.B + (int64_t)mine.id * a.N * a.R;
+    const int units = a.R / 8;
+    constexpr int COLS = 4;                                  // columns of a thread at a time
+    bool ready = false;
+    for (int n0 = 0; n0 < a.N; n0 += COLS * kRowThreads) {
+        v4u b[COLS][2 * RT];
+        uint16_t yv[COLS];
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            const int n = min(n0 + c * kRowThreads + tid, a.N - 1);
+            yv[c] = y[n];
+#pragma unroll
+            for (int u = 0; u < 2 * RT; ++u) b[c][u] = *reinterpret_cast<const v4u*>(bp + (int64_t)n * a.R + 8 * min(u, units - 1));
+        }
+        if (!ready) __syncthreads();                         // A x is there
+        ready = true;
+        float d[COLS] = {};
+#pragma unroll
+        for (int u = 0; u < 2 * RT; ++u) {
+            if (u >= units) continue;
+            const v4f v[2] = {low[2 * u], low[2 * u + 1]};
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d[c] = __builtin_fmaf(__uint_as_float(b[c][u][e] << 16), v[e >> 1][2 * (e & 1)], d[c]);
+                    d[c] = __builtin_fmaf(__uint_as_float(b[c][u][e] & 0xFFFF0000u), v[e >> 1][2 * (e & 1) + 1], d[c]);
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            const int n = n0 + c * kRowThreads + tid;
+            if (n < a.N) out[n] = f32_to_bf16(__builtin_fmaf(d[c], scale, bf16_to_f32(yv[c])));
+        }
+    }
+}
+
 // A x for 64 places a workgroup, for batches whose places mostly share an adapter with their neighbours.  Slices of
 // 64 values of K of the 64 rows of X and the adapter's rows of A pass through a ring in LDS, 128-byte rows with
 // 16-byte chunk c of row r at c ^ swz(r) (as in the FP8 kernel); a wave has 16 places and all of the rank.
@@ -313,8 +420,6 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
         *reinterpret_cast<uint2*>(d + a.rank / 2) = make_uint2(lo[0], lo[1]);
     }
 }
-
-__device__ __forceinline__ float scale_of(const LoraArgs& a, int id) { return a.scales && id >= 0 ? a.scales[id] : 1.0f; }
 
 // The results of 16 rows and 64 columns, in LDS, onto Y's: lane l has rows l / 8 and 8 + l / 8, 8 columns.
 __device__ __forceinline__ void add_lines(const LoraArgs& a, const float* line, int lane, int n0, const int64_t (&row)[2],
@@ -664,6 +769,12 @@ void launch_up(const LoraArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+void launch_lora_rows(const LoraArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)a.places);
+    if (a.rank <= 16) lora_row_kernel<1><<<grid, kDownWaves * 64, 0, s>>>(a);
+    else lora_row_kernel<2><<<grid, kDownWaves * 64, 0, s>>>(a);
+}
 
 void launch_lora_down(const LoraArgs& a, hipStream_t s) {
     if (a.tile <= 16) {

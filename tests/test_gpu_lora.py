@@ -58,7 +58,10 @@ def check(c, out, scales=True, ids=None):
 
 SIZES = [(1, 1, 8, 8, 8), (1, 3, 16, 7168, 4096), (2, 5, 24, 72, 264), (15, 4, 32, 200, 40), (16, 2, 8, 1544, 512), (17, 300, 16, 320, 248),
          (45, 9, 8, 1544, 2112), (100, 3, 128, 64, 72), (256, 64, 16, 640, 1024), (513, 5, 40, 264, 520), (600, 4, 64, 128, 256),
-         (700, 3, 72, 1000, 136), (1500, 2, 128, 512, 264), (3000, 200, 16, 256, 512)]
+         (700, 3, 72, 1000, 136), (1500, 2, 128, 512, 264), (3000, 200, 16, 256, 512),
+         # both sides of where a row's two products are one launch: the rows, K, R K and R N
+         (512, 6, 8, 2048, 1024), (513, 6, 8, 2048, 1024), (9, 3, 16, 2056, 128), (33, 3, 32, 1032, 128), (70, 9, 16, 128, 2056),
+         (20, 2, 32, 1024, 1024), (130, 7, 40, 128, 136), (300, 11, 48, 264, 72), (5, 2, 16, 2312, 264)]
 
 
 @pytest.mark.parametrize("T,L,R,K,N", SIZES)
