@@ -55,7 +55,7 @@ struct Call {
         if (t->scalar_type() != at::kBFloat16 || t->dim() != 2 || t->size(0) != rows || t->size(1) != cols ||
             (cols > 1 && t->stride(1) != 1))
             return refuse();
-        *stride = rows > 1 ? t->stride(0) : cols;
+        *stride = rows > 1 && cols > 0 ? t->stride(0) : cols;
         return t->data_ptr();
     }
     int64_t integer(int i) {

@@ -249,16 +249,16 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     if (M > 0 && (!dH || !dpre || (!X && (!pre || dW)) || (!W && (!pre || dX)))) return FP8GEMM_ERR_NULL_PTR;
     for (const void* p : {dH, X, W, pre, static_cast<const void*>(dpre), static_cast<const void*>(dX), static_cast<const void*>(dW)})
         if (!aligned(p, 16)) return FP8GEMM_ERR_MISALIGNED;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (M == 0) {
-        if (!dW) return FP8GEMM_OK;
-        launch_fill_zero(dW, 4 * I * K, s);
-        return launched();
-    }
-    if (2 * M * 2 * I >= kMaxBytes || (M * I / 8 + 255) / 256 > kMaxUnits * 4 - 1) return FP8GEMM_ERR_UNSUPPORTED;
+    if ((M * I / 8 + 255) / 256 > kMaxUnits * 4 - 1) return FP8GEMM_ERR_UNSUPPORTED;
+    if (M == 0 && !dW) return FP8GEMM_OK;
     HostDevice d;
     st = host_device(&d);
     if (st != FP8GEMM_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M == 0) {
+        launch_fill_zero(dW, 4 * I * K, s);
+        return launched();
+    }
     // every choice and the workspace before the first launch
     Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0};
     ProductArgs ap{}, ax{}, aw{};
