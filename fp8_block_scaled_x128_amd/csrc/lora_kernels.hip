@@ -290,7 +290,8 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
 // A x for 64 places a workgroup, for batches whose places mostly share an adapter with their neighbours.  Slices of
 // 64 values of K of the 64 rows of X and the adapter's rows of A pass through a ring in LDS, 128-byte rows with
 // 16-byte chunk c of row r at c ^ swz(r) (as in the FP8 kernel); a wave has 16 places and all of the rank.
-// The last of a tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum
+// A tile of several adapters is shared by 1 << apart workgroups, that have them in turn: else it would take as many
+// times as long as the others.  The last of a tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum
 // is within 2^-17 of it (partials are written and read past the L2s of the XCDs, with agent-coherent accesses).
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2); }
 __device__ __forceinline__ void dma_far(uint32_t lds_base, const void* p) {
@@ -307,22 +308,23 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row16 = lane & 15, grp = lane >> 4;
     const int p0 = blockIdx.y * 64;
-    const int split = blockIdx.x;
+    const int apart = (1 << a.apart) - 1, turn = (int)blockIdx.x & apart, split = (int)blockIdx.x >> a.apart;
     const int s0 = split * a.per_split, nks = min(a.per_split, a.steps - s0);
     const uint32_t base = lds_addr(smem);
     const int tail = a.K - (a.steps - 1) * 64, tail_at = tail < 64 ? a.steps - 1 - s0 : -1;
     const int frag[2] = {((2 * grp) ^ swz(row16)) << 4, ((2 * grp + 1) ^ swz(row16)) << 4};
 
-    const Place mine = place_of(a, p0 + lane, split == 0 && wave == 0);
-    const uint64_t all = __builtin_amdgcn_ballot_w64(mine.id >= 0);
+    const Place mine = place_of(a, p0 + lane, blockIdx.x == 0 && wave == 0);
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
         uniform_ptr(a.low), 0, (int)((int64_t)a.splits * a.places * a.rank * 4), kBufferFlags);
-    uint64_t left = all;
-    while (left) {
+    uint64_t left = __builtin_amdgcn_ballot_w64(mine.id >= 0), own = 0;
+    for (int n = 0; left; ++n) {
         const int first = __builtin_ctzll(left);
         const int adapter = __builtin_amdgcn_readlane(mine.id, first);
         const uint64_t has = __builtin_amdgcn_ballot_w64(mine.id == adapter);
         left &= ~has;
+        if ((n & apart) != turn) continue;
+        own |= has;
         // a lane's rows of the loads: place 8 (2 wave + q) + lane / 8 (the first of the adapter, where it is another's)
         const int c8 = lane & 7;
         const uint16_t* xp[X_LOADS];
@@ -386,35 +388,48 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
         wait_vmcnt<0>();
         __syncthreads();
     }
+    if (!own) return;                                        // (in all splits alike)
     if (a.splits > 1) {
+        int32_t* counter = a.counters + ((int)blockIdx.y << a.apart) + turn;
         if (tid == 0) {
-            const int old = __hip_atomic_fetch_add(a.counters + blockIdx.y, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const int old = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             s_last = old == a.splits - 1;
-            if (s_last) __hip_atomic_store(a.counters + blockIdx.y, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (s_last) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         __syncthreads();
         if (!s_last) return;
     }
-    // a thread has a float4 of a place, in all RT * 64 / 64
-    const int per = a.rank / 4;
+    // a thread has RT float4 of places; the reads of all of them, of some splits, are on their way together
+    constexpr int SPLITS = RT <= 2 ? 8 : 16 / RT;
+    const int per = a.rank / 4, step = a.places * a.rank * 4;
+    int at[RT];
+    v4f v[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int x = i * kThreads + tid, p = x / per, c = x - p * per;
-        if (p >= 64 || !((all >> p) & 1)) continue;
-        const int at = ((p0 + p) * a.rank + 4 * c) * 4, step = a.places * a.rank * 4;
-        v4f v = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < a.splits; s += 4) {
-            v4f t[4];
+        at[i] = p < 64 && ((own >> p) & 1) ? ((p0 + p) * a.rank + 4 * c) * 4 : -1;
+        v[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    }
+    for (int s = 0; s < a.splits; s += SPLITS) {
+        v4u t[SPLITS][RT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                t[e] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(parts, at + min(s + e, a.splits - 1) * step, 0, kSc1));
+        for (int e = 0; e < SPLITS; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (s + e < a.splits) v += t[e];
-        }
-        if (4 * c >= a.R) v = (v4f){0.f, 0.f, 0.f, 0.f};     // (a rank that is padded)
+            for (int i = 0; i < RT; ++i)
+                t[e][i] = __builtin_amdgcn_raw_buffer_load_b128(parts, max(at[i], 0) + min(s + e, a.splits - 1) * step, 0, kSc1);
+#pragma unroll
+        for (int e = 0; e < SPLITS; ++e)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                if (s + e < a.splits) v[i] += __builtin_bit_cast(v4f, t[e][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        if (at[i] < 0) continue;
+        const int x = i * kThreads + tid, p = x / per, c = x - p * per;
+        if (4 * c >= a.R) v[i] = (v4f){0.f, 0.f, 0.f, 0.f};  // (a rank that is padded)
         uint32_t hi[2], lo[2];
-        halves_of(v, hi, lo);
+        halves_of(v[i], hi, lo);
         uint32_t* d = reinterpret_cast<uint32_t*>(a.halves + ((int64_t)(p0 + p) * 2) * a.rank + 4 * c);
         *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(d + a.rank / 2) = make_uint2(lo[0], lo[1]);
@@ -757,7 +772,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_up64_kernel(const LoraArgs a
 
 template <int RT>
 void launch_down64(const LoraArgs& a, hipStream_t s) {
-    lora_down64_kernel<RT, RT <= 4 ? 4 : 3><<<dim3((uint32_t)a.splits, (uint32_t)((a.places + 63) / 64)), kThreads, 0, s>>>(a);
+    lora_down64_kernel<RT, RT <= 4 ? 4 : 3><<<dim3((uint32_t)a.splits << a.apart, (uint32_t)((a.places + 63) / 64)), kThreads, 0, s>>>(a);
 }
 
 template <int RS>
