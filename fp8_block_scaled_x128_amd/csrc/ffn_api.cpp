@@ -388,14 +388,16 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     if (T >= 16 * (int64_t)L && T > (R > 32 ? 512 : 1024)) a.tile = 64;
     else for (a.tile = 1; a.tile < 16 && a.tile * 32 < T;) a.tile *= 2;
     const int64_t row_tiles = (T + a.tile - 1) / a.tile;
-    // Tiles of 64 rows with several adapters have them side by side where the CUs have room: measured, one after the other
-    // and side by side, us: 573 rows of 4 adapters, R = 40, 2016 to 72, 15.0 and 12.0; 1356 of 2, R = 104, 856 to 112, 18.2
-    // and 15.2; 2000 of 3, R = 128, 4096 to 7168, 40 and 38; but 5963 of 4, R = 128, 3640 to 80, 36 and 46, since a
-    // workgroup without an adapter holds a place until it knows.
-    if (a.tile == 64 && L > 1 && 8 * row_tiles <= d.cus) a.apart = 1;
-    // splits of K that give the CUs two workgroups each, of 8 steps at least: 4, 8 and 16 steps, us: 1 row 7.5, 6.9
-    // and 7.4, 256 rows of 64 adapters 19.8, 16.3 and 20.1
-    const int64_t want = std::max<int64_t>(1, 2 * d.cus / (row_tiles << a.apart));
+    // Splits of K, of 8 steps at least.  Few rows: such that the CUs have two workgroups each; 4, 8 and 16 steps, us: 1
+    // row 7.5, 6.9 and 7.4, 256 rows of 64 adapters 19.8, 16.3 and 20.1.  Tiles of 64 rows: a power of two, so that
+    // each CU has a workgroup, beside those for the tiles' second adapters: 1, 2, 4 and 8 splits, us: 8192 rows of 8
+    // adapters, R = 32, 7168 to 4096, 61, 53, 57 and 57; 5963 of 4, R = 128, 3640 to 80, 39, 38, 31 and 39; 2000 of 3,
+    // R = 128, 4096 to 7168, 55, 42, 36.3 and 36.6.  Without the second workgroups these took 57, 35 and 39 at best.
+    int64_t want = std::max<int64_t>(1, 2 * d.cus / row_tiles);
+    if (a.tile == 64) {
+        a.apart = L > 1;
+        for (want = 1; want * row_tiles < d.cus;) want *= 2;
+    }
     const int64_t splits = std::min<int64_t>(want, (a.steps + 7) / 8);
     a.per_split = (int32_t)((a.steps + splits - 1) / splits);
     a.splits = (a.steps + a.per_split - 1) / a.per_split;
@@ -407,9 +409,9 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     // dimension and the counters
     const int64_t row_bytes = (int64_t)a.rank * 4 * (a.splits + 1);
     const int64_t room = (int64_t)d.cus * 512 * 1024 / row_bytes / 64 * 64;
-    const int64_t pass = std::min(T, std::min<int64_t>(room, (int64_t)(4096 >> a.apart) * a.tile));
+    const int64_t pass = std::min(T, std::min<int64_t>(room, (int64_t)(a.tile == 64 ? 2048 : 4096) * a.tile));
     std::unique_lock<std::mutex> hold;
-    st = host_stream_workspace(s, (size_t)(pass * row_bytes), a.tile == 64 ? (size_t)((pass + 63) / 64) << a.apart : 0, &a.low, &a.counters, &hold);
+    st = host_stream_workspace(s, (size_t)(pass * row_bytes), a.tile == 64 ? (size_t)((pass + 63) / 64) * 2 : 0, &a.low, &a.counters, &hold);
     if (st != FP8GEMM_OK) return st;
     a.halves = reinterpret_cast<uint16_t*>(a.low + pass * a.splits * a.rank);
     host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld rows=%lld split=%lld", {T, R, K, N, a.tile, a.splits});

@@ -109,7 +109,7 @@ struct LoraArgs {
     int32_t rank;               // R rounded up to 16
     int32_t steps;              // ceil(K / 64)
     int32_t splits, per_split;  // steps of a split
-    int32_t apart;              // tiles of 64 places: 1 << apart workgroups have their adapters in turn
+    int32_t apart;              // tiles of 64 places: 0, or 1: two workgroups have their adapters in turn
     int32_t chunks;             // runs of kLoraSpan columns that a workgroup takes
 };
 

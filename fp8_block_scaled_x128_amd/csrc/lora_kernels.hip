@@ -290,8 +290,8 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
 // A x for 64 places a workgroup, for batches whose places mostly share an adapter with their neighbours.  Slices of
 // 64 values of K of the 64 rows of X and the adapter's rows of A pass through a ring in LDS, 128-byte rows with
 // 16-byte chunk c of row r at c ^ swz(r) (as in the FP8 kernel); a wave has 16 places and all of the rank.
-// A tile of several adapters is shared by 1 << apart workgroups, that have them in turn: else it would take as many
-// times as long as the others.  The last of a tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum
+// A tile of several adapters is shared by two workgroups (apart = 1), that have them in turn: else it would take as many
+// times as long as the others.  The second ones come first in the grid, where most of them end at once.  The last of a tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum
 // is within 2^-17 of it (partials are written and read past the L2s of the XCDs, with agent-coherent accesses).
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2); }
 __device__ __forceinline__ void dma_far(uint32_t lds_base, const void* p) {
@@ -307,14 +307,14 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row16 = lane & 15, grp = lane >> 4;
-    const int p0 = blockIdx.y * 64;
-    const int apart = (1 << a.apart) - 1, turn = (int)blockIdx.x & apart, split = (int)blockIdx.x >> a.apart;
+    const int split = blockIdx.x, tiles = (a.places + 63) / 64;
+    const int turn = a.apart && (int)blockIdx.y < tiles, tile = (int)blockIdx.y - (a.apart && !turn ? tiles : 0), p0 = tile * 64;
     const int s0 = split * a.per_split, nks = min(a.per_split, a.steps - s0);
     const uint32_t base = lds_addr(smem);
     const int tail = a.K - (a.steps - 1) * 64, tail_at = tail < 64 ? a.steps - 1 - s0 : -1;
     const int frag[2] = {((2 * grp) ^ swz(row16)) << 4, ((2 * grp + 1) ^ swz(row16)) << 4};
 
-    const Place mine = place_of(a, p0 + lane, blockIdx.x == 0 && wave == 0);
+    const Place mine = place_of(a, p0 + lane, split == 0 && !turn && wave == 0);
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
         uniform_ptr(a.low), 0, (int)((int64_t)a.splits * a.places * a.rank * 4), kBufferFlags);
     uint64_t left = __builtin_amdgcn_ballot_w64(mine.id >= 0), own = 0;
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
         const int adapter = __builtin_amdgcn_readlane(mine.id, first);
         const uint64_t has = __builtin_amdgcn_ballot_w64(mine.id == adapter);
         left &= ~has;
-        if ((n & apart) != turn) continue;
+        if ((n & a.apart) != turn) continue;
         own |= has;
         // a lane's rows of the loads: place 8 (2 wave + q) + lane / 8 (the first of the adapter, where it is another's)
         const int c8 = lane & 7;
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_down64_kernel(const LoraArgs
     }
     if (!own) return;                                        // (in all splits alike)
     if (a.splits > 1) {
-        int32_t* counter = a.counters + ((int)blockIdx.y << a.apart) + turn;
+        int32_t* counter = a.counters + 2 * tile + turn;
         if (tid == 0) {
             const int old = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             s_last = old == a.splits - 1;
@@ -772,7 +772,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_up64_kernel(const LoraArgs a
 
 template <int RT>
 void launch_down64(const LoraArgs& a, hipStream_t s) {
-    lora_down64_kernel<RT, RT <= 4 ? 4 : 3><<<dim3((uint32_t)a.splits << a.apart, (uint32_t)((a.places + 63) / 64)), kThreads, 0, s>>>(a);
+    lora_down64_kernel<RT, RT <= 4 ? 4 : 3><<<dim3((uint32_t)a.splits, (uint32_t)((a.places + 63) / 64) << a.apart), kThreads, 0, s>>>(a);
 }
 
 template <int RS>
