@@ -383,10 +383,13 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     // Rows of a workgroup.  64, where there are many and an adapter has 16 of them or more on average: measured, 64
     // and 16 rows, us: 8192 rows of 8 adapters, R = 32, 7168 to 4096, 64 and 117; 1000 of 4, R = 64, 22.5 and 26.0,
     // but R = 16 15.2 and 14.0; 4096 of 64, R = 16, 38 and 42; 2048 of 128, R = 8, 32 and 25.  Else so few that the
-    // workgroups go through few adapters each, and 32 of them have rows: 1, 4 and 16 rows, us, 64 adapters, R = 16,
-    // 7168 to 4096: 16 rows 7.3, 10.8 and 19.3; 128 rows 15.6, 14.9 and 20.7; 512 rows 37, 26 and 16.5.
+    // workgroups go through few adapters each and many of them have rows, more the more an adapter's matrices hold: 1, 2,
+    // 4, 8 and 16 rows, us, rows in any order and by adapter: 64 adapters, R = 16, 7168 to 4096: 48 rows 10.0, 9.9, 10.4,
+    // 13.2, 20.4 and 10.0, 9.7, 10.2, 13.2, 19.2; 270 rows 31, 25, 21, 22, 23 and 31, 25, 18, 14.7, 14.5; 512 rows 38,
+    // 33, 34, 32, 32 and 39, 31, 23, 18, 15.5.  3 adapters, R = 104, 2496 to 952: 128 rows 28, 23, 21, 17, 16 and 29, 18,
+    // 16, 13.7, 14.0.
     if (T >= 16 * (int64_t)L && T > (R > 32 ? 512 : 1024)) a.tile = 64;
-    else for (a.tile = 1; a.tile < 16 && a.tile * 32 < T;) a.tile *= 2;
+    else for (a.tile = 1; a.tile < 16 && a.tile * 40 < T * ((R + 31) / 32);) a.tile *= 2;
     const int64_t row_tiles = (T + a.tile - 1) / a.tile;
     // Splits of K, of 8 steps at least.  Few rows: such that the CUs have two workgroups each; 4, 8 and 16 steps, us: 1
     // row 7.5, 6.9 and 7.4, 256 rows of 64 adapters 19.8, 16.3 and 20.1.  Tiles of 64 rows: a power of two, so that
