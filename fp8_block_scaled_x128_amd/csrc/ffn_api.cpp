@@ -46,14 +46,23 @@ bool forced(Choice* c) {
     return false;
 }
 
-double slower(const TileShape& t, Product kind) { return kind == kTimesW ? t.turned : kind == kTurned ? t.both_turned : 1.0; }
+// `off`: rows off the lines (of one operand of kTimesW)
+double slower(const TileShape& t, Product kind, bool off) {
+    const double r = kind == kTimesW ? t.turned : kind == kTurned ? t.both_turned : 1.0;
+    return !off ? r : kind == kTimesW ? r * 0.5 * (1.0 + t.off) : r * t.off;
+}
+
+// Whether the loads of rows off the lines make a difference, by all that the tiles load: H, us, tiles of 128 x 128 with loads
+// by slices and by lines: 51 MB 10.7 and 11.9, 102 MB 12.7 and 12.7, 122 MB 34.5 and 24.4; of 64 x 64: 79 MB 11.9 and 14.2,
+// 100 MB 10.5 and 10.0, 159 MB 18.7 and 16.7.  dX, with one such operand, gains or stays (9 to 216 tiles).
+bool loads_count(int64_t tiles, const TileShape& t, int64_t slices) { return tiles * slices * (t.bm + t.bn) * 128 >= 96000000; }
 
 // Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K:
 // the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes, where
 // those take longer than reading both operands and writing the result.  Over 26 sizes of each product (17 to 4096 rows, I 64 to 2048, K
 // 128 to 7168) the choice is within 7% of the best of all tiles with 1 to 16 splits, but for three that are 13 to 17%
 // off (exchanges of many partials: 256 rows, 2048, 7168; dX of 3565 and 3808 rows, K about 400).
-Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus) {
+Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus, bool off) {
     const bool gated = kind == kGated || kind == kGatedBack;
     Choice best{0, 1, 1e30};
     if (forced(&best)) return best;
@@ -63,12 +72,13 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus)
         const int64_t width = gated ? t.bn / 2 : t.bn;
         const int64_t tiles = ((rows + t.bm - 1) / t.bm) * ((cols + width - 1) / width);
         const int64_t slots = (int64_t)cus * t.per_cu;
+        const double slow = slower(t, kind, off && loads_count(tiles, t, slices));
         for (int64_t s = 1; s <= 16 && (s == 1 || (s * 2 <= slices && tiles * s <= slots)); ++s) {
             const int64_t per = (slices + s - 1) / s;
             if (s > 1 && (slices + per - 1) / per != s) continue;
             const int64_t units = tiles * s, last = units % slots;
             const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared);
-            const double cost = std::max(((double)per + t.ends) * rounds * slower(t, kind), bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
+            const double cost = std::max(((double)per + t.ends) * rounds * slow, bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
             if (cost < best.us) best = {i, (int)s, cost};
         }
     }
@@ -84,7 +94,7 @@ bool few_rows(int64_t M, int64_t I, int64_t K, int cus) {
     if (M > kGatedRowsMax || (I + 8) * K * 2 >= (int64_t(1) << 31)) return false;
     const double rounds = (double)((K + 511) / 512);                             // steps of a wave
     const double bytes = 4e-6 * (double)I * (double)K / 5.2 + 2e-6 * (double)M * (double)K * (double)((I + 7) / 8) / 12.0;
-    return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 3.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, cus).us;
+    return 2.5 + std::max(rounds * (0.55 + 0.02 * (double)M), bytes) < 3.5 + choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, cus, false).us;
 }
 
 // Time, in slices, until n units of L slices and then n2 of L2 are done on `slots` places that take the next unit as
@@ -112,6 +122,7 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
     const int64_t sx = (x.K + kSliceK - 1) / kSliceK, sw = (w.K + kSliceK - 1) / kSliceK;
     const double bytes = (128e-6 * ((double)sx * (double)(x.rows + x.cols) + (double)sw * (double)(w.rows + w.cols)) +
                           2e-6 * ((double)x.rows * (double)x.cols + (double)w.rows * (double)w.cols)) / 5.2;
+    const bool off = off_the_lines(x, kTimesW);
     double least = cx->us + cw->us + 3.5;
     bool pair = false;
     for (int i = 0; i < kTileShapes; ++i) {
@@ -120,7 +131,7 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
         const int64_t tx = tiles(x), tw = tiles(w), slots = (int64_t)cus * t.per_cu;
         for (int64_t px = 1; px <= 8 && (px == 1 || (px * 2 <= sx && px * tx <= slots)); px *= 2)
             for (int64_t pw = 1; pw <= 8 && (pw == 1 || (pw * 2 <= sw && pw * tw <= slots)); pw *= 2) {
-                const double lx = ((double)((sx + px - 1) / px) + t.ends) * t.turned;
+                const double lx = ((double)((sx + px - 1) / px) + t.ends) * slower(t, kTimesW, off);
                 const double lw = ((double)((sw + pw - 1) / pw) + t.ends) * t.both_turned;
                 const int64_t nx = tx * px, nw = tw * pw;
                 const double rounds = lx >= lw ? rounds_of(nx, lx, nw, lw, slots) : rounds_of(nw, lw, nx, lx, slots);
@@ -138,7 +149,8 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
 }
 
 // Sizes and order of the tiles of a product.
-int arrange(ProductArgs* a, Choice* c, bool gated) {
+int arrange(ProductArgs* a, Choice* c, Product kind) {
+    const bool gated = kind == kGated || kind == kGatedBack;
     a->slices = (a->K + kSliceK - 1) / kSliceK;
     const TileShape& t = kTiles[c->shape];
     const int width = gated ? t.bn / 2 : t.bn;
@@ -146,6 +158,7 @@ int arrange(ProductArgs* a, Choice* c, bool gated) {
     a->per_split = (a->slices + c->splits - 1) / c->splits;
     a->splits = c->splits = (a->slices + a->per_split - 1) / a->per_split;       // none without a slice
     if (tm > kMaxUnits / tn || tm * tn > kMaxUnits / a->splits) return FP8GEMM_ERR_UNSUPPORTED;
+    a->lag = t.bm <= 128 && t.bn <= 128 && off_the_lines(*a, kind) && (kind == kTimesW || loads_count(tm * tn, t, a->slices));
     a->tiles_m = (int32_t)tm;
     a->tiles_n = (int32_t)tn;
     a->group_m = (int32_t)std::min<int64_t>(tm, 8);
@@ -230,8 +243,8 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     a.cols = (int32_t)I;
     a.K = a.ldp = a.ldq = (int32_t)K;
     a.gelu = act == FP8GEMM_ACT_GELU_TANH;
-    c = choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, d.cus);
-    st = arrange(&a, &c, true);
+    c = choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, d.cus, off_the_lines(a, kGated));
+    st = arrange(&a, &c, kGated);
     if (st != FP8GEMM_OK) return st;
     std::unique_lock<std::mutex> hold;
     st = share_workspace({{&a, c}}, s, &hold);
@@ -272,8 +285,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ap.cols = (int32_t)I;
         ap.K = ap.ldp = ap.ldq = (int32_t)K;
         ap.gelu = act == FP8GEMM_ACT_GELU_TANH;
-        cp = choose(M, I, slices(K), kGatedBack, d.cus);
-        st = arrange(&ap, &cp, true);
+        cp = choose(M, I, slices(K), kGatedBack, d.cus, off_the_lines(ap, kGatedBack));
+        st = arrange(&ap, &cp, kGatedBack);
         if (st != FP8GEMM_OK) return st;
     }
     if (dX) {
@@ -283,7 +296,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ax.rows = (int32_t)M;
         ax.cols = ax.ldq = (int32_t)K;
         ax.K = ax.ldp = (int32_t)(2 * I);
-        cx = choose(M, K, slices(2 * I), kTimesW, d.cus);
+        cx = choose(M, K, slices(2 * I), kTimesW, d.cus, off_the_lines(ax, kTimesW));
     }
     if (dW) {
         aw.P = static_cast<const uint16_t*>(dpre);
@@ -292,11 +305,11 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         aw.rows = aw.ldp = (int32_t)(2 * I);
         aw.cols = aw.ldq = (int32_t)K;
         aw.K = (int32_t)M;
-        cw = choose(2 * I, K, slices(M), kTurned, d.cus);
+        cw = choose(2 * I, K, slices(M), kTurned, d.cus, false);
     }
     const bool pair = dX && dW && choose_pair(ax, aw, d.cus, &cx, &cw);
-    if (dX && (st = arrange(&ax, &cx, false)) != FP8GEMM_OK) return st;
-    if (dW && (st = arrange(&aw, &cw, false)) != FP8GEMM_OK) return st;
+    if (dX && (st = arrange(&ax, &cx, kTimesW)) != FP8GEMM_OK) return st;
+    if (dW && (st = arrange(&aw, &cw, kTurned)) != FP8GEMM_OK) return st;
     if (pair && (int64_t)ax.tiles_m * ax.tiles_n * ax.splits + (int64_t)aw.tiles_m * aw.tiles_n * aw.splits > kMaxUnits)
         return FP8GEMM_ERR_UNSUPPORTED;
     // (dX and dW, which follow, take the first product's part again)

@@ -36,20 +36,27 @@ struct ProductArgs {
     int32_t splits, per_split;  // slices of a split
     int32_t group_m;            // M tiles of a band of the tile order
     int32_t gelu;               // activation: silu, or gelu by its tanh form
+    int32_t lag;                // tiles of 128 x 128 and 64 x 64: loads by whole lines of rows off the lines
     FastDiv div_splits, div_band_units, div_band_h, div_band_h_last;
 };
 
+// Whether rows of a straight operand start beside 128-byte lines, so that a slice of a row lies in two of them.
+inline bool off_the_lines(const ProductArgs& a, Product kind) {
+    const auto off = [](const void* p, int32_t ld) { return ((reinterpret_cast<uintptr_t>(p) | 2 * (uintptr_t)ld) & 127) != 0; };
+    return (kind != kTurned && off(a.P, a.ldp)) || ((kind == kGated || kind == kGatedBack) && off(a.Q, a.ldq));
+}
+
 // Tiles of a workgroup: bm rows of P, bn rows of Q.  Times in us, measured: a slice where the workgroup has a
 // CU to itself, and where `per_cu` share it (for all of them); how much longer it takes with Q turned, and with both
-// operands; its start and end, in slices; a K split's exchange (constant, and by split).
+// operands, and with rows off the lines; its start and end, in slices; a K split's exchange (constant, and by split).
 struct TileShape {
     int bm, bn, per_cu;
-    double alone, shared, turned, both_turned, ends, exchange, exchange_split;
+    double alone, shared, turned, both_turned, off, ends, exchange, exchange_split;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 1.00, 1.05, 5.3, 20.0, 2.7},
-                                {128, 256, 1, 0.83, 0.83, 1.05, 1.15, 6.0, 8.0, 1.5},
-                                {128, 128, 1, 0.47, 0.47, 1.15, 1.30, 8.0, 6.0, 0.7},
-                                {64, 64, 2, 0.25, 0.46, 1.05, 1.10, 5.3, 1.0, 0.3}};
+constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 1.00, 1.05, 1.15, 5.3, 20.0, 2.7},
+                                {128, 256, 1, 0.83, 0.83, 1.05, 1.15, 1.30, 6.0, 8.0, 1.5},
+                                {128, 128, 1, 0.47, 0.47, 1.15, 1.30, 1.10, 8.0, 6.0, 0.7},
+                                {64, 64, 2, 0.25, 0.46, 1.05, 1.10, 1.20, 5.3, 1.0, 0.3}};
 constexpr int kTileShapes = 4;
 constexpr int kSliceK = 64;
 

@@ -78,8 +78,10 @@ struct Operand {
     }
 };
 
-template <int BM_, int BN_, int WMW_, int WNW_, int STAGES_, int KIND_>
+// LAG: a straight operand's rows do not start at 128-byte lines (product() below).
+template <int BM_, int BN_, int WMW_, int WNW_, int STAGES_, int KIND_, bool LAG_>
 struct Tile {
+    static constexpr bool LAG = LAG_;
     static constexpr int BM = BM_, BN = BN_, WMW = WMW_, WNW = WNW_, STAGES = STAGES_, KIND = KIND_;
     static constexpr bool PT = KIND == kTurned, QT = KIND == kTimesW || KIND == kTurned;
     static constexpr bool GATED = KIND == kGated || KIND == kGatedBack;
@@ -92,6 +94,7 @@ struct Tile {
     static constexpr int STAGE_BYTES = OpQ::BYTES + OpP::BYTES;
     static constexpr int NDMA = OpQ::LOADS + OpP::LOADS;
     static_assert(NDMA * (STAGES - 1) < 64, "vmcnt range");
+    static_assert(!LAG || (STAGES >= 4 && !(PT && QT)), "a place of the ring to spare, and rows to use it");
     static constexpr int OUT_COLS = GATED ? BN / 2 : BN;     // columns of the output that a tile covers
     // epilogue: a wave's rows in an LDS region of its own, an odd number of 16-byte units apart
     static constexpr int W_COLS = OUT_COLS / WNW;
@@ -132,65 +135,89 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     const int n0 = (int)tq * T::OUT_COLS;                    // first output column
     const int s0 = split * a.per_split, nks = min(a.per_split, a.slices - s0);
 
-    // ---- what each lane loads: byte offsets from a slice's bases --------------------------------------------
-    // rows and columns past the end repeat the last (their results are not stored); `kvalid` values of k
-    auto p_off = [&](int q, int kvalid) -> uint32_t {
-        const int r = OpP::row(wave, q, lane), c = OpP::chunk(r, lane);
-        if constexpr (T::PT) return (uint32_t)min(r, kvalid - 1) * (uint32_t)(2 * a.ldp) + (uint32_t)(2 * min(m0 + 8 * c, a.rows - 8));
-        else return (uint32_t)min(r, a.rows - 1 - m0) * (uint32_t)(2 * a.ldp) + (uint32_t)(2 * min(8 * c, kvalid - 8));
+    // LAG: a slice's 128 bytes of a row lie in two lines.  Those chunks of it that are in the second are loaded a slice
+    // later, with the rest of their line, so that no line is loaded twice: place i of the ring holds line i of each
+    // row, and slice i is read from places i and i + 1, in which every chunk stands where it would in a place of its own.
+    // Measured, us, without and with, beside whole lines: H of 1001 rows, I = 1416, K = 3400 38, 28.9 and 26.2 (128 x 128),
+    // 49, 38.8 and 32 (64 x 64).  A place less for loads on their way costs where few are: 128 rows, K = 3400, 64 x 64 tiles
+    // 11.9 and 14.2.
+    constexpr int lag = T::LAG;
+    const int lines = nks + lag;
+    const int tail = a.K - (a.slices - 1) * 64;              // values of the last slice
+    const int tail_at = tail < 64 ? a.slices - 1 - s0 : -1;  // this unit's slice that is not whole
+    // whether chunk c of row r comes with the next slice (tiles, and a tile's 16 rows, start at multiples of 8)
+    auto late_p = [&](int r, int c) { return T::LAG && !T::PT && c + (((int)(reinterpret_cast<uintptr_t>(a.P) >> 4) + r * (a.ldp >> 3)) & 7) >= 8; };
+    auto late_q = [&](int r, int c) { return T::LAG && !T::QT && c + (((int)(reinterpret_cast<uintptr_t>(a.Q) >> 4) + r * (a.ldq >> 3)) & 7) >= 8; };
+
+    // ---- what each lane loads: byte offsets from a line's bases ----------------------------------------------
+    // rows and columns past the end repeat the last (their results are not stored), and so do slices and values
+    auto values = [&](int slice) { return slice == tail_at ? tail : 64; };
+    auto k_off = [&](int line, bool late, int c) {
+        if constexpr (!T::LAG) return (uint32_t)(2 * min(8 * c, values(line) - 8));
+        const int slice = min(max(line - (int)late, 0), nks - 1);
+        return (uint32_t)(128 * (slice - line + lag) + 2 * min(8 * c, values(slice) - 8));
     };
-    auto q_off = [&](int q, int kvalid) -> uint32_t {
+    auto p_off = [&](int q, int line) -> uint32_t {
+        const int r = OpP::row(wave, q, lane), c = OpP::chunk(r, lane);
+        if constexpr (T::PT) return (uint32_t)min(r, values(line) - 1) * (uint32_t)(2 * a.ldp) + (uint32_t)(2 * min(m0 + 8 * c, a.rows - 8));
+        else return (uint32_t)min(r, a.rows - 1 - m0) * (uint32_t)(2 * a.ldp) + k_off(line, late_p(r, c), c);
+    };
+    auto q_off = [&](int q, int line) -> uint32_t {
         const int r = OpQ::row(wave, q, lane), c = OpQ::chunk(r, lane);
-        if constexpr (T::QT) return (uint32_t)min(r, kvalid - 1) * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(n0 + 8 * c, a.cols - 8));
-        // gate and up rows in turn, 16 each, so that a lane ends with a pair of them (up: qs below)
-        const int n = min(((r >> 5) << 4) + (r & 15), a.cols - 1 - n0);
-        return (uint32_t)n * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(8 * c, kvalid - 8));
+        if constexpr (T::QT) {
+            return (uint32_t)min(r, values(T::LAG ? min(line, nks - 1) : line) - 1) * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(n0 + 8 * c, a.cols - 8));
+        } else {
+            // gate and up rows in turn, 16 each, so that a lane ends with a pair of them (up: qs below)
+            const int n = min(((r >> 5) << 4) + (r & 15), a.cols - 1 - n0);
+            return (uint32_t)n * (uint32_t)(2 * a.ldq) + k_off(line, late_q(r, c), c);
+        }
     };
     uint32_t poff[OpP::LOADS], qoff[OpQ::LOADS];
 #pragma unroll
-    for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, 64);
+    for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, -1);
 #pragma unroll
-    for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, 64);
-    const uint16_t* pbase = a.P + (T::PT ? (int64_t)s0 * 64 * a.ldp : (int64_t)m0 * a.ldp + (int64_t)s0 * 64);
-    const uint16_t* qbase = a.Q + (T::QT ? (int64_t)s0 * 64 * a.ldq : (int64_t)n0 * a.ldq + (int64_t)s0 * 64);
+    for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, -1);
+    const uint16_t* pbase = a.P + (T::PT ? (int64_t)s0 * 64 * a.ldp : (int64_t)m0 * a.ldp + ((int64_t)s0 - lag) * 64);
+    const uint16_t* qbase = a.Q + (T::QT ? (int64_t)s0 * 64 * a.ldq : (int64_t)n0 * a.ldq + ((int64_t)s0 - lag) * 64);
     const int64_t pstep = T::PT ? (int64_t)64 * a.ldp : 64, qstep = T::QT ? (int64_t)64 * a.ldq : 64;
     const int64_t up = (int64_t)a.cols * a.ldq;              // gated: from a gate row to its up row
-    const int tail = a.K - (a.slices - 1) * 64;              // values of the last slice
-    const int tail_at = tail < 64 ? a.slices - 1 - s0 : -1;  // this unit's slice that is not whole
 
-    // load x of slice i (of a wave's NDMA: Q's, then P's)
+    // load x of line i (of a wave's NDMA: Q's, then P's)
     auto issue = [&](int i, int x) {
         const uint32_t st = smem_base + (uint32_t)((i % STAGES) * T::STAGE_BYTES);
         if (x < OpQ::LOADS) {
             const int l = wave * OpQ::LOADS + x;
-            dma_x4(st + l * 1024, uniform_ptr(qbase + i * qstep + (T::GATED && (l >> 1 & 1) ? up : 0)), qoff[x]);
+            dma_x4(st + l * 1024, uniform_ptr(qbase + (T::LAG && T::QT ? min(i, nks - 1) : i) * qstep + (T::GATED && (l >> 1 & 1) ? up : 0)), qoff[x]);
         } else {
             const int l = wave * OpP::LOADS + x - OpQ::LOADS;
             dma_x4(st + T::P_OFF + l * 1024, uniform_ptr(pbase + i * pstep), poff[x - OpQ::LOADS]);
         }
     };
-    // before the loads of slice i, in order: the last one may not be whole
+    // before the loads of line i, in order: the first and the last are not like the others
+    const int special = tail_at >= 0 ? min(tail_at, nks) : nks;
     auto aim = [&](int i) {
-        if (i != tail_at) return;
+        if (T::LAG ? i > 1 && i < special : i != tail_at) return;
 #pragma unroll
-        for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, tail);
+        for (int q = 0; q < OpP::LOADS; ++q) poff[q] = p_off(q, i);
 #pragma unroll
-        for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, tail);
+        for (int q = 0; q < OpQ::LOADS; ++q) qoff[q] = q_off(q, i);
     };
     // zeros in both operands for the values of k that the last slice does not have
     auto clear_tail = [&](int i) {
-        uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
-        auto clear = [&](uint8_t* part, int rows, bool turned, int row_bytes) {
+        const int here = (i % STAGES) * T::STAGE_BYTES, next = ((i + lag) % STAGES) * T::STAGE_BYTES;
+        auto clear = [&](int part, int rows, bool turned, int row_bytes, auto late) {
             if (turned) {
                 for (int o = tail * row_bytes + tid * 16; o < 64 * row_bytes; o += T::NT * 16)
-                    *reinterpret_cast<v4u*>(part + o) = (v4u){0, 0, 0, 0};
+                    *reinterpret_cast<v4u*>(smem + here + part + o) = (v4u){0, 0, 0, 0};
             } else {
-                for (int x = tid; x < rows * 8; x += T::NT)
-                    if ((x & 7) * 8 >= tail) *reinterpret_cast<v4u*>(part + (x >> 3) * 128 + (((x & 7) ^ swz(x >> 3)) << 4)) = (v4u){0, 0, 0, 0};
+                for (int x = tid; x < rows * 8; x += T::NT) {
+                    const int r = x >> 3, c = x & 7;
+                    if (c * 8 >= tail) *reinterpret_cast<v4u*>(smem + (late(r, c) ? next : here) + part + r * 128 + ((c ^ swz(r)) << 4)) = (v4u){0, 0, 0, 0};
+                }
             }
         };
-        clear(st, BN, T::QT, OpQ::ROW_BYTES);
-        clear(st + T::P_OFF, BM, T::PT, OpP::ROW_BYTES);
+        clear(0, BN, T::QT, OpQ::ROW_BYTES, late_q);
+        clear(T::P_OFF, BM, T::PT, OpP::ROW_BYTES, late_p);
         __syncthreads();
     };
 
@@ -203,6 +230,7 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     const int straight[2] = {((2 * grp) ^ swz(row16)) << 4, ((2 * grp + 1) ^ swz(row16)) << 4};
     const int tk = 16 * grp + (row16 >> 2);                   // a turned read's row of LDS
     const int turned_lane = (lane & 3) * 8, tp = turn<BM>(tk) << 5, tqr = turn<BN>(tk) << 5;   // and its permutations
+    const bool plate[2] = {late_p(row16, 2 * grp), late_p(row16, 2 * grp + 1)}, qlate[2] = {late_q(row16, 2 * grp), late_q(row16, 2 * grp + 1)};
     auto fragment = [&](const uint8_t* part, int row0, int s, bool turned, int row_bytes, int tx) -> v4u {
         if (!turned) return *reinterpret_cast<const v4u*>(part + (row0 + row16) * 128 + straight[s]);
         const uint8_t* p = part + ((row0 << 1) ^ tx) + (tk + 8 * s) * row_bytes + turned_lane;
@@ -215,12 +243,19 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     struct Step {
         v4u f[T::JM + T::IN];
     };
+    auto fragment_p = [&](int i, int x, int s, int xp) {
+        const uint8_t *here = smem + (i % STAGES) * T::STAGE_BYTES, *next = smem + ((i + lag) % STAGES) * T::STAGE_BYTES;
+        return fragment((T::LAG && plate[s] ? next : here) + T::P_OFF, wm * T::WM + 16 * x, s, T::PT, OpP::ROW_BYTES, xp);
+    };
+    auto fragment_q = [&](int i, int x, int s, int xq) {
+        const uint8_t *here = smem + (i % STAGES) * T::STAGE_BYTES, *next = smem + ((i + lag) % STAGES) * T::STAGE_BYTES;
+        return fragment(T::LAG && qlate[s] ? next : here, wn * T::WN + 16 * x, s, T::QT, OpQ::ROW_BYTES, xq);
+    };
     // The products of the fragments in `from` and, in groups between them, reads of the fragments of step s of slice
     // i and the loads of slice i2 (load 1: if there is one, 2: there is): the matrix core, LDS and the loads' issue work side by side.
     auto products = [&](const Step& from, Step& to, int i, int s, auto load, int i2) {
         constexpr bool LOAD = decltype(load)::value != 0, CERTAIN = decltype(load)::value == 2;
         constexpr int READS = T::JM + T::IN, MFMAS = T::JM * T::IN, GROUPS = LOAD && T::NDMA > 4 ? T::NDMA : 4;
-        const uint8_t* st = smem + (i % STAGES) * T::STAGE_BYTES;
         // (opaque: an address for each fragment, formed ahead of the loop, costs registers that spill)
         int xp = tp, xq = tqr;
         if constexpr (T::PT) asm volatile("" : "+v"(xp));
@@ -229,12 +264,11 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
         for (int g = 0; g < GROUPS; ++g) {
 #pragma unroll
             for (int x = READS * g / GROUPS; x < READS * (g + 1) / GROUPS; ++x)
-                to.f[x] = x < T::JM ? fragment(st + T::P_OFF, wm * T::WM + 16 * x, s, T::PT, OpP::ROW_BYTES, xp)
-                                    : fragment(st, wn * T::WN + 16 * (x - T::JM), s, T::QT, OpQ::ROW_BYTES, xq);
+                to.f[x] = x < T::JM ? fragment_p(i, x, s, xp) : fragment_q(i, x - T::JM, s, xq);
             if constexpr (LOAD) {
 #pragma unroll
                 for (int x = T::NDMA * g / GROUPS; x < T::NDMA * (g + 1) / GROUPS; ++x)
-                    if (CERTAIN || i2 < nks) issue(i2, x);
+                    if (CERTAIN || i2 < lines) issue(i2, x);
             }
 #pragma unroll
             for (int x = MFMAS * g / GROUPS; x < MFMAS * (g + 1) / GROUPS; ++x)
@@ -243,40 +277,39 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
         }
     };
 
-    // Slices stand in a ring of STAGES.  The second step's fragments of a slice are read during the products of
+    // Slices (their lines) stand in a ring of STAGES.  The second step's fragments of a slice are read during the products of
     // its first, then the slice's place is free for slice i + STAGES, and the next slice's first step is read
     // during the products of the second: a wave's matrix core works across the barrier.
     Step f0, f1;
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-        if (i >= nks) continue;
+        if (i >= lines) continue;
         aim(i);
 #pragma unroll
         for (int x = 0; x < T::NDMA; ++x) issue(i, x);
     }
-    wait_slices<T::NDMA, STAGES - 1, 0>(min(STAGES - 1, nks - 1));
+    wait_slices<T::NDMA, STAGES - 1, 0>(min(STAGES - 1 - lag, nks - 1));
     __syncthreads();
     if (tail_at == 0) clear_tail(0);
 #pragma unroll
     for (int x = 0; x < T::JM + T::IN; ++x)
-        f0.f[x] = x < T::JM ? fragment(smem + T::P_OFF, wm * T::WM + 16 * x, 0, T::PT, OpP::ROW_BYTES, tp)
-                            : fragment(smem, wn * T::WN + 16 * (x - T::JM), 0, T::QT, OpQ::ROW_BYTES, tqr);
+        f0.f[x] = x < T::JM ? fragment_p(0, x, 0, tp) : fragment_q(0, x - T::JM, 0, tqr);
     using load = std::integral_constant<int, 1>;
     using load_surely = std::integral_constant<int, 2>;
     using none = std::integral_constant<int, 0>;
     int i = 0;
-    // slices with a whole one to load, without a branch
-    const int steady = nks - STAGES - (tail_at >= 0 ? 1 : 0);
+    // slices with a whole line to load, without a branch
+    const int steady = special - STAGES;
     for (; i < steady; ++i) {
         products(f0, f1, i, 1, none{}, 0);
-        wait_vmcnt<T::NDMA * (STAGES - 2)>();
+        wait_vmcnt<T::NDMA * (STAGES - 2 - lag)>();
         __syncthreads();
         products(f1, f0, i + 1, 0, load_surely{}, i + STAGES);
     }
     for (; i < nks; ++i) {
         products(f0, f1, i, 1, none{}, 0);
         if (i + 1 < nks) {
-            wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2, nks - 2 - i));
+            wait_slices<T::NDMA, STAGES - 2, 0>(min(STAGES - 2 - lag, nks - 2 - i));
             __syncthreads();
             aim(i + STAGES);
             if (i + 1 == tail_at) clear_tail(i + 1);
@@ -510,36 +543,38 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(v4u* p, int64_t units) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += (int64_t)gridDim.x * 256) p[i] = (v4u){0, 0, 0, 0};
 }
 
-template <int KIND>
-using Tile256 = Tile<256, 256, 2, 4, 2, KIND>;
-template <int KIND>
-using Tile128x256 = Tile<128, 256, 2, 4, 3, KIND>;
-template <int KIND>
-using Tile128 = Tile<128, 128, 2, 4, 4, KIND>;
-template <int KIND>
-using Tile64 = Tile<64, 64, 2, 2, 4, KIND>;
+template <int KIND, bool LAG>
+using Tile256 = Tile<256, 256, 2, 4, 2, KIND, false>;
+template <int KIND, bool LAG>
+using Tile128x256 = Tile<128, 256, 2, 4, 3, KIND, false>;
+template <int KIND, bool LAG>
+using Tile128 = Tile<128, 128, 2, 4, 4, KIND, LAG && KIND != kTurned>;
+template <int KIND, bool LAG>
+using Tile64 = Tile<64, 64, 2, 2, 4, KIND, LAG && KIND != kTurned>;
 
 uint32_t units(const ProductArgs& a) { return (uint32_t)(a.tiles_m * a.tiles_n * a.splits); }
 
-template <template <int> class T, int KIND>
+template <class T>
 void launch_one(const ProductArgs& a, hipStream_t s) {
-    product_kernel<T<KIND>><<<dim3(units(a)), T<KIND>::NT, 0, s>>>(a);
+    product_kernel<T><<<dim3(units(a)), T::NT, 0, s>>>(a);
 }
 
 template <int KIND>
 void launch_kind(const ProductArgs& a, int shape, hipStream_t s) {
-    if (shape == 0) launch_one<Tile256, KIND>(a, s);
-    else if (shape == 1) launch_one<Tile128x256, KIND>(a, s);
-    else if (shape == 2) launch_one<Tile128, KIND>(a, s);
-    else launch_one<Tile64, KIND>(a, s);
+    if (shape == 0) launch_one<Tile256<KIND, false>>(a, s);
+    else if (shape == 1) launch_one<Tile128x256<KIND, false>>(a, s);
+    else if (shape == 2 && a.lag) launch_one<Tile128<KIND, true>>(a, s);
+    else if (shape == 2) launch_one<Tile128<KIND, false>>(a, s);
+    else if (a.lag) launch_one<Tile64<KIND, true>>(a, s);
+    else launch_one<Tile64<KIND, false>>(a, s);
 }
 
 // the longer units first
-template <template <int> class T>
+template <class TX, class TW>
 void launch_two(const ProductArgs& x, const ProductArgs& w, hipStream_t s) {
     const dim3 grid(units(x) + units(w));
-    if (x.per_split >= w.per_split) product_pair_kernel<T<kTimesW>, T<kTurned>><<<grid, T<kTurned>::NT, 0, s>>>(x, w);
-    else product_pair_kernel<T<kTurned>, T<kTimesW>><<<grid, T<kTurned>::NT, 0, s>>>(w, x);
+    if (x.per_split >= w.per_split) product_pair_kernel<TX, TW><<<grid, TW::NT, 0, s>>>(x, w);
+    else product_pair_kernel<TW, TX><<<grid, TW::NT, 0, s>>>(w, x);
 }
 
 }  // namespace
@@ -554,10 +589,12 @@ void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s
 }
 
 void launch_gradients(const ProductArgs& x, const ProductArgs& w, int shape, hipStream_t s) {
-    if (shape == 0) launch_two<Tile256>(x, w, s);
-    else if (shape == 1) launch_two<Tile128x256>(x, w, s);
-    else if (shape == 2) launch_two<Tile128>(x, w, s);
-    else launch_two<Tile64>(x, w, s);
+    if (shape == 0) launch_two<Tile256<kTimesW, false>, Tile256<kTurned, false>>(x, w, s);
+    else if (shape == 1) launch_two<Tile128x256<kTimesW, false>, Tile128x256<kTurned, false>>(x, w, s);
+    else if (shape == 2 && x.lag) launch_two<Tile128<kTimesW, true>, Tile128<kTurned, false>>(x, w, s);
+    else if (shape == 2) launch_two<Tile128<kTimesW, false>, Tile128<kTurned, false>>(x, w, s);
+    else if (x.lag) launch_two<Tile64<kTimesW, true>, Tile64<kTurned, false>>(x, w, s);
+    else launch_two<Tile64<kTimesW, false>, Tile64<kTurned, false>>(x, w, s);
 }
 
 void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s) {

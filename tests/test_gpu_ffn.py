@@ -470,3 +470,28 @@ def test_training_runs():
     from gated_ffn import Block
     losses = Block(256, 128, 2, 8).train(normal(1, 96, 256), torch.zeros((96, 128), device="cuda"), 3)
     assert len(losses) == 3 and all(np.isfinite(losses))
+
+
+def off_by(x, chunks):
+    """The same matrix `chunks` x 16 bytes behind a 512-byte boundary, between NaN."""
+    t = torch.full((x.numel() + 512,), float("nan"), dtype=bf16, device="cuda")
+    v = t[8 * chunks:8 * chunks + x.numel()].view(x.shape)
+    v.copy_(x)
+    assert v.data_ptr() % 128 == 16 * (chunks % 8)
+    return v
+
+
+@pytest.mark.parametrize("chunks", [0, 1, 6])
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("tile,M,I,K", [("128x128", 777, 1032, 2056), ("64x64", 777, 1032, 2064), ("128x128", 1300, 456, 2080),
+                                        ("64x64", 1300, 456, 2112), ("128x256", 300, 264, 1032), ("256x256", 300, 264, 1032)])
+def test_rows_off_the_lines(tile, M, I, K, split, chunks, monkeypatch):
+    """Rows and matrices that start at any 16 bytes, with loads enough that the tiles take them by whole lines."""
+    monkeypatch.setenv("FP8GEMM_FORCE_CONFIG", "product:%s:%d" % (tile, split))
+    X, W, dH = off_by(normal(1, M, K), chunks), off_by(normal(2, 2 * I, K, scale=K ** -0.5), 7 * chunks % 8), off_by(normal(3, M, I), chunks)
+    pre, dpre = off_by(torch.zeros((M, 2 * I), dtype=bf16, device="cuda"), chunks), off_by(torch.zeros((M, 2 * I), dtype=bf16, device="cuda"), chunks)
+    H = fg.gated_ffn(X, W, pre=pre, out=off_by(torch.zeros((M, I), dtype=bf16, device="cuda"), chunks))
+    forward_close(X, W, "silu", H, pre)
+    for kept in (pre, None):
+        dX, dW = fg.gated_ffn_backward(dH, X, W, pre=kept, dpre=dpre)
+        backward_close(dH, X, W, "silu", kept, dpre, dX, dW)
