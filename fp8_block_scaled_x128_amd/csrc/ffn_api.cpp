@@ -385,9 +385,12 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     a.N = (int32_t)N;
     a.rank = (R + 15) / 16 * 16;
     a.steps = (int32_t)((K + 63) / 64);
-    // A workgroup a row, one launch and no workspace, while each of an adapter's matrices is small: the kernel's comment
-    // has both sides.  Of many rows (1000, R = 8, 256 to 256: 8.2 us either way) the matrices are read too often.
-    if (R <= 32 && K <= 2048 && R * K <= 32768 && R * N <= 32768 && T <= 512) {
+    // A workgroup a row, one launch and no workspace, while the two matrices are small: one CU reads them, and all of the
+    // workgroups do.  Measured, two launches and this, us, by R, K, N: 8 rows 16, 2048, 2048 6.8 and 6.1; 32, 1024, 1024
+    // 7.4 and 5.9; 16, 1024, 4096 6.8 and 7.5; 64, 1024, 1024 8.3 and 9.3; 20 rows 120, 800, 296 11.6 and 9.0; 70 rows
+    // 72, 176, 1152 14.0 and 10.7; 512 rows 128, 256, 256 17.4 and 9.2; 1000 rows 8, 512, 512 12.7 and 10.6; 1 row 8,
+    // 7168, 512 6.3 and 8.9.
+    if (K <= 4096 && T <= 1024 && R * (K + N) <= (T < 16 ? 72000 : T <= 512 ? 100000 : 16384)) {
         a.places = (int32_t)T;
         host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld by row", {T, R, K, N});
         launch_lora_rows(a, s);

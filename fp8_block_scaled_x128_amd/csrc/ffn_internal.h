@@ -120,7 +120,7 @@ struct LoraArgs {
     int32_t chunks;             // runs of kLoraSpan columns that a workgroup takes
 };
 
-void launch_lora_rows(const LoraArgs& a, hipStream_t s);      // both products, ranks up to 32
+void launch_lora_rows(const LoraArgs& a, hipStream_t s);      // both products, a workgroup a row
 void launch_lora_down(const LoraArgs& a, hipStream_t s);
 void launch_lora_up(const LoraArgs& a, hipStream_t s);
 

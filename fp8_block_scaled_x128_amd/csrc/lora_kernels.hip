@@ -7,6 +7,8 @@
 // adapter are left out of the results.  So any mix of rows is right, and one whose neighbours share an adapter
 // reads each of its matrices once per tile.
 
+#include <type_traits>
+
 #include "ffn_internal.h"
 #include "fp8gemm_device.h"
 #include "moe_device.h"
@@ -182,11 +184,19 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_down_kernel(const Lor
     }
 }
 
-// Both products of a row by one workgroup, for small adapters of a rank up to 16 RT: its waves take the steps of K in
-// turn, their sums meet in LDS, and a thread forms a column of the result from A x in fp32.  The adapter's two matrices
-// come to one CU, so this pays while they are small: measured, this and two launches, us, 64 rows, R = 8, 2048 to 1024,
-// 4.7 and 8.0; 45 rows, R = 8, 1544 to 2112, 5.4 and 7.9; 32 rows, R = 16, 2048 to 2048, 5.6 and 7.0, R = 32, 1024 to
-// 1024, 6.3 and 7.5; but 8 rows, R = 8, 4096 to 4096, 7.5 and 6.8, 1 row, R = 16, 7168 to 4096, 13 and 6.7.
+// Sum over groups of 1 << shift lanes, at most 16.
+__device__ __forceinline__ float sum_of_lanes(float d, int shift) {
+    auto moved = [](float x, auto ctrl) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true)); };
+    if (shift > 0) d += moved(d, std::integral_constant<int, 0xB1>{});      // lane ^ 1
+    if (shift > 1) d += moved(d, std::integral_constant<int, 0x4E>{});      // lane ^ 2
+    if (shift > 2) d += moved(d, std::integral_constant<int, 0x141>{});     // 7 - lane of 8: the other four
+    if (shift > 3) d += moved(d, std::integral_constant<int, 0x140>{});     // 15 - lane of 16: the other eight
+    return d;
+}
+
+// Both products of a row by one workgroup, for small adapters: its waves take the steps of K in turn, their sums meet in
+// LDS, and lanes form the columns of the result from A x in fp32.  One CU brings the adapter's two matrices in, so this
+// pays while they are small (the choice, with both sides measured, is the host's): 64 rows, R = 8, 2048 to 1024, 4.6 us.
 template <int RT>
 __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const LoraArgs a) {
     constexpr int kRowThreads = kDownWaves * 64;
@@ -211,7 +221,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
     v4f acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
-    constexpr int AHEAD = 4 / RT;                            // steps whose loads go out together
+    constexpr int AHEAD = RT < 4 ? 4 / RT : 1;                           // steps whose loads go out together
     for (int s0 = wave; s0 < a.steps; s0 += AHEAD * kDownWaves) {
         v4u w[AHEAD][2][RT], x[AHEAD][2];
 #pragma unroll
@@ -249,40 +259,39 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
         for (int w = 1; w < kDownWaves; ++w) v += red[w][tid >> 2][tid & 3];
         low[tid] = v;
     }
+    // a column's row of B, and the sums with A x, are shared by as many lanes as it has 16-byte pieces (a power of two)
     const float scale = scale_of(a, mine.id);
-    const uint16_t* bp = a.B + (int64_t)mine.id * a.N * a.R;
     const int units = a.R / 8;
-    constexpr int COLS = 4;                                  // columns of a thread at a time
-    bool ready = false;
-    for (int n0 = 0; n0 < a.N; n0 += COLS * kRowThreads) {
-        v4u b[COLS][2 * RT];
+    const int shift = RT == 1 ? units - 1 : 32 - __builtin_clz(units - 1);
+    const int u = tid & ((1 << shift) - 1), col = tid >> shift, cols = kRowThreads >> shift;
+    const uint16_t* bp = a.B + (int64_t)mine.id * a.N * a.R + 8 * min(u, units - 1);
+    constexpr int COLS = RT == 1 ? 4 : 8;                    // columns of a lane at a time
+    v4f v[2];
+    for (int n0 = 0; n0 < a.N; n0 += COLS * cols) {
+        v4u b[COLS];
         uint16_t yv[COLS];
 #pragma unroll
         for (int c = 0; c < COLS; ++c) {
-            const int n = min(n0 + c * kRowThreads + tid, a.N - 1);
+            const int n = min(n0 + c * cols + col, a.N - 1);
+            b[c] = *reinterpret_cast<const v4u*>(bp + (int64_t)n * a.R);
             yv[c] = y[n];
-#pragma unroll
-            for (int u = 0; u < 2 * RT; ++u) b[c][u] = *reinterpret_cast<const v4u*>(bp + (int64_t)n * a.R + 8 * min(u, units - 1));
         }
-        if (!ready) __syncthreads();                         // A x is there
-        ready = true;
-        float d[COLS] = {};
-#pragma unroll
-        for (int u = 0; u < 2 * RT; ++u) {
-            if (u >= units) continue;
-            const v4f v[2] = {low[2 * u], low[2 * u + 1]};
-#pragma unroll
-            for (int c = 0; c < COLS; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    d[c] = __builtin_fmaf(__uint_as_float(b[c][u][e] << 16), v[e >> 1][2 * (e & 1)], d[c]);
-                    d[c] = __builtin_fmaf(__uint_as_float(b[c][u][e] & 0xFFFF0000u), v[e >> 1][2 * (e & 1) + 1], d[c]);
-                }
+        if (n0 == 0) {
+            __syncthreads();                                 // A x is there
+            v[0] = low[2 * min(u, units - 1)];
+            v[1] = low[2 * min(u, units - 1) + 1];
         }
 #pragma unroll
         for (int c = 0; c < COLS; ++c) {
-            const int n = n0 + c * kRowThreads + tid;
-            if (n < a.N) out[n] = f32_to_bf16(__builtin_fmaf(d[c], scale, bf16_to_f32(yv[c])));
+            float d = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d = __builtin_fmaf(__uint_as_float(b[c][e] << 16), v[e >> 1][2 * (e & 1)], d);
+                d = __builtin_fmaf(__uint_as_float(b[c][e] & 0xFFFF0000u), v[e >> 1][2 * (e & 1) + 1], d);
+            }
+            d = sum_of_lanes(u < units ? d : 0.f, shift);
+            const int n = n0 + c * cols + col;
+            if (u == 0 && n < a.N) out[n] = f32_to_bf16(__builtin_fmaf(d, scale, bf16_to_f32(yv[c])));
         }
     }
 }
@@ -788,7 +797,9 @@ void launch_up(const LoraArgs& a, hipStream_t s) {
 void launch_lora_rows(const LoraArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)a.places);
     if (a.rank <= 16) lora_row_kernel<1><<<grid, kDownWaves * 64, 0, s>>>(a);
-    else lora_row_kernel<2><<<grid, kDownWaves * 64, 0, s>>>(a);
+    else if (a.rank <= 32) lora_row_kernel<2><<<grid, kDownWaves * 64, 0, s>>>(a);
+    else if (a.rank <= 64) lora_row_kernel<4><<<grid, kDownWaves * 64, 0, s>>>(a);
+    else lora_row_kernel<8><<<grid, kDownWaves * 64, 0, s>>>(a);
 }
 
 void launch_lora_down(const LoraArgs& a, hipStream_t s) {

@@ -78,7 +78,7 @@ def test_refusals_of_device_tensors():
 
 # a kernel of few rows, tiles with and without K splits; adapters by row, a few rows a workgroup, 64 rows
 GATED = [(3, 128, 512), (40, 72, 1024), (300, 264, 712), (1023, 336, 456)]
-LORA = [(20, 4, 16, 640, 264), (70, 9, 16, 2560, 520), (1500, 4, 32, 328, 520)]
+LORA = [(20, 4, 16, 640, 264), (70, 9, 16, 2560, 520), (70, 9, 16, 4360, 520), (1500, 4, 32, 328, 520)]
 
 
 def test_graphs():
@@ -129,7 +129,7 @@ def test_capture_on_an_unprepared_stream(monkeypatch):
     M, I, K = 40, 72, 1024
     X, W, dH = normal(1, M, K), normal(2, 2 * I, K, scale=K ** -0.5), normal(3, M, I)
     c = case(20, 4, 16, 640, 264, seed=2)
-    big = case(20, 4, 16, 2560, 264, seed=2)
+    big = case(20, 4, 16, 4608, 264, seed=2)
     o = [torch.zeros(n, dtype=bf16, device="cuda") for n in ((M, 2 * I), (M, K), (2 * I, K), (20, 264))]
     fg.gated_ffn(X, W)
     torch.cuda.synchronize()
@@ -186,7 +186,7 @@ def test_threads_on_their_own_streams():
 def test_threads_on_one_stream():
     """Two threads' calls on one stream share its workspace and keep apart."""
     s = torch.cuda.Stream()
-    c = case(70, 9, 16, 2560, 520, seed=70)
+    c = case(70, 9, 16, 4360, 520, seed=70)
     X, W, dH = normal(1, 40, 1024), normal(2, 144, 1024, scale=2.0 ** -5), normal(3, 40, 72)
     jobs = [lambda: (fg.lora_add(c["Y"], c["X"], c["A"], c["B"], c["ids"], c["scales"], stream=s),),
             lambda: (fg.gated_ffn(X, W, stream=s),) + fg.gated_ffn_backward(dH, X, W, stream=s)]
@@ -330,7 +330,7 @@ def test_pre_past_4gib():
         backward_close(dH[rows], X[rows], W, "silu", None if p is None else p[rows], dpre[rows], dX[rows], dW)
 
 
-@pytest.mark.parametrize("T,R,K,N", [(300, 16, 136, 264), (300, 16, 2568, 264), (1100, 16, 136, 264)])
+@pytest.mark.parametrize("T,R,K,N", [(300, 16, 136, 264), (300, 16, 2568, 264), (300, 16, 4168, 264), (1100, 16, 136, 264)])
 def test_adapters_rows_past_4gib(T, R, K, N):
     """Rows of X, Y and the result so far apart that they pass 2^32 bytes."""
     c = case(T, 3, R, K, N, seed=T)
@@ -338,7 +338,7 @@ def test_adapters_rows_past_4gib(T, R, K, N):
     step = 1 << 23 if T <= 300 else 1 << 21
     wide = torch.empty((T, step), dtype=bf16, device="cuda")
     assert 2 * wide.numel() > 1 << 32
-    X, Y, out = wide[:, :K], wide[:, 4096:4096 + N], wide[:, 8192:8192 + N]
+    X, Y, out = wide[:, :K], wide[:, 8192:8192 + N], wide[:, 12288:12288 + N]
     X.copy_(c["X"])
     Y.copy_(c["Y"])
     assert torch.equal(fg.lora_add(Y, X, c["A"], c["B"], c["ids"], c["scales"], out=out), want)
@@ -379,7 +379,7 @@ def test_adapters_in_several_passes(T, L, R, K, N):
     assert fg.read_device_error() == 0
 
 
-@pytest.mark.parametrize("T,L,R,K,N", [(20, 4, 24, 264, 136), (40, 4, 16, 2568, 136), (1100, 4, 16, 200, 264), (700, 3, 72, 136, 136)])
+@pytest.mark.parametrize("T,L,R,K,N", [(20, 4, 24, 264, 136), (40, 4, 16, 2568, 136), (40, 4, 16, 4168, 136), (70, 4, 104, 1200, 136), (1100, 4, 16, 200, 264), (700, 3, 72, 136, 136)])
 def test_adapters_in_every_kernel(T, L, R, K, N):
     """By row, a few rows a workgroup, and 64 rows: apart, in place, in another order, ids and orders out of range, neighbours
     that are not finite, an infinite A x."""

@@ -61,7 +61,13 @@ SIZES = [(1, 1, 8, 8, 8), (1, 3, 16, 7168, 4096), (2, 5, 24, 72, 264), (15, 4, 3
          (700, 3, 72, 1000, 136), (1500, 2, 128, 512, 264), (3000, 200, 16, 256, 512),
          # both sides of where a row's two products are one launch: the rows, K, R K and R N
          (512, 6, 8, 2048, 1024), (513, 6, 8, 2048, 1024), (9, 3, 16, 2056, 128), (33, 3, 32, 1032, 128), (70, 9, 16, 128, 2056),
-         (20, 2, 32, 1024, 1024), (130, 7, 40, 128, 136), (300, 11, 48, 264, 72), (5, 2, 16, 2312, 264)]
+         (20, 2, 32, 1024, 1024), (130, 7, 40, 128, 136), (300, 11, 48, 264, 72), (5, 2, 16, 2312, 264),
+         (15, 3, 16, 2048, 2448), (15, 3, 16, 2048, 2456), (16, 3, 64, 1024, 536), (16, 3, 64, 1024, 544), (9, 2, 104, 72, 600),
+         (77, 2, 120, 40, 776), (3, 1, 8, 4096, 64), (3, 1, 8, 4104, 64), (1024, 5, 40, 264, 136), (1025, 5, 40, 264, 136),
+         (1030, 70, 24, 264, 72), (60, 1, 24, 40, 4120), (33, 2, 8, 16, 12000),
+         # two launches, few rows a workgroup
+         (5, 3, 16, 4168, 264), (33, 20, 24, 4168, 136), (70, 9, 32, 4104, 264), (130, 7, 48, 2400, 264), (300, 11, 72, 1400, 136),
+         (256, 64, 16, 7168, 512), (20, 4, 128, 1000, 1000), (40, 13, 104, 1200, 264), (400, 2, 24, 4160, 264)]
 
 
 @pytest.mark.parametrize("T,L,R,K,N", SIZES)
