@@ -196,6 +196,17 @@ int share_workspace(std::initializer_list<std::pair<ProductArgs*, Choice>> produ
     return FP8GEMM_OK;
 }
 
+// Whether adapters are added by a workgroup a row, one launch and no workspace.  One CU reads a row's two matrices, so they
+// have to be small; two rounds of workgroups take twice as long, and the two launches take longer the more rows with
+// different adapters stand together, which the host does not know.  Measured, two launches (rows in any order, by adapter)
+// and this, us, by R (K + N): 8 rows 32768 6.8 and 5.3, 65536 7.4 and 5.9, 81920 6.8 and 7.5; 40 rows 104448 10.6, 10.5 and
+// 9.3, 144000 15.5, 12.0 and 12.4; 100 rows 104448 19.3, 12.9 and 9.4, 166400 17, 10.6 and 10.8; 200 rows 110336 16, 9.8 and
+// 9.7; 400 rows 51968 17.6, 10.2 and 9.0, 104448 29, 11.0 and 16; 1000 rows 8192 12.7 and 10.6.
+bool by_row(int64_t T, int64_t R, int64_t K, int64_t N) {
+    const int64_t most = T < 32 ? (R > 64 ? 100000 : 72000) : T < 64 ? 110000 : T <= 256 ? 150000 : T <= 512 ? 72000 : T <= 1024 ? 16384 : 0;
+    return K <= 4096 && R * (K + N) <= most;
+}
+
 int check_gated(int64_t M, int64_t I, int64_t K, int32_t act) {
     if (M < 0 || I <= 0 || K <= 0 || I % 8 != 0 || K % 8 != 0) return FP8GEMM_ERR_BAD_SHAPE;
     if (act != FP8GEMM_ACT_SILU && act != FP8GEMM_ACT_GELU_TANH) return FP8GEMM_ERR_BAD_SHAPE;
@@ -385,12 +396,7 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     a.N = (int32_t)N;
     a.rank = (R + 15) / 16 * 16;
     a.steps = (int32_t)((K + 63) / 64);
-    // A workgroup a row, one launch and no workspace, while the two matrices are small: one CU reads them, and all of the
-    // workgroups do.  Measured, two launches and this, us, by R, K, N: 8 rows 16, 2048, 2048 6.8 and 6.1; 32, 1024, 1024
-    // 7.4 and 5.9; 16, 1024, 4096 6.8 and 7.5; 64, 1024, 1024 8.3 and 9.3; 20 rows 120, 800, 296 11.6 and 9.0; 70 rows
-    // 72, 176, 1152 14.0 and 10.7; 512 rows 128, 256, 256 17.4 and 9.2; 1000 rows 8, 512, 512 12.7 and 10.6; 1 row 8,
-    // 7168, 512 6.3 and 8.9.
-    if (K <= 4096 && T <= 1024 && R * (K + N) <= (T < 16 ? 72000 : T <= 512 ? 100000 : 16384)) {
+    if (by_row(T, R, K, N)) {
         a.places = (int32_t)T;
         host_set_config("lora_add T=%lld R=%lld K=%lld N=%lld by row", {T, R, K, N});
         launch_lora_rows(a, s);

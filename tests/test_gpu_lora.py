@@ -67,7 +67,8 @@ SIZES = [(1, 1, 8, 8, 8), (1, 3, 16, 7168, 4096), (2, 5, 24, 72, 264), (15, 4, 3
          (1030, 70, 24, 264, 72), (60, 1, 24, 40, 4120), (33, 2, 8, 16, 12000),
          # two launches, few rows a workgroup
          (5, 3, 16, 4168, 264), (33, 20, 24, 4168, 136), (70, 9, 32, 4104, 264), (130, 7, 48, 2400, 264), (300, 11, 72, 1400, 136),
-         (256, 64, 16, 7168, 512), (20, 4, 128, 1000, 1000), (40, 13, 104, 1200, 264), (400, 2, 24, 4160, 264)]
+         (256, 64, 16, 7168, 512), (20, 4, 128, 1000, 1000), (40, 13, 104, 1200, 264), (400, 2, 24, 4160, 264), (63, 40, 48, 2104, 264),
+         (64, 40, 48, 2104, 264), (256, 3, 128, 400, 776), (257, 3, 128, 400, 776), (200, 12, 72, 2200, 136), (150, 30, 32, 1400, 3600)]
 
 
 @pytest.mark.parametrize("T,L,R,K,N", SIZES)
