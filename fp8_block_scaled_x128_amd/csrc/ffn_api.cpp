@@ -284,10 +284,21 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         return launched();
     }
     // every choice and the workspace before the first launch
-    Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0};
+    Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0}, any;
     ProductArgs ap{}, ax{}, aw{};
+    GatedRowsArgs ar{};
+    const bool rows = !pre && !forced(&any) && few_rows(M, I, K, d.cus);
     auto slices = [](int64_t k) { return (k + kSliceK - 1) / kSliceK; };
-    if (!pre) {
+    if (rows) {
+        ar.X = static_cast<const uint16_t*>(X);
+        ar.W = static_cast<const uint16_t*>(W);
+        ar.dH = static_cast<const uint16_t*>(dH);
+        ar.pre = static_cast<uint16_t*>(dpre);
+        ar.M = (int32_t)M;
+        ar.I = (int32_t)I;
+        ar.K = (int32_t)K;
+        ar.gelu = act == FP8GEMM_ACT_GELU_TANH;
+    } else if (!pre) {
         ap.P = static_cast<const uint16_t*>(X);
         ap.Q = static_cast<const uint16_t*>(W);
         ap.dH = static_cast<const uint16_t*>(dH);
@@ -340,6 +351,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         g.gelu = act == FP8GEMM_ACT_GELU_TANH;
         g.div_row = make_fastdiv((uint32_t)(I / 8));
         launch_gated_grad(g, s);
+    } else if (rows) {
+        launch_gated_rows(ar, s);
     } else {
         launch_product(ap, kGatedBack, cp.shape, s);
     }

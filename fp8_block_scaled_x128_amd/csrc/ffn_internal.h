@@ -69,8 +69,9 @@ void launch_gradients(const ProductArgs& x, const ProductArgs& w, int shape, hip
 struct GatedRowsArgs {
     const uint16_t* X;          // [M][K]
     const uint16_t* W;          // [2I][K]
-    uint16_t* out;              // [M][I]
-    uint16_t* pre;              // [M][2I] or null
+    const uint16_t* dH;         // [M][I], for gradients, or null
+    uint16_t* out;              // [M][I]; none with dH
+    uint16_t* pre;              // [M][2I] or null; the gradients with dH
     int32_t M, I, K;
     int32_t gelu;
 };

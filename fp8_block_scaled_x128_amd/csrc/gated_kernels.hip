@@ -451,7 +451,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES_PER_SIMD) void product_pair_kernel(
 // ---- the block for few rows -----------------------------------------------------------------------------
 // A workgroup has 8 output columns, whose 8 gate rows and 8 up rows of W are the 16 rows of one matrix-core
 // operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in turn, two on
-// their way each; their sums meet in LDS and are added in wave order.
+// their way each; their sums meet in LDS and are added in wave order.  With dH the sums' gradients go to `pre`.
 constexpr int kRowsWaves = 8, kRowsAhead = 2;
 
 __global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const GatedRowsArgs a) {
@@ -507,7 +507,15 @@ __global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const Ga
             g += red[w][from][c & 3];
             u += red[w][from + 32][c & 3];
         }
-        a.out[(int64_t)m * a.I + n0 + c] = f32_to_bf16(activation(g, a.gelu) * u);
+        if (a.dH) {
+            const float d = bf16_to_f32(a.dH[(int64_t)m * a.I + n0 + c]);
+            float act;
+            const float der = activation_grad(g, a.gelu, &act);
+            g = d * u * der;
+            u = d * act;
+        } else {
+            a.out[(int64_t)m * a.I + n0 + c] = f32_to_bf16(activation(g, a.gelu) * u);
+        }
         if (a.pre) {
             a.pre[(int64_t)m * 2 * a.I + n0 + c] = f32_to_bf16(g);
             a.pre[(int64_t)m * 2 * a.I + a.I + n0 + c] = f32_to_bf16(u);
