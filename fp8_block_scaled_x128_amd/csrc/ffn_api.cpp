@@ -33,17 +33,23 @@ struct Choice {
     double us;                  // of its slices and exchange
 };
 
-// FP8GEMM_FORCE_CONFIG=product:BMxBN:SPLIT
-bool forced(Choice* c) {
+// FP8GEMM_FORCE_CONFIG=product:BMxBN:SPLIT or product:BMxBNxRING:SPLIT
+bool forced(Choice* c, bool gated) {
     const char* s = std::getenv("FP8GEMM_FORCE_CONFIG");
-    int bm, bn, split;
-    if (!s || std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3) return false;
-    for (int i = 0; i < kTileShapes; ++i)
-        if (kTiles[i].bm == bm && kTiles[i].bn == bn) {
+    int bm, bn, split, ring = 0;
+    if (!s || (std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3 && std::sscanf(s, "product:%dx%dx%d:%d", &bm, &bn, &ring, &split) != 4)) return false;
+    for (int i = 0; i < (gated ? kGatedShapes : kTileShapes); ++i)
+        if (kTiles[i].bm == bm && kTiles[i].bn == bn && (ring == 0 || kTiles[i].ring == ring)) {
             *c = {i, std::max(1, split), 0.0};
             return true;
         }
     return false;
+}
+
+// Time of a slice where the CUs have up to `units` workgroups together.
+double slice_us(const TileShape& t, int64_t units, int cus) {
+    const int64_t most = std::min<int64_t>((units + cus - 1) / cus, t.per_cu);
+    return most <= 1 ? t.alone : t.alone + (t.shared - t.alone) * (double)(most - 1) / (double)(t.per_cu - 1);
 }
 
 // `off`: rows off the lines (of one operand of kTimesW)
@@ -65,9 +71,9 @@ bool loads_count(int64_t tiles, const TileShape& t, int64_t slices) { return til
 Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus, bool off) {
     const bool gated = kind == kGated || kind == kGatedBack;
     Choice best{0, 1, 1e30};
-    if (forced(&best)) return best;
+    if (forced(&best, gated)) return best;
     const double bytes = (128e-6 * (double)slices * (double)(rows + (gated ? 2 : 1) * cols) + 2e-6 * (double)rows * (double)cols) / 5.2;
-    for (int i = 0; i < kTileShapes; ++i) {
+    for (int i = 0; i < (gated ? kGatedShapes : kTileShapes); ++i) {
         const TileShape& t = kTiles[i];
         const int64_t width = gated ? t.bn / 2 : t.bn;
         const int64_t tiles = ((rows + t.bm - 1) / t.bm) * ((cols + width - 1) / width);
@@ -77,7 +83,7 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus,
             const int64_t per = (slices + s - 1) / s;
             if (s > 1 && (slices + per - 1) / per != s) continue;
             const int64_t units = tiles * s, last = units % slots;
-            const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : last <= cus ? t.alone : t.shared);
+            const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : slice_us(t, last, cus));
             const double cost = std::max(((double)per + t.ends) * rounds * slow, bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
             if (cost < best.us) best = {i, (int)s, cost};
         }
@@ -115,7 +121,7 @@ double rounds_of(int64_t n, double L, int64_t n2, double L2, int64_t slots) {
 // other and together, us: M = 1023, I = 1416, K = 2056 55 and 47; 1024, 2048, 7168 138 and 120; 905, 336, 456 17.8 and
 // 13.1; 77, 512, 1536 12.7 and 11.4; but 256, 2048, 7168 62 and 73, 4096, 2048, 7168 417 and 420.
 bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx, Choice* cw) {
-    if (forced(cx)) {
+    if (forced(cx, false)) {
         *cw = *cx;
         return true;
     }
@@ -136,7 +142,7 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
                 const int64_t nx = tx * px, nw = tw * pw;
                 const double rounds = lx >= lw ? rounds_of(nx, lx, nw, lw, slots) : rounds_of(nw, lw, nx, lx, slots);
                 const int64_t most = std::max(px > 1 ? px : 0, pw > 1 ? pw : 0);
-                const double us = 1.03 * std::max(rounds * (nx + nw <= cus ? t.alone : t.shared), bytes) +
+                const double us = 1.03 * std::max(rounds * slice_us(t, nx + nw, cus), bytes) +
                                   (most ? t.exchange + t.exchange_split * (double)most : 0.0);
                 if (us >= least) continue;
                 least = us;
@@ -158,7 +164,7 @@ int arrange(ProductArgs* a, Choice* c, Product kind) {
     a->per_split = (a->slices + c->splits - 1) / c->splits;
     a->splits = c->splits = (a->slices + a->per_split - 1) / a->per_split;       // none without a slice
     if (tm > kMaxUnits / tn || tm * tn > kMaxUnits / a->splits) return FP8GEMM_ERR_UNSUPPORTED;
-    a->lag = t.bm <= 128 && t.bn <= 128 && off_the_lines(*a, kind) && (kind == kTimesW || loads_count(tm * tn, t, a->slices));
+    a->lag = t.ring >= 4 && off_the_lines(*a, kind) && (kind == kTimesW || loads_count(tm * tn, t, a->slices));
     a->tiles_m = (int32_t)tm;
     a->tiles_n = (int32_t)tn;
     a->group_m = (int32_t)std::min<int64_t>(tm, 8);
@@ -231,7 +237,7 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     if (st != FP8GEMM_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     Choice c;
-    if (!forced(&c) && few_rows(M, I, K, d.cus)) {
+    if (!forced(&c, true) && few_rows(M, I, K, d.cus)) {
         GatedRowsArgs a{};
         a.X = static_cast<const uint16_t*>(X);
         a.W = static_cast<const uint16_t*>(W);
@@ -287,7 +293,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     Choice cp{0, 1, 0}, cx{0, 1, 0}, cw{0, 1, 0}, any;
     ProductArgs ap{}, ax{}, aw{};
     GatedRowsArgs ar{};
-    const bool rows = !pre && !forced(&any) && few_rows(M, I, K, d.cus);
+    const bool rows = !pre && !forced(&any, true) && few_rows(M, I, K, d.cus);
     auto slices = [](int64_t k) { return (k + kSliceK - 1) / kSliceK; };
     if (rows) {
         ar.X = static_cast<const uint16_t*>(X);
@@ -339,8 +345,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     st = share_workspace({{&ap, cp}}, s, &hold);
     if (st == FP8GEMM_OK) st = share_workspace({{&ax, cx}, {&aw, cw}}, s, &hold);
     if (st != FP8GEMM_OK) return st;
-    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lld split=%lld dW tile=%lld split=%lld",
-                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, cx.splits, dW ? kTiles[cw.shape].bm : 0, cw.splits});
+    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lld split=%lld dW tile=%lldx%lld split=%lld",
+                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, kTiles[cx.shape].ring, cx.splits, dW ? kTiles[cw.shape].bm : 0, kTiles[cw.shape].ring, cw.splits});
     if (pre) {
         GatedGradArgs g{};
         g.pre = static_cast<const uint16_t*>(pre);

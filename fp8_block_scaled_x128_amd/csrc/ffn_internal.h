@@ -46,18 +46,20 @@ inline bool off_the_lines(const ProductArgs& a, Product kind) {
     return (kind != kTurned && off(a.P, a.ldp)) || ((kind == kGated || kind == kGatedBack) && off(a.Q, a.ldq));
 }
 
-// Tiles of a workgroup: bm rows of P, bn rows of Q.  Times in us, measured: a slice where the workgroup has a
-// CU to itself, and where `per_cu` share it (for all of them); how much longer it takes with Q turned, and with both
-// operands, and with rows off the lines; its start and end, in slices; a K split's exchange (constant, and by split).
+// Tiles of a workgroup: bm rows of P, bn rows of Q, a ring of `ring` slices.  Times in us, measured: a slice where the
+// workgroup has a CU to itself, and where `per_cu` share it (for all of them); how much longer it takes with Q turned, with
+// both operands, and with rows off the lines; its start and end, in slices; a K split's exchange (constant, and by split).
+// The last shape is for gradients: its starts and ends, most of the time of short sums, go on beside those of three others.
 struct TileShape {
-    int bm, bn, per_cu;
+    int bm, bn, ring, per_cu;
     double alone, shared, turned, both_turned, off, ends, exchange, exchange_split;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1, 1.48, 1.48, 1.00, 1.05, 1.15, 5.3, 20.0, 2.7},
-                                {128, 256, 1, 0.83, 0.83, 1.05, 1.15, 1.30, 6.0, 8.0, 1.5},
-                                {128, 128, 1, 0.47, 0.47, 1.15, 1.30, 1.10, 8.0, 6.0, 0.7},
-                                {64, 64, 2, 0.25, 0.46, 1.05, 1.10, 1.20, 5.3, 1.0, 0.3}};
-constexpr int kTileShapes = 4;
+constexpr TileShape kTiles[] = {{256, 256, 2, 1, 1.48, 1.48, 1.00, 1.05, 1.15, 5.3, 20.0, 2.7},
+                                {128, 256, 3, 1, 0.83, 0.83, 1.05, 1.15, 1.30, 6.0, 8.0, 1.5},
+                                {128, 128, 4, 1, 0.47, 0.47, 1.15, 1.30, 1.10, 8.0, 6.0, 0.7},
+                                {64, 64, 4, 2, 0.25, 0.46, 1.05, 1.10, 1.20, 5.3, 1.0, 0.3},
+                                {64, 64, 2, 4, 0.42, 0.85, 1.05, 1.10, 1.25, 2.5, 1.5, 0.6}};
+constexpr int kTileShapes = 5, kGatedShapes = 4;
 constexpr int kSliceK = 64;
 
 void launch_product(const ProductArgs& a, Product kind, int shape, hipStream_t s);

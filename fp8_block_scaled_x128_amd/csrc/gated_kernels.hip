@@ -103,7 +103,7 @@ struct Tile {
     static constexpr int STG = WM * PITCH;
     static constexpr int SMEM = STAGES * STAGE_BYTES > NW * STG ? STAGES * STAGE_BYTES : NW * STG;
     static_assert(SMEM < 160 * 1024, "LDS budget");
-    static constexpr int WAVES_PER_SIMD = NW / 4 * (SMEM < 80 * 1024 ? 2 : 1);   // as LDS allows
+    static constexpr int WAVES_PER_SIMD = NW / 4 * (SMEM < 40 * 1024 ? 4 : SMEM < 80 * 1024 ? 2 : 1);   // as LDS allows
 };
 
 // Unit `block` of the `blocks` of a product; smem: T::SMEM bytes.
@@ -560,6 +560,9 @@ using Tile128 = Tile<128, 128, 2, 4, 4, KIND, LAG && KIND != kTurned>;
 template <int KIND, bool LAG>
 using Tile64 = Tile<64, 64, 2, 2, 4, KIND, LAG && KIND != kTurned>;
 
+template <int KIND>
+using Tile64Short = Tile<64, 64, 2, 2, 2, KIND, false>;
+
 uint32_t units(const ProductArgs& a) { return (uint32_t)(a.tiles_m * a.tiles_n * a.splits); }
 
 template <class T>
@@ -573,8 +576,9 @@ void launch_kind(const ProductArgs& a, int shape, hipStream_t s) {
     else if (shape == 1) launch_one<Tile128x256<KIND, false>>(a, s);
     else if (shape == 2 && a.lag) launch_one<Tile128<KIND, true>>(a, s);
     else if (shape == 2) launch_one<Tile128<KIND, false>>(a, s);
-    else if (a.lag) launch_one<Tile64<KIND, true>>(a, s);
-    else launch_one<Tile64<KIND, false>>(a, s);
+    else if (shape == 3 && a.lag) launch_one<Tile64<KIND, true>>(a, s);
+    else if (shape == 3) launch_one<Tile64<KIND, false>>(a, s);
+    else if constexpr (KIND == kTimesW || KIND == kTurned) launch_one<Tile64Short<KIND>>(a, s);
 }
 
 // the longer units first
@@ -601,8 +605,9 @@ void launch_gradients(const ProductArgs& x, const ProductArgs& w, int shape, hip
     else if (shape == 1) launch_two<Tile128x256<kTimesW, false>, Tile128x256<kTurned, false>>(x, w, s);
     else if (shape == 2 && x.lag) launch_two<Tile128<kTimesW, true>, Tile128<kTurned, false>>(x, w, s);
     else if (shape == 2) launch_two<Tile128<kTimesW, false>, Tile128<kTurned, false>>(x, w, s);
-    else if (x.lag) launch_two<Tile64<kTimesW, true>, Tile64<kTurned, false>>(x, w, s);
-    else launch_two<Tile64<kTimesW, false>, Tile64<kTurned, false>>(x, w, s);
+    else if (shape == 3 && x.lag) launch_two<Tile64<kTimesW, true>, Tile64<kTurned, false>>(x, w, s);
+    else if (shape == 3) launch_two<Tile64<kTimesW, false>, Tile64<kTurned, false>>(x, w, s);
+    else launch_two<Tile64Short<kTimesW>, Tile64Short<kTurned>>(x, w, s);
 }
 
 void launch_gated_rows(const GatedRowsArgs& a, hipStream_t s) {

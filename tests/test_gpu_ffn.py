@@ -28,14 +28,14 @@ def bits(t):
 
 @pytest.mark.parametrize("act,kept", [("silu", True), ("gelu_tanh", False)])
 @pytest.mark.parametrize("split", [1, 2, 3, 5])
-@pytest.mark.parametrize("tile", ["256x256", "128x256", "128x128", "64x64"])
+@pytest.mark.parametrize("tile", ["256x256", "128x256", "128x128", "64x64", "64x64x2"])
 def test_every_tile_and_split(tile, split, act, kept, monkeypatch):
     monkeypatch.setenv("FP8GEMM_FORCE_CONFIG", "product:%s:%d" % (tile, split))
     M, I, K = 333, 264, 712
     X, W, dH = normal(1, M, K), normal(2, 2 * I, K, scale=K ** -0.5), normal(3, M, I)
     pre = torch.empty((M, 2 * I), dtype=bf16, device="cuda")
     H = fg.gated_ffn(X, W, act=act, pre=pre)
-    assert tile in fg.last_config()
+    assert tile in fg.last_config() or tile == "64x64x2"     # (a shape of the gradients)
     forward_close(X, W, act, H, pre)
     dpre = torch.empty_like(pre)
     for need in ((True, True), (True, False), (False, True)):
@@ -484,7 +484,7 @@ def off_by(x, chunks):
 @pytest.mark.parametrize("chunks", [0, 1, 6])
 @pytest.mark.parametrize("split", [1, 3])
 @pytest.mark.parametrize("tile,M,I,K", [("128x128", 777, 1032, 2056), ("64x64", 777, 1032, 2064), ("128x128", 1300, 456, 2080),
-                                        ("64x64", 1300, 456, 2112), ("128x256", 300, 264, 1032), ("256x256", 300, 264, 1032)])
+                                        ("64x64", 1300, 456, 2112), ("64x64x2", 300, 264, 1032), ("128x256", 300, 264, 1032), ("256x256", 300, 264, 1032)])
 def test_rows_off_the_lines(tile, M, I, K, split, chunks, monkeypatch):
     """Rows and matrices that start at any 16 bytes, with loads enough that the tiles take them by whole lines."""
     monkeypatch.setenv("FP8GEMM_FORCE_CONFIG", "product:%s:%d" % (tile, split))
