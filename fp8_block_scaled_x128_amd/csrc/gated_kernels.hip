@@ -2,6 +2,17 @@
 //   H = act(X Wg^T) * (X Wu^T)          W [2I,K] = gate rows, then up rows
 //   dg = dH u act'(g), du = dH act(g);  dX = [dg|du] W;  dW = [dg|du]^T X
 // The mathematics and the limits are stated in include/fp8gemm.h.
+//
+// Four products with one body (product() below): the two with W's rows pair each gate row with its up row in one lane, so
+// that the activation, or its gradient, is an epilogue; the other two read operands whose contraction runs along rows of
+// memory with LDS's transposing reads, so nothing is transposed in memory.  dg and du are rounded to bf16 once, between
+// the products, since the matrix cores take them so; g and u, formed again, and all sums stay in fp32.
+//
+// What bounds them: large sizes the matrix cores and what feeds them.  H of 4096 rows, I = 2048, K = 7168 takes 178 us,
+// 1.35 PFLOP/s (a library product with as many operations 183 us, the matrix instructions alone on the same data, from
+// registers, 143 us); its gradients 412 us, 1.17 PFLOP/s (a library's two products 489 us).  Middle sizes: how the tiles fill 256
+// CUs, and a tile's start and end (3 to 8 us); few rows: W's bytes, 1 row 10.6 us, 5.5 TB/s of them from HBM and the
+// memory-side cache.
 
 #include <algorithm>
 #include <type_traits>
@@ -452,6 +463,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES_PER_SIMD) void product_pair_kernel(
 // A workgroup has 8 output columns, whose 8 gate rows and 8 up rows of W are the 16 rows of one matrix-core
 // operand; X's rows are the other's.  Its 8 waves take the steps of K (64 values, a 128-byte line of a row) in turn, two on
 // their way each; their sums meet in LDS and are added in wave order.  With dH the sums' gradients go to `pre`.
+// Bound by W's bytes: I = 2048, K = 7168, us, 1 row 10.6, 8 rows 13.0.
 constexpr int kRowsWaves = 8, kRowsAhead = 2;
 
 __global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const GatedRowsArgs a) {
@@ -523,7 +535,7 @@ __global__ __launch_bounds__(kRowsWaves * 64, 2) void gated_rows_kernel(const Ga
     }
 }
 
-// ---- gradients of kept products: 8 values of a row a thread ---------------------------------------------
+// ---- gradients of kept products: 8 values of a row a thread, a pass at the rate of a copy ----------------
 __global__ __launch_bounds__(256) void gated_grad_kernel(const GatedGradArgs a) {
     const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (unit >= a.units) return;
@@ -551,6 +563,8 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(v4u* p, int64_t units) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += (int64_t)gridDim.x * 256) p[i] = (v4u){0, 0, 0, 0};
 }
 
+// A wave's part is 128 x 64 of the largest tile, 64 x 64 or 64 x 32 of the next, 32 x 32 of the smallest.  Larger tiles
+// bring less into LDS for a product; their rings are as long as LDS allows.  Measured, us a slice of 64 of K: kTiles.
 template <int KIND, bool LAG>
 using Tile256 = Tile<256, 256, 2, 4, 2, KIND, false>;
 template <int KIND, bool LAG>

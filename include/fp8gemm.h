@@ -33,15 +33,16 @@
  *   - Results are deterministic: the same inputs give the same bits, whatever the launch
  *     configuration's timing (split-K and stream-K partials are summed in a fixed K order).
  *     The launch configuration itself depends on the shape, the device's CU count and the CU
- *     cap, so a different cap (or stream-K turned off) may sum the same products in another
+ *     cap (for the gated block and its gradients, on whether rows start at 128-byte lines), so a different cap (or stream-K turned off) may sum the same products in another
  *     order, within the same tolerance.
  *   - Stream workspace: each stream (hipStreamPerThread: each host thread's, held until the
  *     process ends) has its own library-owned workspace (fp32 partial tiles
  *     and arrival counters, CUs x 512 KiB + 16 KiB on the stream's device).  It serves the
  *     K splits of decode-sized launches, the stream-K schedule of large dense launches (the
  *     256-row tiles left over after the last full round of tiles, shared out over every CU
- *     by K block) and the counts, ranks and scales of a dispatch of more than 8192 pairs, whose
- *     several launches stay together: of two threads' calls on one stream that use its
+ *     by K block), the K splits of the gated block and of its gradients, the rank-R products of
+ *     low-rank adapters, and the counts, ranks and scales of a dispatch of more than 8192 pairs.
+ *     The several launches of a call stay together: of two threads' calls on one stream that use its
  *     workspace, one enqueues all its launches before the other enqueues its first.
  *     It is allocated once, at full size, by fp8gemm_prepare_stream or by the
  *     first call on the stream whose launch needs it (one hipMalloc pair and one blocking
@@ -59,7 +60,8 @@
  *     flight.
  *   - Environment (read at each call; for experiments and tests, not needed in normal use):
  *     FP8GEMM_FORCE_CONFIG forces a table entry (BMxBN:WMxWN:STAGES:SPLIT for the tiled kernel,
- *     stream:MT:W:JN:KP:PF:SPLIT for the masked decode kernel), FP8GEMM_STREAMK=0 or 1 turns
+ *     stream:MT:W:JN:KP:PF:SPLIT for the masked decode kernel, product:BMxBN:SPLIT or
+ *     product:BMxBNxRING:SPLIT for the gated block and its gradients), FP8GEMM_STREAMK=0 or 1 turns
  *     stream-K off, or on wherever dense 256-row tiles leave a partial round, and FP8GEMM_LOG
  *     prints each launch configuration to stderr.  FP8GEMM_HIPRTC names the hipRTC library for
  *     the run-time specialised kernels (default $ROCM_PATH/lib/libhiprtc.so.7).
@@ -359,7 +361,7 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
  *   dX [M][K] = bf16(dpre W),  dW [2I][K] = bf16(dpre^T X), sums in fp32 of the rounded dpre.
  * With `pre` (as fp8gemm_gated_ffn wrote it) g and u are its bf16 values; with pre NULL they are
  * formed again from X and W and not rounded.  dpre is written (a workspace, and the gradient with
- * respect to the two projections); it may be `pre` itself.  dX or dW NULL: not formed; X may be
+ * respect to the two projections); it may be `pre` itself, and no output overlaps anything else.  dX or dW NULL: not formed; X may be
  * NULL with `pre` and without dW, W with `pre` and without dX.  M == 0 sets dW to zeros.  Sizes,
  * alignment and workspace as above. */
 int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, const void* pre, void* dpre, void* dX, void* dW,
@@ -371,22 +373,24 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
  *   X [T][ldx], Y [T][ldy], out [T][ldo] bf16, rows of K, N and N values (strides in values, multiples
  *   of 8); A [L][R][K], B [L][N][R] bf16; ids [T] int32; scales [L] fp32 or NULL (ones).
  * Sums in fp32; A x enters the second product with 16 bits.  An adapter of smaller rank is padded with
- * zeros.  out may be Y itself (rows without an adapter are then not written).  An id of L or more
- * counts as none and flags FP8GEMM_DEVERR_BAD_INDEX.
+ * zeros.  out may be Y itself, with its stride (rows without an adapter are then not written), and
+ * overlaps nothing else.  An id of L or more counts as none and flags FP8GEMM_DEVERR_BAD_INDEX.
  *   order [T] int32 or NULL: a permutation of the rows that brings those of an adapter together.  It
  *   changes no result, only the time of a batch in which neighbours have different adapters: rows are
- *   taken 16 at a time (32 or 64 in batches of more than 512), each adapter among them in turn.  An
+ *   taken one at a time in small batches, else up to 64 together, each adapter among them in turn.  An
  *   entry outside [0, T) is left out and flags FP8GEMM_DEVERR_BAD_INDEX; rows that it does not name are
  *   not written, with repeated entries rows are unspecified.
  * R: a positive multiple of 8, at most 128; K, N: multiples of 8, at most 2^20; X, Y, A, B, out 16-byte
- * aligned.  Uses the stream's workspace (see fp8gemm_prepare_stream). */
+ * aligned.  All but small adapters in small batches use the stream's workspace (see
+ * fp8gemm_prepare_stream). */
 int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B, const int32_t* ids, const int32_t* order,
                      const float* scales, void* out, int64_t T, int32_t L, int32_t R, int64_t K, int64_t N, int64_t ldx,
                      int64_t ldy, int64_t ldo, void* stream);
 
 /* Device-side precondition flags (bits of the device error word). */
 #define FP8GEMM_DEVERR_BAD_INDEX 1 /* contiguous: an m_indices entry outside [-1, G) or off its block's group;
-                                      combine: a row_map entry of R or more */
+                                      combine: a row_map entry of R or more; lora_add: an id of L or more, an
+                                      order entry outside [0, T) */
 #define FP8GEMM_DEVERR_BAD_COUNT 2 /* masked GEMM or quantiser: a masked_m entry outside [0, M_max];
                                       dispatch: an expert's rows exceed the capacity */
 
