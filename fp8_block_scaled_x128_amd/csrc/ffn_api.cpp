@@ -65,9 +65,8 @@ bool loads_count(int64_t tiles, const TileShape& t, int64_t slices) { return til
 
 // Tile and K splits of a product with `rows` x `cols` results (gated: cols pairs) and `slices` slices of 64 of K:
 // the least of the times that the measured slices (kTiles) give for the rounds of workgroups that a CU takes, where
-// those take longer than reading both operands and writing the result.  Over 26 sizes of each product (17 to 4096 rows, I 64 to 2048, K
-// 128 to 7168) the choice is within 7% of the best of all tiles with 1 to 16 splits, but for three that are 13 to 17%
-// off (exchanges of many partials: 256 rows, 2048, 7168; dX of 3565 and 3808 rows, K about 400).
+// those take longer than reading both operands and writing the result.  Over 25 sizes of H and of dX (17 to 4096 rows,
+// I 64 to 2048, K 128 to 7168) the choice is within 5% of the best of all tiles with 1 to 16 splits.
 Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus, bool off) {
     const bool gated = kind == kGated || kind == kGatedBack;
     Choice best{0, 1, 1e30};
@@ -119,7 +118,8 @@ double rounds_of(int64_t n, double L, int64_t n2, double L2, int64_t slots) {
 // dX and dW as one launch, if that is quicker than one after the other (the second's units fill the CUs that the
 // first's last ones leave, but L2 serves both): a shape for both, and the splits of each.  Measured, one after the
 // other and together, us: M = 1023, I = 1416, K = 2056 55 and 47; 1024, 2048, 7168 138 and 120; 905, 336, 456 17.8 and
-// 13.1; 77, 512, 1536 12.7 and 11.4; but 256, 2048, 7168 62 and 73, 4096, 2048, 7168 417 and 420.
+// 13.1; 77, 512, 1536 12.7 and 11.4; but 256, 2048, 7168 62 and 73, 4096, 2048, 7168 417 and 420.  Over 35 sizes the
+// choice is 2% from the best of one shape for both on average, 17% at most (64, 2048, 7168 from cold memory).
 bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx, Choice* cw) {
     if (forced(cx, false)) {
         *cw = *cx;
