@@ -8,6 +8,7 @@ nested loop (the K loop, the split-K sums) spills to scratch memory.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import re
 import shutil
@@ -117,14 +118,18 @@ def build(verbose: bool = False) -> str:
     try:
         with open(os.path.join(gen, "fp8gemm_jit_sources.inc"), "w") as f:
             f.write(jit_sources_inc())
-        _run([HIPCC, "--offload-arch=" + ARCH] + COMMON + DEVICE_FLAGS + ["-I", gen, "-shared", "-o", tmp] +
-             SOURCES + ["-ldl"])
-        with tempfile.TemporaryDirectory() as td:
+        hipcc = [HIPCC, "--offload-arch=" + ARCH] + COMMON + DEVICE_FLAGS
+        with tempfile.TemporaryDirectory() as td, concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            def out(src, ext):
+                return os.path.join(td, os.path.basename(src) + ext)
+            jobs = [pool.submit(_run, hipcc + ["-I", gen, "-c", "-o", out(src, ".o"), src]) for src in SOURCES]
+            jobs += [pool.submit(_run, hipcc + ["--cuda-device-only", "-S", "-o", out(src, ".s"), src]) for src in DEVICE_SOURCES]
+            for job in jobs:
+                job.result()
             for src in DEVICE_SOURCES:
-                asm = os.path.join(td, os.path.basename(src) + ".s")
-                _run([HIPCC, "--offload-arch=" + ARCH] + COMMON + DEVICE_FLAGS +
-                     ["--cuda-device-only", "-S", "-o", asm, src])
-                check_isa(open(asm).read())
+                with open(out(src, ".s")) as f:
+                    check_isa(f.read())
+            _run(hipcc + ["-shared", "-o", tmp] + [out(src, ".o") for src in SOURCES] + ["-ldl"])
         os.replace(tmp, LIB)
         _run([HIPCC, "--offload-arch=" + ARCH] + COMMON + DEVICE_FLAGS + ["-shared", "-o", tmp, PROBE_SOURCE])
         os.replace(tmp, PROBE_LIB)

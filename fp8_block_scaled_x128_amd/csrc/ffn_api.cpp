@@ -76,6 +76,7 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus,
         const TileShape& t = kTiles[i];
         const int64_t width = gated ? t.bn / 2 : t.bn;
         const int64_t tiles = ((rows + t.bm - 1) / t.bm) * ((cols + width - 1) / width);
+        if (tiles > kMaxUnits) continue;
         const int64_t slots = (int64_t)cus * t.per_cu;
         const double slow = slower(t, kind, off && loads_count(tiles, t, slices));
         for (int64_t s = 1; s <= 16 && (s == 1 || (s * 2 <= slices && tiles * s <= slots)); ++s) {
@@ -135,6 +136,7 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
         const TileShape& t = kTiles[i];
         auto tiles = [&](const ProductArgs& a) { return (((int64_t)a.rows + t.bm - 1) / t.bm) * (((int64_t)a.cols + t.bn - 1) / t.bn); };
         const int64_t tx = tiles(x), tw = tiles(w), slots = (int64_t)cus * t.per_cu;
+        if (tx + tw > kMaxUnits) continue;
         for (int64_t px = 1; px <= 8 && (px == 1 || (px * 2 <= sx && px * tx <= slots)); px *= 2)
             for (int64_t pw = 1; pw <= 8 && (pw == 1 || (pw * 2 <= sw && pw * tw <= slots)); pw *= 2) {
                 const double lx = ((double)((sx + px - 1) / px) + t.ends) * slower(t, kTimesW, off);

@@ -164,6 +164,8 @@ def _workspace_limits(so):
     assert r.hip.record_allocations() == before + 2
     assert r.count(r.lora, 0x10, T=140000, R=128, K=64, N=64) == 4        # 128 MiB hold 131072 rows of 128 and their halves
     assert r.count(r.lora, 0x10, T=70000, L=5000, R=8, K=64, N=64) == 4   # tiles of 16 rows, 4096 a launch
+    assert r.count(r.gated, 0x10, M=1 << 29, I=8, K=8) == 1                # few tiles in one launch, of as many rows as it takes
+    assert r.count(r.backward, 0x10, M=1 << 29, I=8, K=8) in (2, 3)
     os.environ["FP8GEMM_FORCE_CONFIG"] = "product:256x256:2"
     n = len(r.launches())
     assert r.gated(0x10, M=4096, I=4096) == UNSUPPORTED
