@@ -111,8 +111,11 @@ double rounds_of(int64_t n, double L, int64_t n2, double L2, int64_t slots) {
     // every place has time for at least (mean - a) / L2 of the second, rounded down
     const double mean = ((double)n * L + (double)n2 * L2) / (double)slots;
     for (int64_t k = std::max<int64_t>(1, (int64_t)((mean - a) / L2));; ++k) {
-        const double t = a + (double)k * L2;
-        if ((slots - late) * k + (t > b ? late * (int64_t)((t - b) / L2) : 0) >= n2) return std::max(L, 0.5 * (mean + std::max(t, b)));
+        const double t = a + (double)k * L2;                  // the early places' k-th ends; the late ones' last until then
+        const int64_t j = t > b ? (int64_t)((t - b) / L2) : 0;
+        const double tj = b + (double)j * L2;
+        if (j > 0 && tj > t - L2 && (slots - late) * (k - 1) + late * j >= n2) return std::max(L, 0.5 * (mean + tj));
+        if ((slots - late) * k + late * j >= n2) return std::max(L, 0.5 * (mean + std::max(t, b)));
     }
 }
 
