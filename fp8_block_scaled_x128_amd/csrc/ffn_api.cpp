@@ -37,7 +37,9 @@ struct Choice {
 bool forced(Choice* c, bool gated) {
     const char* s = std::getenv("FP8GEMM_FORCE_CONFIG");
     int bm, bn, split, ring = 0;
-    if (!s || (std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3 && std::sscanf(s, "product:%dx%dx%d:%d", &bm, &bn, &ring, &split) != 4)) return false;
+    if (!s || (std::sscanf(s, "product:%dx%d:%d", &bm, &bn, &split) != 3 &&
+               std::sscanf(s, "product:%dx%dx%d:%d", &bm, &bn, &ring, &split) != 4))
+        return false;
     for (int i = 0; i < (gated ? kGatedShapes : kTileShapes); ++i)
         if (kTiles[i].bm == bm && kTiles[i].bn == bn && (ring == 0 || kTiles[i].ring == ring)) {
             *c = {i, std::max(1, split), 0.0};
@@ -84,7 +86,8 @@ Choice choose(int64_t rows, int64_t cols, int64_t slices, Product kind, int cus,
             if (s > 1 && (slices + per - 1) / per != s) continue;
             const int64_t units = tiles * s, last = units % slots;
             const double rounds = (double)(units / slots) * t.shared + (last == 0 ? 0.0 : slice_us(t, last, cus));
-            const double cost = std::max(((double)per + t.ends) * rounds * slow, bytes) + (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
+            const double cost = std::max(((double)per + t.ends) * rounds * slow, bytes) +
+                                (s > 1 ? t.exchange + t.exchange_split * (double)s : 0.0);
             if (cost < best.us) best = {i, (int)s, cost};
         }
     }
@@ -351,7 +354,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     if (st == FP8GEMM_OK) st = share_workspace({{&ax, cx}, {&aw, cw}}, s, &hold);
     if (st != FP8GEMM_OK) return st;
     host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lld split=%lld dW tile=%lldx%lld split=%lld",
-                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, kTiles[cx.shape].ring, cx.splits, dW ? kTiles[cw.shape].bm : 0, kTiles[cw.shape].ring, cw.splits});
+                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, kTiles[cx.shape].ring, cx.splits,
+                     dW ? kTiles[cw.shape].bm : 0, kTiles[cw.shape].ring, cw.splits});
     if (pre) {
         GatedGradArgs g{};
         g.pre = static_cast<const uint16_t*>(pre);

@@ -157,8 +157,11 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     const int tail = a.K - (a.slices - 1) * 64;              // values of the last slice
     const int tail_at = tail < 64 ? a.slices - 1 - s0 : -1;  // this unit's slice that is not whole
     // whether chunk c of row r comes with the next slice (tiles, and a tile's 16 rows, start at multiples of 8)
-    auto late_p = [&](int r, int c) { return T::LAG && !T::PT && c + (((int)(reinterpret_cast<uintptr_t>(a.P) >> 4) + r * (a.ldp >> 3)) & 7) >= 8; };
-    auto late_q = [&](int r, int c) { return T::LAG && !T::QT && c + (((int)(reinterpret_cast<uintptr_t>(a.Q) >> 4) + r * (a.ldq >> 3)) & 7) >= 8; };
+    auto late = [](const uint16_t* p, int ld, int r, int c) {
+        return c + (int)(((uint32_t)(reinterpret_cast<uintptr_t>(p) >> 4) + (uint32_t)r * (uint32_t)(ld >> 3)) & 7) >= 8;
+    };
+    auto late_p = [&](int r, int c) { return T::LAG && !T::PT && late(a.P, a.ldp, r, c); };
+    auto late_q = [&](int r, int c) { return T::LAG && !T::QT && late(a.Q, a.ldq, r, c); };
 
     // ---- what each lane loads: byte offsets from a line's bases ----------------------------------------------
     // rows and columns past the end repeat the last (their results are not stored), and so do slices and values
@@ -176,7 +179,8 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     auto q_off = [&](int q, int line) -> uint32_t {
         const int r = OpQ::row(wave, q, lane), c = OpQ::chunk(r, lane);
         if constexpr (T::QT) {
-            return (uint32_t)min(r, values(T::LAG ? min(line, nks - 1) : line) - 1) * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(n0 + 8 * c, a.cols - 8));
+            const int there = values(T::LAG ? min(line, nks - 1) : line);
+            return (uint32_t)min(r, there - 1) * (uint32_t)(2 * a.ldq) + (uint32_t)(2 * min(n0 + 8 * c, a.cols - 8));
         } else {
             // gate and up rows in turn, 16 each, so that a lane ends with a pair of them (up: qs below)
             const int n = min(((r >> 5) << 4) + (r & 15), a.cols - 1 - n0);
@@ -198,7 +202,8 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
         const uint32_t st = smem_base + (uint32_t)((i % STAGES) * T::STAGE_BYTES);
         if (x < OpQ::LOADS) {
             const int l = wave * OpQ::LOADS + x;
-            dma_x4(st + l * 1024, uniform_ptr(qbase + (T::LAG && T::QT ? min(i, nks - 1) : i) * qstep + (T::GATED && (l >> 1 & 1) ? up : 0)), qoff[x]);
+            const uint16_t* from = qbase + (T::LAG && T::QT ? min(i, nks - 1) : i) * qstep + (T::GATED && (l >> 1 & 1) ? up : 0);
+            dma_x4(st + l * 1024, uniform_ptr(from), qoff[x]);
         } else {
             const int l = wave * OpP::LOADS + x - OpQ::LOADS;
             dma_x4(st + T::P_OFF + l * 1024, uniform_ptr(pbase + i * pstep), poff[x - OpQ::LOADS]);
@@ -216,14 +221,15 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
     // zeros in both operands for the values of k that the last slice does not have
     auto clear_tail = [&](int i) {
         const int here = (i % STAGES) * T::STAGE_BYTES, next = ((i + lag) % STAGES) * T::STAGE_BYTES;
-        auto clear = [&](int part, int rows, bool turned, int row_bytes, auto late) {
+        auto clear = [&](int part, int rows, bool turned, int row_bytes, auto comes_late) {
             if (turned) {
                 for (int o = tail * row_bytes + tid * 16; o < 64 * row_bytes; o += T::NT * 16)
                     *reinterpret_cast<v4u*>(smem + here + part + o) = (v4u){0, 0, 0, 0};
             } else {
                 for (int x = tid; x < rows * 8; x += T::NT) {
                     const int r = x >> 3, c = x & 7;
-                    if (c * 8 >= tail) *reinterpret_cast<v4u*>(smem + (late(r, c) ? next : here) + part + r * 128 + ((c ^ swz(r)) << 4)) = (v4u){0, 0, 0, 0};
+                    uint8_t* at = smem + (comes_late(r, c) ? next : here) + part + r * 128 + ((c ^ swz(r)) << 4);
+                    if (c * 8 >= tail) *reinterpret_cast<v4u*>(at) = (v4u){0, 0, 0, 0};
                 }
             }
         };

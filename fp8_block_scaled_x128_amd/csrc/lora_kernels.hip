@@ -1,11 +1,18 @@
 // lora_kernels.hip -- gfx950 kernels of low-rank adapters of many requests beside a shared projection:
 //   out[t] = bf16(Y[t] + s[a] * B[a] (A[a] x[t])),  a = ids[t] the adapter of row t, or none.
-// Two launches: the rank-R products A x, in fp32 through the workspace, then B's product, the sum and the store.
+// Three forms, by the rows' number and the adapters' size (the host's rules have both sides measured):
+//   a workgroup a row, both products in one launch: small adapters in small batches.  Bound by the launch and by what
+//     one CU reads: 45 rows, R = 8, 1544 to 2112, 5.0 us.
+//   two launches, 1 to 16 places a workgroup: the rank-R products A x, in fp32 through the workspace, then B's product,
+//     the sum and the store.  Bound by two launches, then the adapters' bytes: 1 row 6.9 us, 256 rows of 64 adapters,
+//     R = 16, 7168 to 4096, 15.0 us.
+//   two launches, 64 places a workgroup, operands through LDS: prefill.  Bound by HBM: 8192 rows of 8 adapters, R = 32,
+//     7168 to 4096, 61 us, 4.2 TB/s; with large ranks by A's and B's way through L2: 2000 rows, R = 128, 2048 to 7168, 37 us.
 //
-// Both take the rows by tiles of 16 places (places are rows, or positions in the order the caller gives) and go
-// through the adapters that a tile's rows have, one after the other; matrix-core columns of rows with another
-// adapter are left out of the results.  So any mix of rows is right, and one whose neighbours share an adapter
-// reads each of its matrices once per tile.
+// Places are rows, or positions in the order the caller gives.  A tile of them goes through the adapters that its rows
+// have, one after the other; matrix-core columns of rows with another adapter are left out of the results.  So any mix
+// of rows is right, and one whose neighbours share an adapter reads each of its matrices once per tile.  A x stays in
+// 32 bits until the second product, which takes it as two bf16 halves: one rounding of the result, as in the formula.
 
 #include <type_traits>
 
@@ -72,9 +79,10 @@ __device__ __forceinline__ int64_t row_of(int64_t row, int from) {
 
 constexpr int kDownWaves = 8;
 
-// A x for 16 places a workgroup, or fewer, and 16 RT of the rank; AHEAD: loads of 32 values of K on their way.  The waves share the split's steps of 64 values of K, and their sums meet in LDS and
-// are added in wave order; where the places have three adapters or more, each wave has adapters of its own and all
-// of the steps, and adds the eight waves' sums in the same order.
+// A x for 16 places a workgroup, or fewer, and 16 RT of the rank; AHEAD: loads of 32 values of K on their way.  The
+// waves share the split's steps of 64 values of K, and their sums meet in LDS and are added in wave order; where the
+// places have three adapters or more, each wave has adapters of its own and all of the steps, and adds the eight
+// waves' sums in the same order.
 template <int RT, int AHEAD>
 __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_down_kernel(const LoraArgs a) {
     __shared__ v4f red[kDownWaves][RT][64];
@@ -120,7 +128,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_down_kernel(const Lor
             v4u w[RT], x;
         };
         Half ring[AHEAD];
-        // the u-th half of this wave: steps 4 apart, for each of the four waves in turn where the wave has all of them
+        // the u-th half of this wave: steps 8 apart, for each of the eight waves in turn where the wave has all of them
         const int halves = 2 * rounds * (apart ? kDownWaves : 1);
         auto load = [&](Half& f, int u) {
             if (u >= halves) return;
@@ -186,7 +194,9 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_down_kernel(const Lor
 
 // Sum over groups of 1 << shift lanes, at most 16.
 __device__ __forceinline__ float sum_of_lanes(float d, int shift) {
-    auto moved = [](float x, auto ctrl) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true)); };
+    auto moved = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
     if (shift > 0) d += moved(d, std::integral_constant<int, 0xB1>{});      // lane ^ 1
     if (shift > 1) d += moved(d, std::integral_constant<int, 0x4E>{});      // lane ^ 2
     if (shift > 2) d += moved(d, std::integral_constant<int, 0x141>{});     // 7 - lane of 8: the other four
@@ -300,8 +310,9 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
 // 64 values of K of the 64 rows of X and the adapter's rows of A pass through a ring in LDS, 128-byte rows with
 // 16-byte chunk c of row r at c ^ swz(r) (as in the FP8 kernel); a wave has 16 places and all of the rank.
 // A tile of several adapters is shared by two workgroups (apart = 1), that have them in turn: else it would take as many
-// times as long as the others.  The second ones come first in the grid, where most of them end at once.  The last of a tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum
-// is within 2^-17 of it (partials are written and read past the L2s of the XCDs, with agent-coherent accesses).
+// times as long as the others.  The second ones come first in the grid, where most of them end at once.  The last of a
+// tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum is within 2^-17
+// of it (partials are written and read past the L2s of the XCDs, with agent-coherent accesses).
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2); }
 __device__ __forceinline__ void dma_far(uint32_t lds_base, const void* p) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds_base), "v"(p) : "memory");
