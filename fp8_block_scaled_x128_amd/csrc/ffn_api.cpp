@@ -22,6 +22,7 @@ namespace {
 
 constexpr int64_t kMaxBytes = int64_t(1) << 40;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;         // values of a row of X, W or dpre: a tile stays below 2^31 bytes
+constexpr size_t kCounters = 4096;                      // of a stream's workspace
 constexpr int64_t kMaxUnits = int64_t(1) << 22;         // workgroups of a launch: below 2^32 threads
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -196,7 +197,8 @@ int share_workspace(std::initializer_list<std::pair<ProductArgs*, Choice>> produ
     if (tiles == 0) return FP8GEMM_OK;
     float* ws = nullptr;
     int32_t* counters = nullptr;
-    const int st = host_stream_workspace(stream, floats * sizeof(float), tiles, &ws, &counters,
+    const size_t spread = std::max<size_t>(1, std::min<size_t>(32, kCounters / tiles));
+    const int st = host_stream_workspace(stream, floats * sizeof(float), tiles * spread, &ws, &counters,
                                          hold->owns_lock() ? nullptr : hold);
     if (st != FP8GEMM_OK) return st;
     for (const auto& p : products) {
@@ -204,7 +206,8 @@ int share_workspace(std::initializer_list<std::pair<ProductArgs*, Choice>> produ
         const size_t n = (size_t)p.first->tiles_m * p.first->tiles_n;
         p.first->ws = ws;
         p.first->counters = counters;
-        counters += n;
+        p.first->spread = (int32_t)spread;
+        counters += n * spread;
         ws += n * p.first->splits * kTiles[p.second.shape].bm * kTiles[p.second.shape].bn;
     }
     return FP8GEMM_OK;

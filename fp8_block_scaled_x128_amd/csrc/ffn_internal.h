@@ -27,7 +27,8 @@ struct ProductArgs {
     uint16_t* out;              // [rows][cols]
     uint16_t* pre;              // kGated: [rows][2 cols] or null; kGatedBack: [rows][2 cols]
     float* ws;                  // K splits: partial tiles [tile][split][BM * BN]
-    int32_t* counters;          // K splits: arrivals by tile, zero between launches
+    int32_t* counters;          // K splits: arrivals by tile, `spread` from one to the next, zero between launches
+    int32_t spread;
     int32_t rows, cols;         // of out (kGated, kGatedBack: cols = I)
     int32_t K;                  // contraction
     int32_t ldp, ldq;           // values from one row of memory to the next

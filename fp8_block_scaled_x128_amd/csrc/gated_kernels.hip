@@ -349,10 +349,10 @@ __device__ __forceinline__ void product(const ProductArgs& a, int block, int blo
         wait_vmcnt<0>();
         __syncthreads();
         if (tid == 0) {
-            const int old = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const int old = __hip_atomic_fetch_add(a.counters + tile * (uint32_t)a.spread, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             s_flag = old == a.splits - 1;
             if (old == a.splits - 1)
-                __hip_atomic_store(a.counters + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(a.counters + tile * (uint32_t)a.spread, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         __syncthreads();
         if (!s_flag) return;
