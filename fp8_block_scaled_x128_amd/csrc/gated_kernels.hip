@@ -43,13 +43,14 @@ __device__ __forceinline__ float logistic(float x, bool gelu) {
 }
 __device__ __forceinline__ float activation(float x, bool gelu) { return x * logistic(x, gelu); }
 // act(x) and act'(x) = s + x s (1 - s) z'(x).  The second term vanishes long before |x| = 64; taken at the
-// bounded x it cannot overflow.
+// bounded x it cannot overflow.  Both bounds, this one and the exponential's, turn NaN into a number: act(x) has it
+// again from its factor x, act'(x) is given it back.
 __device__ __forceinline__ float activation_grad(float x, bool gelu, float* value) {
     const float s = logistic(x, gelu);
     const float xb = __builtin_amdgcn_fmed3f(x, -64.0f, 64.0f);
     const float dz = gelu ? kGeluA * __builtin_fmaf(3.0f * kGeluB * xb, xb, 1.0f) : 1.0f;
     *value = x * s;
-    return __builtin_fmaf(xb * s * (1.0f - s), dz, s);
+    return __builtin_isnan(x) ? x : __builtin_fmaf(xb * s * (1.0f - s), dz, s);
 }
 
 __device__ __forceinline__ v2u pack4(const v4f& v) { return (v2u){pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)}; }

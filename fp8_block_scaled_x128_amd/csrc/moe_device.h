@@ -46,7 +46,7 @@ __device__ __forceinline__ void wave_sync() {
 
 // e^x within 2 units in the last place, subnormal results included: x log2(e) = n + f with n a
 // whole number and f formed with the low part of log2(e), then 2^f by the hardware and n by ldexp.
-// Outside [-120, 100] the result is 0 or infinity all the same.
+// Outside [-120, 100] the result is 0 or infinity all the same; NaN is taken as -120.
 __device__ __forceinline__ float exp_f32(float x) {
     x = __builtin_amdgcn_fmed3f(x, -120.0f, 100.0f);
     const float n = __builtin_rintf(x * 1.44269504088896341f);
