@@ -61,13 +61,22 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Four values as bf16 halves: the values rounded, and what that leaves (nothing, where the first is infinite).
+// Four values as bf16 halves: a value's first 8 bits, and what they leave of it, rounded, together within 2^-16 of it.
+// The first is cut off, not rounded, so that both have the value's sign, and the second is 2^-133, the least bf16, where
+// nothing is left: B's infinities then give the same infinity with both, as with the value, and zero times infinity is
+// left to zeros (and to values below 2^-133).  Of an infinity nothing is left either (fmed3 of NaN and two numbers is the
+// smaller number); NaN, as sums give it, keeps its first bits.
 __device__ __forceinline__ void halves_of(const v4f& v, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+    float rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float first = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
+        rest[e] = __builtin_copysignf(__builtin_amdgcn_fmed3f(__builtin_fabsf(v[e] - first), 0x1p-133f, __builtin_fabsf(first)), v[e]);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-        const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xFFFF0000u);
-        lo[e] = pack_bf16x2(__builtin_isinf(h0) ? 0.0f : v[2 * e] - h0, __builtin_isinf(h1) ? 0.0f : v[2 * e + 1] - h1);
+        hi[e] = __float_as_uint(v[2 * e]) >> 16 | (__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
+        lo[e] = pack_bf16x2(rest[2 * e], rest[2 * e + 1]);
     }
 }
 
@@ -311,7 +320,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 2) void lora_row_kernel(const Lora
 // 16-byte chunk c of row r at c ^ swz(r) (as in the FP8 kernel); a wave has 16 places and all of the rank.
 // A tile of several adapters is shared by two workgroups (apart = 1), that have them in turn: else it would take as many
 // times as long as the others.  The second ones come first in the grid, where most of them end at once.  The last of a
-// tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum is within 2^-17
+// tile's splits to arrive adds their sums in split order and leaves A x as two bf16 halves, whose sum is within 2^-16
 // of it (partials are written and read past the L2s of the XCDs, with agent-coherent accesses).
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2); }
 __device__ __forceinline__ void dma_far(uint32_t lds_base, const void* p) {
@@ -479,7 +488,7 @@ __device__ __forceinline__ void add_lines(const LoraArgs& a, const float* line, 
 
 // The second product for 16 places a workgroup, or fewer.  RS: matrix-core steps of the rank.  A workgroup takes
 // `chunks` runs of 256 columns, a wave 64 of each; its results become 128-byte lines of rows through LDS.
-// A x enters as two bf16 halves, whose sum is within 2^-17 of it, formed in LDS from the splits' sums.  RS = 0: a
+// A x enters as two bf16 halves, whose sum is within 2^-16 of it, formed in LDS from the splits' sums.  RS = 0: a
 // rank of 16 at most in one step, the high halves in the step's first 16 values and the low ones in its last, against
 // the same 16 values of B.  Else steps of 32 values of the rank, twice, with the high halves and with the low ones.
 template <int RS>

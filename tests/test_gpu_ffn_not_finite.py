@@ -1,5 +1,6 @@
-"""GPU: NaN in the gate of the gated block's gradients, in every kernel, against the same call without it: what it must not
-reach keeps its bits."""
+"""GPU: NaN in the gate of the gated block's gradients, and infinities in an adapter's second matrix, in every kernel.
+
+Both are compared with the same call without such values: what they must not reach keeps its bits."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,40 @@ def test_nan_gate_reaches_its_gradient(tile, M, I, K, act, monkeypatch):
     the_same_but(dp, dpre, one)
     the_same_but(dx, dX, one.any(1)[:, None].expand(M, K))
     the_same_but(dw, dW, rows)
+
+
+# by row, a few rows a workgroup, 64 rows; ranks of every kernel
+@pytest.mark.parametrize("T,L,R,K,N", [(20, 4, 24, 264, 136), (40, 4, 16, 2568, 136), (40, 4, 16, 4168, 136), (70, 4, 104, 1200, 136),
+                                       (40, 4, 32, 4168, 136), (40, 4, 56, 4168, 136), (1100, 4, 16, 200, 264), (1100, 4, 32, 200, 136),
+                                       (700, 3, 56, 136, 136), (700, 3, 72, 136, 136), (700, 3, 128, 136, 136)])
+def test_infinities_of_b(T, L, R, K, N):
+    """An infinite value of B gives the infinity of the formula, with the sign of B, A x and the scale, whatever A x is:
+    any value, one that bf16 holds exactly, one near the least; and NaN where A x is zero."""
+    X, Y = normal(T, T, K), normal(T + 1, T, N)
+    A, B = normal(T + 2, L, R, K, scale=K ** -0.5), normal(T + 3, L, N, R, scale=R ** -0.5)
+    ids = (torch.arange(T, device="cuda") % 3).int()
+    ids[[2, 4, 7, 10]] = 1
+    scales = torch.tensor([0.5, 1.5, -2.0, 1.0][:L], device="cuda")
+    A[1, :, 0] = 0.5
+    X[[2, 4, 7]] = 0.0
+    X[2, 0], X[7, 0] = 3.0, -2.0 ** -100                        # A x of 1.5, 0 and -2^-101
+    for sign in (1.0, -1.0):
+        scales[1] = 1.5 * sign
+        want = fg.lora_add(Y, X, A, B, ids, scales)
+        n = torch.arange(N, device="cuda")
+        r = n % R
+        at = torch.tensor([float("inf"), -float("inf"), 0.0], device="cuda")[n % 3]
+        inf = at != 0
+        bad = B.clone()
+        bad[1, n[inf], r[inf]] = at[inf].to(bf16)
+        got = fg.lora_add(Y, X, A, bad, ids, scales)
+        mine = ids == 1
+        assert torch.equal(got[~mine], want[~mine]) and torch.equal(got[:, ~inf], want[:, ~inf])
+        v = (X[mine].double() @ A[1].double().t())[:, r[inf]]
+        sure = (v == 0) | (v.abs() > 2.0 ** -12) | (v.abs() == 2.0 ** -101)      # fp32 sums keep the sign of these
+        assert sure.float().mean() > 0.99 and (v == 0).any() and (v.abs() == 2.0 ** -101).any()
+        ref = v * at[inf].double() * sign                      # zero times infinity is NaN
+        res = got[mine][:, inf].double()
+        assert torch.equal(res[sure].isnan(), ref[sure].isnan())
+        there = sure & ~ref.isnan()
+        assert torch.equal(res[there], ref[there])
