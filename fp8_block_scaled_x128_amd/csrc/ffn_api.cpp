@@ -136,7 +136,7 @@ bool choose_pair(const ProductArgs& x, const ProductArgs& w, int cus, Choice* cx
     const int64_t sx = (x.K + kSliceK - 1) / kSliceK, sw = (w.K + kSliceK - 1) / kSliceK;
     const double bytes = (128e-6 * ((double)sx * (double)(x.rows + x.cols) + (double)sw * (double)(w.rows + w.cols)) +
                           2e-6 * ((double)x.rows * (double)x.cols + (double)w.rows * (double)w.cols)) / 5.2;
-    const bool off = off_the_lines(x, kTimesW);
+    const bool off = off_the_lines(x, kTimesW, true);
     double least = cx->us + cw->us + 3.5;
     bool pair = false;
     for (int i = 0; i < kTileShapes; ++i) {
@@ -173,7 +173,7 @@ int arrange(ProductArgs* a, Choice* c, Product kind) {
     a->per_split = (a->slices + c->splits - 1) / c->splits;
     a->splits = c->splits = (a->slices + a->per_split - 1) / a->per_split;       // none without a slice
     if (tm > kMaxUnits / tn || tm * tn > kMaxUnits / a->splits) return FP8GEMM_ERR_UNSUPPORTED;
-    a->lag = t.ring >= 4 && off_the_lines(*a, kind) && (kind == kTimesW || loads_count(tm * tn, t, a->slices));
+    a->lag = t.ring >= 4 && off_the_lines(*a, kind, false) && (kind == kTimesW || loads_count(tm * tn, t, a->slices));
     a->tiles_m = (int32_t)tm;
     a->tiles_n = (int32_t)tn;
     a->group_m = (int32_t)std::min<int64_t>(tm, 8);
@@ -271,7 +271,7 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     a.cols = (int32_t)I;
     a.K = a.ldp = a.ldq = (int32_t)K;
     a.gelu = act == FP8GEMM_ACT_GELU_TANH;
-    c = choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, d.cus, off_the_lines(a, kGated));
+    c = choose(M, I, (K + kSliceK - 1) / kSliceK, kGated, d.cus, off_the_lines(a, kGated, true));
     st = arrange(&a, &c, kGated);
     if (st != FP8GEMM_OK) return st;
     std::unique_lock<std::mutex> hold;
@@ -324,7 +324,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ap.cols = (int32_t)I;
         ap.K = ap.ldp = ap.ldq = (int32_t)K;
         ap.gelu = act == FP8GEMM_ACT_GELU_TANH;
-        cp = choose(M, I, slices(K), kGatedBack, d.cus, off_the_lines(ap, kGatedBack));
+        cp = choose(M, I, slices(K), kGatedBack, d.cus, off_the_lines(ap, kGatedBack, true));
         st = arrange(&ap, &cp, kGatedBack);
         if (st != FP8GEMM_OK) return st;
     }
@@ -335,7 +335,7 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
         ax.rows = (int32_t)M;
         ax.cols = ax.ldq = (int32_t)K;
         ax.K = ax.ldp = (int32_t)(2 * I);
-        cx = choose(M, K, slices(2 * I), kTimesW, d.cus, off_the_lines(ax, kTimesW));
+        cx = choose(M, K, slices(2 * I), kTimesW, d.cus, off_the_lines(ax, kTimesW, true));
     }
     if (dW) {
         aw.P = static_cast<const uint16_t*>(dpre);

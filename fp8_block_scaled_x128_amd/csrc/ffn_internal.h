@@ -41,9 +41,11 @@ struct ProductArgs {
     FastDiv div_splits, div_band_units, div_band_h, div_band_h_last;
 };
 
-// Whether rows of a straight operand start beside 128-byte lines, so that a slice of a row lies in two of them.
-inline bool off_the_lines(const ProductArgs& a, Product kind) {
-    const auto off = [](const void* p, int32_t ld) { return ((reinterpret_cast<uintptr_t>(p) | 2 * (uintptr_t)ld) & 127) != 0; };
+// Whether rows of a straight operand start beside 128-byte lines, so that a slice of a row lies in two of them: where it
+// stands in memory (that is how it is loaded), or anywhere, for its rows' length alone (that is what tiles and K splits
+// are chosen by, and with them the order of the sums).
+inline bool off_the_lines(const ProductArgs& a, Product kind, bool anywhere) {
+    const auto off = [=](const void* p, int32_t ld) { return (((anywhere ? 0 : reinterpret_cast<uintptr_t>(p)) | 2 * (uintptr_t)ld) & 127) != 0; };
     return (kind != kTurned && off(a.P, a.ldp)) || ((kind == kGated || kind == kGatedBack) && off(a.Q, a.ldq));
 }
 

@@ -33,7 +33,7 @@
  *   - Results are deterministic: the same inputs give the same bits, whatever the launch
  *     configuration's timing (split-K and stream-K partials are summed in a fixed K order).
  *     The launch configuration itself depends on the shape, the device's CU count and the CU
- *     cap (for the gated block and its gradients, on whether rows start at 128-byte lines), so a different cap (or stream-K turned off) may sum the same products in another
+ *     cap, so a different cap (or stream-K turned off) may sum the same products in another
  *     order, within the same tolerance.
  *   - Stream workspace: each stream (hipStreamPerThread: each host thread's, held until the
  *     process ends) has its own library-owned workspace (fp32 partial tiles
