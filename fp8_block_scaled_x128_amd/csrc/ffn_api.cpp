@@ -356,9 +356,13 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     st = share_workspace({{&ap, cp}}, s, &hold);
     if (st == FP8GEMM_OK) st = share_workspace({{&ax, cx}, {&aw, cw}}, s, &hold);
     if (st != FP8GEMM_OK) return st;
-    host_set_config("gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lld split=%lld dW tile=%lldx%lld split=%lld",
-                    {M, I, K, pair, dX ? kTiles[cx.shape].bm : 0, kTiles[cx.shape].ring, cx.splits,
-                     dW ? kTiles[cw.shape].bm : 0, kTiles[cw.shape].ring, cw.splits});
+    // (zeros for a product that is not formed)
+    const TileShape none{}, &tp = ap.splits ? kTiles[cp.shape] : none, &tx = dX ? kTiles[cx.shape] : none, &tw = dW ? kTiles[cw.shape] : none;
+    const char* words = pre    ? "gated_ffn_backward M=%lld I=%lld K=%lld kept together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld"
+                        : rows ? "gated_ffn_backward M=%lld I=%lld K=%lld rows together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld"
+                               : "gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld "
+                                 "products tile=%lldx%lldx%lld split=%lld";
+    host_set_config(words, {M, I, K, pair, tx.bm, tx.bn, tx.ring, ax.splits, tw.bm, tw.bn, tw.ring, aw.splits, tp.bm, tp.bn, tp.ring, ap.splits});
     if (pre) {
         GatedGradArgs g{};
         g.pre = static_cast<const uint16_t*>(pre);
