@@ -468,7 +468,7 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     // rows of a pass: the splits' sums of A x and its halves fit the workspace, the tiles the grid's second
     // dimension and the counters
     const int64_t row_bytes = (int64_t)a.rank * 4 * (a.splits + 1);
-    const int64_t room = (int64_t)d.cus * 512 * 1024 / row_bytes / 64 * 64;
+    const int64_t room = (int64_t)d.all_cus * 512 * 1024 / row_bytes / 64 * 64;
     const int64_t pass = std::min(T, std::min<int64_t>(room, (int64_t)(a.tile == 64 ? 2048 : 4096) * a.tile));
     std::unique_lock<std::mutex> hold;
     st = host_stream_workspace(s, (size_t)(pass * row_bytes), a.tile == 64 ? (size_t)((pass + 63) / 64) * 2 : 0, &a.low, &a.counters, &hold);

@@ -124,6 +124,12 @@ int device_state(DeviceState** out) {
     return FP8GEMM_OK;
 }
 
+// CUs that launch shapes are sized for (fp8gemm_set_num_cus).
+int capped_cus(const DeviceState* d) {
+    const int cap = g_cu_cap.load();
+    return cap > 0 && cap < d->cus ? cap : d->cus;
+}
+
 // Capacity of a stream's split-K workspace.  An automatically chosen split launch has at most one
 // unit per CU (pick_split), and the largest tile compiled with the split-K exchange is 128 x 256
 // fp32 (128 KiB); a stream-K launch of 256 x 256 tiles (one workgroup per CU) keeps two partial
@@ -354,8 +360,7 @@ int launch(int layout, KernelArgs& a, int64_t expected_rows, hipStream_t stream,
     DeviceState* d = nullptr;
     int st = device_state(&d);
     if (st != FP8GEMM_OK) return st;
-    int cap = g_cu_cap.load();
-    int cus = (cap > 0 && cap < d->cus) ? cap : d->cus;
+    const int cus = capped_cus(d);
     Choice c = choose(layout, a.rows, a.N, a.nkb, expected_rows, a.G, cus, fp4);
     if (c.entry < 0) return FP8GEMM_ERR_UNSUPPORTED;
     const KernelEntry& e = kernels()[c.entry];
@@ -582,7 +587,8 @@ int host_device(HostDevice* out) {
     DeviceState* d = nullptr;
     const int st = device_state(&d);
     if (st != FP8GEMM_OK) return st;
-    out->cus = d->cus;
+    out->cus = capped_cus(d);
+    out->all_cus = d->cus;
     out->err = d->err;
     return FP8GEMM_OK;
 }
@@ -722,8 +728,7 @@ int fp8gemm_specialize_nt(int64_t M, int64_t N, int64_t K, double* compile_ms) {
     DeviceState* d = nullptr;
     st = device_state(&d);
     if (st != FP8GEMM_OK) return st;
-    int cap = g_cu_cap.load();
-    int cus = (cap > 0 && cap < d->cus) ? cap : d->cus;
+    const int cus = capped_cus(d);
     Choice c = choose(kDense, M, N, (int)(K / 128), M, 1, cus, false);
     if (c.entry < 0) return FP8GEMM_ERR_UNSUPPORTED;
     const int before = jit_cache_size();

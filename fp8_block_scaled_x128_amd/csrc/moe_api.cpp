@@ -348,8 +348,8 @@ int fp8gemm_w4_gemv(const void* X, const void* W, const void* scales, const uint
     if (st != FP8GEMM_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     a.cols = (int32_t)std::min<int64_t>(M, 16);
-    const int rn = w4_row_tiles(N, K, a.cols, (M + 15) / 16, true, d.cus);
-    a.tiles_per_wave = w4_tiles_per_wave(N, K, a.cols, (M + 15) / 16, d.cus);
+    const int rn = w4_row_tiles(N, K, a.cols, (M + 15) / 16, true, d.all_cus);
+    a.tiles_per_wave = w4_tiles_per_wave(N, K, a.cols, (M + 15) / 16, d.all_cus);
     host_set_config(format == FP8GEMM_W4_MXFP4 ? "w4_gemv mxfp4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld"
                                                : "w4_gemv int4 group=%lld M=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld",
                     {group, M, N, K, rn, a.tiles_per_wave});
@@ -395,8 +395,8 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
     if (st != FP8GEMM_OK) return st;
     const int64_t busy = std::min<int64_t>(a.pairs, E);
     a.cols = w4_expert_rows(T, a.pairs, E, K);
-    a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.cus);
-    const int rn = swiglu ? 2 : w4_row_tiles(a.nout, K, a.cols, busy, false, d.cus);
+    a.tiles_per_wave = w4_tiles_per_wave(a.nout, K, a.cols, busy, d.all_cus);
+    const int rn = swiglu ? 2 : w4_row_tiles(a.nout, K, a.cols, busy, false, d.all_cus);
     host_set_config(format == FP8GEMM_W4_MXFP4
                         ? "w4_gemv_experts mxfp4 group=%lld pairs=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld by_pair=%lld"
                         : "w4_gemv_experts int4 group=%lld pairs=%lld N=%lld K=%lld rn=%lld tiles_per_wave=%lld by_pair=%lld",

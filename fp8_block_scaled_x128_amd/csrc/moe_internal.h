@@ -15,7 +15,8 @@ namespace fp8gemm {
 
 // ---- services of fp8gemm_api.cpp ----
 struct HostDevice {
-    int cus = 0;
+    int cus = 0;                // that launch shapes are sized for: the device's, or the cap (fp8gemm_set_num_cus)
+    int all_cus = 0;            // the device's, which workspaces are sized for
     int32_t* err = nullptr;     // device error word
 };
 int host_device(HostDevice* out);                                       // status code

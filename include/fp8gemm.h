@@ -444,7 +444,7 @@ int fp8gemm_specialized_count(void);
 
 /* Cap the number of compute units the launch shapes are sized for and the persistent grids
  * occupy (the "set max SM count" utility of page "DeepSeek開源第三彈…", section 如何使用？).
- * n == 0 restores all CUs; n < 0 is FP8GEMM_ERR_BAD_SHAPE. */
+ * The 4-bit products go by all CUs.  n == 0 restores all CUs; n < 0 is FP8GEMM_ERR_BAD_SHAPE. */
 int fp8gemm_set_num_cus(int n);
 
 /* The launch configuration chosen by the last GEMM call on the calling host thread, as text

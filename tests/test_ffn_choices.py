@@ -24,6 +24,10 @@ class Choices(Recorded):
         assert self.lib.fp8gemm_gated_ffn(FAKE + at, FAKE, FAKE, pre, M, I, K, 0, 0x10) == 0
         return self.config()
 
+    def lora(self, T, R, K, N, L=64):
+        assert self.lib.fp8gemm_lora_add(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, T, L, R, K, N, K, N, N, 0x10) == 0
+        return self.config()
+
     def backward(self, M, I, K, at=0, pre=None, dX=FAKE, dW=FAKE):
         assert self.lib.fp8gemm_gated_ffn_backward(FAKE, FAKE + at, FAKE, pre, FAKE + at, dX, dW, M, I, K, 0, 0x10) == 0
         return self.config()
@@ -83,6 +87,45 @@ def _words(so):
 
 def test_words_name_the_tiles_that_are_launched(tmp_path):
     in_a_process(tmp_path, "_words", __file__)
+
+
+PER_CU = {"256x256": 1, "128x256": 1, "128x128": 1, "64x64": 2}                    # workgroups of a tile that share a CU
+
+
+def _cap(so):
+    r = Choices(so)
+    rng = random.Random(2)
+    sizes = [(64, 2048, 7168), (300, 512, 7168)] + [tuple(int(2 ** rng.uniform(*e)) * m for e, m in (((5, 11), 1), ((3, 8), 8), ((3, 10), 8)))
+                                                    for _ in range(100)]
+    adapters = [(16, 16, 7168, 4096), (256, 16, 7168, 4096), (2000, 128, 7168, 4096), (8192, 32, 7168, 4096)]
+    free = [r.gated(*s) for s in sizes] + [r.backward(*s) for s in sizes] + [r.lora(*s) for s in adapters]
+    fewer = 0
+    for cap in (1, 7, 24, 100):
+        assert r.lib.fp8gemm_set_num_cus(cap) == 0
+        for i, s in enumerate(sizes):
+            n = len(r.launches())
+            words = r.gated(*s)
+            tile, split = re.search(r"tile=(\S+) split=(\d+)", words).groups()
+            assert split == "1" or r.launches(n)[0][2] <= cap * PER_CU[tile], (cap, words)
+            fewer += words != free[i]
+            r.backward(*s)
+        for T, R, K, N in adapters:
+            n = len(r.launches())
+            words = r.lora(T, R, K, N)
+            rows, split = (int(x) for x in re.search(r"rows=(\d+) split=(\d+)", words).groups())
+            tiles = -(-T // rows)
+            assert split == 1 or tiles * split <= 2 * cap, (cap, words)
+            assert [x[2] for x in r.launches(n)][0] == tiles * split * (-(-R // 32) if rows < 64 else 2)
+        n = len(r.launches())
+        r.lora(140000, 128, 64, 64, L=3)                       # the workspace, and with it the passes, stay as they are
+        assert len(r.launches()) - n == 4
+    assert fewer > 50
+    assert r.lib.fp8gemm_set_num_cus(0) == 0
+    assert free == [r.gated(*s) for s in sizes] + [r.backward(*s) for s in sizes] + [r.lora(*s) for s in adapters]
+
+
+def test_launch_shapes_go_by_the_cap(tmp_path):
+    in_a_process(tmp_path, "_cap", __file__)
 
 
 if __name__ == "__main__":
