@@ -277,8 +277,8 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
     std::unique_lock<std::mutex> hold;
     st = share_workspace({{&a, c}}, s, &hold);
     if (st != FP8GEMM_OK) return st;
-    host_set_config("gated_ffn M=%lld I=%lld K=%lld tile=%lldx%lld split=%lld",
-                    {M, I, K, kTiles[c.shape].bm, kTiles[c.shape].bn, c.splits});
+    host_set_config("gated_ffn M=%lld I=%lld K=%lld tile=%lldx%lld split=%lld lines=%lld",
+                    {M, I, K, kTiles[c.shape].bm, kTiles[c.shape].bn, c.splits, a.lag});
     launch_product(a, kGated, c.shape, s);
     return launched();
 }
@@ -358,11 +358,12 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
     if (st != FP8GEMM_OK) return st;
     // (zeros for a product that is not formed)
     const TileShape none{}, &tp = ap.splits ? kTiles[cp.shape] : none, &tx = dX ? kTiles[cx.shape] : none, &tw = dW ? kTiles[cw.shape] : none;
-    const char* words = pre    ? "gated_ffn_backward M=%lld I=%lld K=%lld kept together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld"
-                        : rows ? "gated_ffn_backward M=%lld I=%lld K=%lld rows together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld"
-                               : "gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lldx%lld split=%lld dW tile=%lldx%lldx%lld split=%lld "
-                                 "products tile=%lldx%lldx%lld split=%lld";
-    host_set_config(words, {M, I, K, pair, tx.bm, tx.bn, tx.ring, ax.splits, tw.bm, tw.bn, tw.ring, aw.splits, tp.bm, tp.bn, tp.ring, ap.splits});
+    const char* words = pre    ? "gated_ffn_backward M=%lld I=%lld K=%lld kept together=%lld dX tile=%lldx%lldx%lld split=%lld lines=%lld dW tile=%lldx%lldx%lld split=%lld"
+                        : rows ? "gated_ffn_backward M=%lld I=%lld K=%lld rows together=%lld dX tile=%lldx%lldx%lld split=%lld lines=%lld dW tile=%lldx%lldx%lld split=%lld"
+                               : "gated_ffn_backward M=%lld I=%lld K=%lld together=%lld dX tile=%lldx%lldx%lld split=%lld lines=%lld dW tile=%lldx%lldx%lld split=%lld "
+                                 "products tile=%lldx%lldx%lld split=%lld lines=%lld";
+    host_set_config(words, {M, I, K, pair, tx.bm, tx.bn, tx.ring, ax.splits, ax.lag, tw.bm, tw.bn, tw.ring, aw.splits, tp.bm, tp.bn, tp.ring,
+                            ap.splits, ap.lag});
     if (pre) {
         GatedGradArgs g{};
         g.pre = static_cast<const uint16_t*>(pre);

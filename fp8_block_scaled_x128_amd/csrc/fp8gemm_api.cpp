@@ -77,7 +77,7 @@ std::atomic<int> g_cu_cap{0};
 thread_local char g_last_config[256] = "";
 
 // The last configuration of an operator whose calls are short: put into words when asked for.
-constexpr int kConfigValues = 16;
+constexpr int kConfigValues = 18;
 struct PendingConfig {
     const char* fmt = nullptr;             // %lld for each value
     long long v[kConfigValues] = {};
@@ -88,7 +88,7 @@ const char* last_config() {
     if (g_pending.fmt) {
         const long long* v = g_pending.v;
         std::snprintf(g_last_config, sizeof g_last_config, g_pending.fmt, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9],
-                      v[10], v[11], v[12], v[13], v[14], v[15]);
+                      v[10], v[11], v[12], v[13], v[14], v[15], v[16], v[17]);
         g_pending.fmt = nullptr;
     }
     return g_last_config;

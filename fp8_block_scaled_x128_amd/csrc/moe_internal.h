@@ -26,7 +26,7 @@ int host_stream_scratch(hipStream_t stream, size_t bytes, void** scratch, std::u
 // The same with `count` arrival counters, which are zero and are left at zero.
 int host_stream_workspace(hipStream_t stream, size_t bytes, size_t count, float** partials, int32_t** counters,
                           std::unique_lock<std::mutex>* hold);
-// The calling thread's last configuration: a static format of %lld fields and at most 16 values.
+// The calling thread's last configuration: a static format of %lld fields and at most 18 values.
 void host_set_config(const char* fmt, std::initializer_list<long long> values);
 
 // ---- routing ----

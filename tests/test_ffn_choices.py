@@ -73,12 +73,13 @@ def _words(so):
                 n = len(r.launches())
                 words = r.backward(M, I, K, pre=FAKE, dX=dX, dW=dW)
                 there, none = "%s split=%d" % (tile, split), "tile=0x0x0 split=0"
+                lines = " lines=%d" % (dX is not None and ring == 4)                  # (rows of dpre start beside the lines)
                 assert " kept together=%d " % (dX is not None and dW is not None) in words, words
-                assert "dX %s " % (there if dX else none) in words and words.endswith("dW " + (there if dW else none)), words
+                assert "dX %s%s " % (there if dX else none, lines) in words and words.endswith("dW " + (there if dW else none)), words
                 assert sum(x[2] for x in r.launches(n)[1:]) == (units(M, K) if dX else 0) + (units(2 * I, K) if dW else 0)
             n = len(r.launches())
             words = r.backward(M, I, K)
-            assert words.endswith("dW %s split=%d products %s split=%d" % (tile, split, tile, split)) or name == "64x64x2", words
+            assert words.endswith("dW %s split=%d products %s split=%d lines=0" % (tile, split, tile, split)) or name == "64x64x2", words
             got = r.launches(n)
             assert got[0][2] == -(-M // bm) * -(-2 * I // bn) * split or name == "64x64x2"     # (a shape of the gradients)
     del os.environ["FP8GEMM_FORCE_CONFIG"]

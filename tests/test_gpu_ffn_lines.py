@@ -9,7 +9,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU runs deselect these 
 
 import fp8_block_scaled_x128_amd as fg  # noqa: E402
 from test_gpu_ffn import bits, off_by  # noqa: E402
-from test_gpu_gated import normal  # noqa: E402
+from test_gpu_gated import backward_close, forward_close, normal  # noqa: E402
 
 bf16 = torch.bfloat16
 
@@ -28,3 +28,23 @@ def test_the_same_bits_anywhere(M, I, K):
         results.append([bits(t) for t in out])
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("chunks", [0, 1, 4, 7])
+@pytest.mark.parametrize("K", [2056, 2080, 2104, 2112])
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("tile,M,I", [("128x128", 1500, 456), ("64x64", 700, 520)])
+def test_by_lines(tile, M, I, split, K, chunks, monkeypatch):
+    """Loads by whole lines, as the configuration says, with every kind of K's end: 1, 4 and 7 chunks of 16 bytes, and a
+    whole slice."""
+    monkeypatch.setenv("FP8GEMM_FORCE_CONFIG", "product:%s:%d" % (tile, split))
+    X, W, dH = off_by(normal(1, M, K), chunks), off_by(normal(2, 2 * I, K, scale=K ** -0.5), 7 * chunks % 8), normal(3, M, I)
+    pre, dpre = torch.zeros((M, 2 * I), dtype=bf16, device="cuda"), off_by(torch.zeros((M, 2 * I), dtype=bf16, device="cuda"), chunks)
+    H = fg.gated_ffn(X, W, pre=pre)
+    lines = chunks > 0 or K % 64 > 0
+    assert fg.last_config().endswith("tile=%s split=%d lines=%d" % (tile, split, lines))
+    forward_close(X, W, "silu", H, pre)
+    dX, dW = fg.gated_ffn_backward(dH, X, W, dpre=dpre)
+    words = fg.last_config()
+    assert "dX tile=%sx4 split=%d lines=1 " % (tile, split) in words and words.endswith("products tile=%sx4 split=%d lines=%d" % (tile, split, lines))
+    backward_close(dH, X, W, "silu", None, dpre, dX, dW)
