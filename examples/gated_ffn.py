@@ -32,9 +32,20 @@ class GatedFfn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dh):
         x, w, pre = ctx.saved_tensors
-        dx, dw = fg.gated_ffn_backward(dh.contiguous(), x, w, pre=pre, act=ctx.act, need_dX=ctx.needs_input_grad[0],
-                                       need_dW=ctx.needs_input_grad[1])
+        dx, dw = GatedFfnGradients.apply(dh.contiguous(), x, w, pre, ctx.act, *ctx.needs_input_grad[:2])
         return dx, dw, None, None
+
+
+class GatedFfnGradients(torch.autograd.Function):
+    """GatedFfn's gradients, which have none of their own: differentiating them is refused, whatever requires it."""
+
+    @staticmethod
+    def forward(ctx, dh, x, w, pre, act, need_dx, need_dw):
+        return fg.gated_ffn_backward(dh, x, w, pre=pre, act=act, need_dX=need_dx, need_dW=need_dw)
+
+    @staticmethod
+    def backward(ctx, *unused):
+        raise RuntimeError("GatedFfn has no second derivative")
 
 
 class Block:
