@@ -405,6 +405,7 @@ int fp8gemm_lora_add(const void* Y, const void* X, const void* A, const void* B,
     if ((int64_t)L * R > kMaxBytes / 2 / std::max<int64_t>(std::max(K, N), 1)) return FP8GEMM_ERR_UNSUPPORTED;
     if (T == 0 || N == 0) return FP8GEMM_OK;
     if (!Y || !X || !A || !B || !ids || !out) return FP8GEMM_ERR_NULL_PTR;
+    if (T > 1 && Y == out && ldy != ldo) return FP8GEMM_ERR_BAD_SHAPE;
     if (!aligned(Y, 16) || !aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16) || !aligned(ids, 4) ||
         !aligned(order, 4) || !aligned(scales, 4))
         return FP8GEMM_ERR_MISALIGNED;

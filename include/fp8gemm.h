@@ -375,7 +375,8 @@ int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, con
  *   of 8); A [L][R][K], B [L][N][R] bf16; ids [T] int32; scales [L] fp32 or NULL (ones).
  * Sums in fp32; A x enters the second product with 16 bits, and infinities and NaN give what the formula
  * gives, whatever the number of rows.  An adapter of smaller rank is padded with zeros.
- * out may be Y itself, with its stride (rows without an adapter are then not written), and overlaps nothing else.  An id of L or more counts as none and flags FP8GEMM_DEVERR_BAD_INDEX.
+ * out may be Y itself, with its stride (else BAD_SHAPE; rows without an adapter are then not written),
+ * and overlaps nothing else.  An id of L or more counts as none and flags FP8GEMM_DEVERR_BAD_INDEX.
  *   order [T] int32 or NULL: a permutation of the rows that brings those of an adapter together.  It
  *   changes no result, only the time of a batch in which neighbours have different adapters: rows are
  *   taken one at a time in small batches, else up to 64 together, each adapter among them in turn.  An

@@ -73,6 +73,15 @@ def test_lora_refusals(lib):
         assert call(**bad) == ALIGN, bad
 
 
+def test_lora_in_place_has_one_stride(lib):
+    """Rows of the result over rows of Y at another stride would be read after they are written."""
+    def call(Y, out, ldy, ldo, T=4, scales=FAKE + 2):          # (the scales' alignment is refused after the strides)
+        return lib.fp8gemm_lora_add(Y, FAKE, FAKE, FAKE, FAKE, None, scales, out, T, 3, 16, 128, 64, 128, ldy, ldo, None)
+    assert call(FAKE, FAKE, 64, 72) == SHAPE and call(FAKE, FAKE, 80, 64) == SHAPE
+    assert call(FAKE, FAKE, 72, 72) == ALIGN and call(FAKE, FAKE + (1 << 20), 64, 72) == ALIGN
+    assert call(FAKE, FAKE, 64, 72, T=1) == ALIGN              # one row has no stride
+
+
 def test_binding_rejects_bad_tensors():
     import torch
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(32, 64, dtype=torch.bfloat16)
