@@ -27,7 +27,8 @@ C ABI declared in include/fp8gemm.h.  torch supplies device memory and the curre
 A and B are E4M3 codes (torch.float8_e4m3fn or uint8), sa one fp32 scale per 1x128 block of a
 row of A stored K-block-major (sa[kb, m], shape [K/128, M]), sb one per 128x128 block of B (page "DeepSeek開源第三彈：V3/R1訓練推理關鍵秘籍，核心代碼僅
 300行", sections 深入了解DeepGEMM and 如何使用？).  There is no CPU fallback: without the built
-library every call raises.
+library every call raises.  Results carry no autograd graph, whatever the arguments require: a program
+that trains wraps a call and its ``_backward`` in an autograd function (examples/gated_ffn.py).
 """
 from __future__ import annotations
 

@@ -218,7 +218,11 @@ int share_workspace(std::initializer_list<std::pair<ProductArgs*, Choice>> produ
 // different adapters stand together, which the host does not know.  Measured, two launches (rows in any order, by adapter)
 // and this, us, by R (K + N): 8 rows 32768 6.8 and 5.3, 65536 7.4 and 5.9, 81920 6.8 and 7.5; 40 rows 104448 10.6, 10.5 and
 // 9.3, 144000 15.5, 12.0 and 12.4; 100 rows 104448 19.3, 12.9 and 9.4, 166400 17, 10.6 and 10.8; 200 rows 110336 16, 9.8 and
-// 9.7; 400 rows 51968 17.6, 10.2 and 9.0, 104448 29, 11.0 and 16; 1000 rows 8192 12.7 and 10.6.
+// 9.7; 400 rows 51968 17.6, 10.2 and 9.0, 104448 29, 11.0 and 16; 1000 rows 8192 12.7 and 10.6.  By R, 1 row (8 rows
+// are like it; of 20 and 31 rows the two launches take up to 13 and 18 with R above 64): 72000 R = 16 6.6 and 6.7, R = 64 7.7 and 6.5;
+// 85000 6.7 and 7.8, 7.7 and 6.8; 99000 R = 72 8.6 and 9.0, R = 96 8.8 and 8.7, R = 128 9.6 and 8.2; 129000 9.1 and
+// 12.6, 8.8 and 9.3, 9.2 and 7.5.  A wave takes K's steps of 4096 values one after the other: R = 8, N = 1024, 1 row,
+// K = 4096 6.6 and 5.9, 5120 6.5 and 7.4; 45 rows 8.0 and 6.1, 8.1 and 7.7.
 bool by_row(int64_t T, int64_t R, int64_t K, int64_t N) {
     const int64_t most = T < 32 ? (R > 64 ? 100000 : 72000) : T < 64 ? 110000 : T <= 256 ? 150000 : T <= 512 ? 72000 : T <= 1024 ? 16384 : 0;
     return K <= 4096 && R * (K + N) <= most;

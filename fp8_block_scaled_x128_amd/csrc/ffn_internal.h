@@ -18,7 +18,6 @@ enum Product {
     kTimesW = 2,       // P = dpre [M,2I], Q = W [2I,K] turned: dX
     kTurned = 3,       // P = dpre [M,2I] turned, Q = X [M,K] turned: dW
 };
-constexpr int kProducts = 4;
 
 struct ProductArgs {
     const uint16_t* P;
@@ -98,7 +97,7 @@ void launch_gated_grad(const GatedGradArgs& a, hipStream_t s);
 
 // ---- low-rank adapters ----
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraSpan = 256;      // columns of the result that a workgroup takes at a time
+constexpr int kLoraSpan = 256;      // columns of the result that a workgroup of at most 16 places takes at a time
 
 struct LoraArgs {
     const uint16_t* X;          // [T][ldx]
@@ -123,7 +122,7 @@ struct LoraArgs {
     int32_t steps;              // ceil(K / 64)
     int32_t splits, per_split;  // steps of a split
     int32_t apart;              // tiles of 64 places: 0, or 1: two workgroups have their adapters in turn
-    int32_t chunks;             // runs of kLoraSpan columns that a workgroup takes
+    int32_t chunks;             // runs of columns that a workgroup takes: of kLoraSpan, or of 64 with tiles of 64 places
 };
 
 void launch_lora_rows(const LoraArgs& a, hipStream_t s);      // both products, a workgroup a row

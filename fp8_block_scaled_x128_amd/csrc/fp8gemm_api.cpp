@@ -130,11 +130,13 @@ int capped_cus(const DeviceState* d) {
     return cap > 0 && cap < d->cus ? cap : d->cus;
 }
 
-// Capacity of a stream's split-K workspace.  An automatically chosen split launch has at most one
-// unit per CU (pick_split), and the largest tile compiled with the split-K exchange is 128 x 256
+// Capacity of a stream's split-K workspace.  An automatically chosen split launch of a GEMM has at most
+// one unit per CU (pick_split), and the largest tile compiled with the split-K exchange is 128 x 256
 // fp32 (128 KiB); a stream-K launch of 256 x 256 tiles (one workgroup per CU) keeps two partial
-// tiles per workgroup (512 KiB).  So cus * 512 KiB of partials and one counter per unit cover
-// every such launch.  A forced configuration (FP8GEMM_FORCE_CONFIG) beyond it is refused.
+// tiles per workgroup (512 KiB).  A product of the gated block has as many split units as share the CUs:
+// one of 256 x 256 (256 KiB), 128 x 256 or 128 x 128, two to four of 64 x 64 (16 KiB each) a CU, and its
+// two gradients as one launch twice as many.  So cus * 512 KiB of partials and one counter per tile (at
+// most four a CU) cover every such launch.  A forced configuration (FP8GEMM_FORCE_CONFIG) beyond it is refused.
 constexpr size_t kMaxPartialBytesPerCu = 2 * 256 * 256 * sizeof(float);
 // Fewest K blocks per workgroup that stream-K must save over whole tiles (see launch()).
 int stream_k_min_blocks(int bn) { return bn >= 256 ? 12 : (bn >= 192 ? 9 : 6); }

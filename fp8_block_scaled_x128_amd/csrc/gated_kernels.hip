@@ -10,11 +10,11 @@
 // rounding) without, and two halves of each value would double the operations of both products.  g and u, formed again,
 // and all sums stay in fp32.
 //
-// What bounds them: large sizes the matrix cores and what feeds them.  H of 4096 rows, I = 2048, K = 7168 takes 178 us,
-// 1.35 PFLOP/s (a library product with as many operations 183 us, the matrix instructions alone on the same data, from
-// registers, 143 us); its gradients 411 us, 1.17 PFLOP/s (a library's two products 489 us).  Middle sizes: how the tiles fill 256
-// CUs, and a tile's start and end (3 to 8 us); few rows: W's bytes, 1 row 10.6 us, 5.5 TB/s of them from HBM and the
-// memory-side cache.
+// What bounds them: large sizes the matrix cores and what feeds them.  H of 4096 rows, I = 2048, K = 7168 takes 180 us,
+// 1.34 PFLOP/s (a library's plain product of the same matrices, in turn with it, 158 us; the matrix instructions alone, on
+// the same data from registers, 143 us); its gradients 410 us, 1.17 PFLOP/s (a library's two products 425 us).  Middle
+// sizes: how the tiles fill 256 CUs, and a tile's start and end (3 to 8 us); few rows: W's bytes, 1 row 10.7 us, 5.5 TB/s of
+// them from HBM and the memory-side cache.
 
 #include <algorithm>
 #include <type_traits>

@@ -349,8 +349,9 @@ int fp8gemm_w4_gemv_experts(const void* X, const void* W, const void* scales, co
  *     FP8GEMM_ACT_GELU_TANH z = 2 sqrt(2 / pi) (x + 0.044715 x^3)
  *   pre [M][2I] = bf16([g | u]) for the gradients, or NULL.
  * X, W, H, pre bf16, dense, 16-byte aligned.  I and K: positive multiples of 8, K <= 2^20,
- * I <= 2^19 (else UNSUPPORTED); M == 0 is a no-op.  H and pre overlap no input.  Some sizes split K
- * over workgroups and use the stream's workspace (see fp8gemm_prepare_stream). */
+ * I <= 2^19; X, H and pre below 2^40 bytes, and 2^22 tiles at most (else UNSUPPORTED); M == 0 is a
+ * no-op.  H and pre overlap no input.  Some sizes split K over workgroups and use the stream's workspace
+ * (see fp8gemm_prepare_stream). */
 #define FP8GEMM_ACT_SILU 0
 #define FP8GEMM_ACT_GELU_TANH 1
 int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t M, int64_t I, int64_t K, int32_t act,
@@ -364,9 +365,9 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
  *   0.003.  A NaN in g gives NaN in dg and du, one in u in dg.
  * With `pre` (as fp8gemm_gated_ffn wrote it) g and u are its bf16 values; with pre NULL they are
  * formed again from X and W and not rounded.  dpre is written (a workspace, and the gradient with
- * respect to the two projections); it may be `pre` itself, and no output overlaps anything else.  dX or dW NULL: not formed; X may be
- * NULL with `pre` and without dW, W with `pre` and without dX.  M == 0 sets dW to zeros.  Sizes,
- * alignment and workspace as above. */
+ * respect to the two projections); it may be `pre` itself, and no output overlaps anything else.
+ * dX or dW NULL: not formed; X may be NULL with `pre` and without dW, W with `pre` and without dX.
+ * M == 0 sets dW to zeros.  Sizes, alignment and workspace as above. */
 int fp8gemm_gated_ffn_backward(const void* dH, const void* X, const void* W, const void* pre, void* dpre, void* dX, void* dW,
                                int64_t M, int64_t I, int64_t K, int32_t act, void* stream);
 
