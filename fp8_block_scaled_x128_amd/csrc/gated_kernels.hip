@@ -36,7 +36,7 @@ __device__ __forceinline__ v4f mfma_bf16(const v4u& x, const v4u& y, const v4f& 
 
 // Both activations are x times a logistic function of z(x): z = x (silu), or z = 2 sqrt(2/pi) (x + 0.044715 x^3)
 // (gelu's tanh form, since 0.5 (1 + tanh(z / 2)) = 1 / (1 + e^-z)).  1 / (1 + e^-z) within 3 units in the last
-// place: the exponential's error and the reciprocal's.
+// place: the exponential's error and the reciprocal's; below 2^-126 (z below -87) the reciprocal gives zero.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;
 
 __device__ __forceinline__ float logistic(float x, bool gelu) {

@@ -362,7 +362,7 @@ int fp8gemm_gated_ffn(const void* X, const void* W, void* H, void* pre, int64_t 
  *   dX [M][K] = bf16(dpre W),  dW [2I][K] = bf16(dpre^T X), sums in fp32 of the rounded dpre.  Each
  *   term carries that rounding, 2^-8 of it at most; over many terms of either sign a gradient's
  *   norm is off by 0.0024 of it, where a single rounding gives 0.0017, and over few terms by up to
- *   0.003.  A NaN in g gives NaN in dg and du, one in u in dg.
+ *   0.003.  A NaN in g gives NaN in dg and du, one in u in dg; act' of an infinite g is its limit, 0 or 1.
  * With `pre` (as fp8gemm_gated_ffn wrote it) g and u are its bf16 values; with pre NULL they are
  * formed again from X and W and not rounded.  dpre is written (a workspace, and the gradient with
  * respect to the two projections); it may be `pre` itself, and no output overlaps anything else.

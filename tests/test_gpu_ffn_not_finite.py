@@ -70,6 +70,17 @@ def test_nan_gate_reaches_its_gradient(tile, M, I, K, act, monkeypatch):
     the_same_but(dw, dW, rows)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_infinite_gate(act):
+    """act' of an infinite gate is its limit: dg = dH u above, zero below; du = dH act(g) is infinite above."""
+    M, I, K = 5, 40, 72
+    X, W, dH, pre = normal(1, M, K), normal(2, 2 * I, K, scale=K ** -0.5), normal(3, M, I), normal(4, M, 2 * I)
+    pre[2, 11], pre[3, 11] = float("inf"), -float("inf")
+    dpre = gradients(dH, X, W, act, pre)[0]
+    assert dpre[2, 11] == (dH[2, 11].float() * pre[2, I + 11].float()).to(bf16) and dpre[3, 11] == 0
+    assert dpre[2, I + 11] == float("inf") * dH[2, 11].sign()
+
+
 # by row, a few rows a workgroup, 64 rows; ranks of every kernel
 @pytest.mark.parametrize("T,L,R,K,N", [(20, 4, 24, 264, 136), (40, 4, 16, 2568, 136), (40, 4, 16, 4168, 136), (70, 4, 104, 1200, 136),
                                        (40, 4, 32, 4168, 136), (40, 4, 56, 4168, 136), (1100, 4, 16, 200, 264), (1100, 4, 32, 200, 136),
